@@ -290,6 +290,108 @@ moe_status moe_layer_noalloc(const moe_shape *shape, const void *x, int32_t T, c
                              const float *logit_bias, const moe_expert *d_table, const void *residual,
                              void *y, int32_t *topk_idx_out, float *topk_w_out, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Operators around the experts.  They take the same shape, types and grouping; every pointer is
+ * device memory, 16-byte aligned where it holds rows of d_model values.  `pick_pos` is
+ * moe_permute's: a pick whose position lies outside [0, T*top_k) - a dropped pick's is -1 - has no
+ * row and is left out of every sum.  With n_shared = 1, rows T*top_k + t of the expert-side
+ * arrays belong to the shared expert and token t, as in moe_expert_ffn's o.
+ * --------------------------------------------------------------------------------------- */
+
+/* Tokens laid out by expert, for expert products of the caller's own (training, dense experts):
+ * xs[pick_pos[t,j]] = x[t] for each pick, and xs[T*top_k + t] = x[t] with n_shared = 1.  xs:
+ * [T*top_k + T*n_shared][d_model] act_dtype, row i the input of row i of moe_expert_ffn's o; rows
+ * that no pick has (past expert_offsets[n_experts]) are left as they were.  xs may not alias x.
+ * The way back, with the weights applied, is moe_combine. */
+moe_status moe_dispatch(const moe_shape *shape, const void *x, int32_t T, const int32_t *pick_pos,
+                        void *xs, hipStream_t stream);
+
+/* Gradient of moe_dispatch: dx[t] = sum_j dxs[pick_pos[t,j]] (+ dxs[T*top_k + t] with
+ * n_shared = 1), summed over j in order in fp32 and rounded once to act_dtype; a token without
+ * picks gets zeros.  dxs: [T*top_k + T*n_shared][d_model] act_dtype; dx: [T][d_model] act_dtype,
+ * not aliasing dxs. */
+moe_status moe_dispatch_backward(const moe_shape *shape, const void *dxs, int32_t T,
+                                 const int32_t *pick_pos, void *dx, hipStream_t stream);
+
+/* Gradient of moe_combine for an upstream dy ([T][d_model] act_dtype; the residual's gradient is
+ * dy itself):
+ *   d_o[pick_pos[t,j]] = routed_scaling * topk_w[t,j] * dy[t]   (fp32, o's layout),
+ *   d_o[T*top_k + t]   = dy[t]                                   (n_shared = 1),
+ *   d_w[t,j]           = routed_scaling * <dy[t], o[pick_pos[t,j]]>, 0 for a pick without a row.
+ * Rows of d_o that no pick has are left as they were.  d_o: [T*top_k + T*n_shared][d_model] fp32
+ * or NULL; d_w: [T][top_k] fp32 or NULL (not both NULL); o may be NULL when d_w is, topk_w when
+ * d_o is.  d_o may be o itself (each value is read before it is overwritten).  No atomics: the
+ * result is the same from run to run. */
+moe_status moe_combine_backward(const moe_shape *shape, const void *dy, const float *o,
+                                const float *topk_w, const int32_t *pick_pos, int32_t T, float *d_o,
+                                float *d_w, hipStream_t stream);
+
+/* The norms before and after a block, with its gate and residual scale, in one pass.  With
+ *   N(v; g)[i] = g[i] * v[i] / sqrt(mean_i v[i]^2 + eps)                 (RMS norm, fp32 sums),
+ *   z[t] = N(y[t]; post_gamma), or y[t] when post_gamma is NULL,
+ *   u[t] = x[t] + residual_scale * gate[t] * z[t],  or x[t] when y is NULL:
+ *   x_out[t]  = u[t]                    rounded to act_dtype (the residual stream), and
+ *   normed[t] = N(u[t]; pre_gamma)      rounded to act_dtype (the next block's input), taken from
+ *                                       the fp32 u, before x_out's rounding.
+ * gate by gate_kind: MOE_GATE_NONE (gate NULL: 1), MOE_GATE_TOKEN ([T] fp32, one per token) or
+ * MOE_GATE_ELEMENT ([T][d_model] act_dtype).  With y NULL, post_gamma and gate are NULL (a plain
+ * pre-norm).  x_out may be NULL (not written); normed and pre_gamma are both given or both NULL;
+ * one of x_out and normed is given.  x, y, x_out, normed: [T][d_model] act_dtype; the gammas:
+ * [d_model] fp32; eps > 0.  Each value is read before its place is written, so x_out and normed
+ * may each be x, y or an element gate, but not one another.  d_model at most 16384
+ * (MOE_ERR_UNSUPPORTED beyond). */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_ELEMENT = 2 } moe_gate_kind;
+
+moe_status moe_block_norm(const moe_shape *shape, const void *x, const void *y, int32_t T,
+                          const float *post_gamma, const float *pre_gamma, const void *gate,
+                          int32_t gate_kind, float residual_scale, float eps, void *x_out,
+                          void *normed, hipStream_t stream);
+
+/* moe_combine and moe_block_norm in one pass: the same with
+ *   y[t] = routed_scaling * sum_j topk_w[t,j] * o[pick_pos[t,j]] (+ o[T*top_k + t])
+ * summed as in moe_combine (without its residual) and never rounded or written. */
+moe_status moe_combine_norm(const moe_shape *shape, const float *o, const float *topk_w,
+                            const int32_t *pick_pos, const void *x, int32_t T,
+                            const float *post_gamma, const float *pre_gamma, const void *gate,
+                            int32_t gate_kind, float residual_scale, float eps, void *x_out,
+                            void *normed, hipStream_t stream);
+
+/* Gradient of moe_block_norm, from its inputs (u is computed again) and the upstream gradients
+ * d_x_out and d_normed ([T][d_model] act_dtype; either may be NULL, meaning zero):
+ *   dx, dy:                   [T][d_model] act_dtype;
+ *   d_gate:                   [T] fp32 (MOE_GATE_TOKEN) or [T][d_model] act_dtype (MOE_GATE_ELEMENT);
+ *   d_post_gamma, d_pre_gamma: [d_model] fp32, summed over the tokens in a fixed order (no atomics).
+ * Outputs that are not wanted are NULL (one is given); outputs of inputs that are not there must
+ * be NULL.  pre_gamma and d_normed are both given or both NULL.  Each value is read before its
+ * place is written, so the row outputs may each be one of the row inputs, but not one another.
+ * ws: a workspace of moe_workspace_bytes(shape, T) bytes (its status word is left alone).
+ * T = 0 writes zeros to the gammas' gradients that are given, and nothing else. */
+moe_status moe_block_norm_backward(const moe_shape *shape, const void *x, const void *y, int32_t T,
+                                   const float *post_gamma, const float *pre_gamma, const void *gate,
+                                   int32_t gate_kind, float residual_scale, float eps,
+                                   const void *d_x_out, const void *d_normed, void *dx, void *dy,
+                                   void *d_gate, float *d_post_gamma, float *d_pre_gamma, void *ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
+/* Matrix-vector products with a dense weight in the experts' formats (the projections beside the
+ * experts, an output head), for up to 64 vectors:
+ *   y[t,n] = tensor_scale * sum_k W[n,k] x[t,k] (+ bias[n]),
+ * W dequantised on the fly from q ([rows][cols/2] codes) and s ([rows][cols/B] scales), as the
+ * experts' sub-tensors are.  The weights and x enter the products exactly (fp32 x as three bf16
+ * terms), sums are fp32, and y is rounded once.  1 <= rows <= 2^24, cols a multiple of 128,
+ * rows * cols <= 2^34, T <= 64 (MOE_ERR_UNSUPPORTED beyond).  tensor_scale is a host value, used
+ * as given (1 for MXFP4).  x: [T][cols], y: [T][rows] act_dtype; bias: [rows] fp32 or NULL; q, s, x
+ * and y 16-byte aligned; y may not alias x. */
+typedef struct {
+    int32_t rows;
+    int32_t cols;
+    int32_t wformat;      /* moe_wformat */
+    int32_t act_dtype;    /* moe_dtype   */
+} moe_matrix;
+
+moe_status moe_linear(const moe_matrix *matrix, const uint8_t *q, const uint8_t *s, float tensor_scale,
+                      const void *x, int32_t T, const float *bias, void *y, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

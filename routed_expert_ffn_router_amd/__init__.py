@@ -23,6 +23,7 @@ MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = r
 MOE_DT_F32, MOE_DT_BF16 = 0, 1
 MOE_WF_MXFP4, MOE_WF_NVFP4 = 0, 1
 MOE_AQ_EXACT, MOE_AQ_MXFP8 = 0, 1
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2
 MOE_WS_STATUS_OFFSET = 0
 MOE_WS_ROUTE_TIMEOUT, MOE_WS_BAD_EXPERT_ID = 0x1, 0x2
 
@@ -47,6 +48,11 @@ class moe_expert(ctypes.Structure):
                 ("reserved", ctypes.c_float)]
 
 
+class moe_matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("wformat", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32)]
+
+
 EXPERT_BYTES = ctypes.sizeof(moe_expert)
 
 if not os.path.exists(LIB_PATH):
@@ -58,6 +64,7 @@ _P = ctypes.c_void_p
 _SP = ctypes.POINTER(moe_shape)
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 TRACE_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int, ctypes.c_void_p)
 EVENT_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_char_p, ctypes.POINTER(ctypes.c_void_p),
                               ctypes.POINTER(ctypes.c_void_p))
@@ -84,6 +91,14 @@ _SIGS = {
     "moe_layer_observed": (ctypes.c_int, [_SP, _P, _i32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _sz, _P,
                                           ctypes.POINTER(moe_observer)]),
     "moe_layer_noalloc": (ctypes.c_int, [_SP, _P, _i32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_dispatch": (ctypes.c_int, [_SP, _P, _i32, _P, _P, _P]),
+    "moe_dispatch_backward": (ctypes.c_int, [_SP, _P, _i32, _P, _P, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_SP, _P, _P, _P, _P, _i32, _P, _P, _P]),
+    "moe_block_norm": (ctypes.c_int, [_SP, _P, _P, _i32, _P, _P, _P, _i32, _f32, _f32, _P, _P, _P]),
+    "moe_combine_norm": (ctypes.c_int, [_SP, _P, _P, _P, _P, _i32, _P, _P, _P, _i32, _f32, _f32, _P, _P, _P]),
+    "moe_block_norm_backward": (ctypes.c_int, [_SP, _P, _P, _i32, _P, _P, _P, _i32, _f32, _f32, _P, _P, _P, _P, _P, _P,
+                                               _P, _P, _sz, _P]),
+    "moe_linear": (ctypes.c_int, [ctypes.POINTER(moe_matrix), _P, _P, _f32, _P, _i32, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -254,3 +269,122 @@ def moe_layer_noalloc(shape, x, T: int, w_router, logit_bias, d_table, residual,
     _check("moe_layer_noalloc", _lib.moe_layer_noalloc(ctypes.byref(shape), _ptr(x), T, _ptr(w_router),
                                                        _ptr(logit_bias), _ptr(d_table), _ptr(residual), _ptr(y),
                                                        _ptr(topk_idx_out), _ptr(topk_w_out), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------------
+# operators around the experts.  Tensors given to them are checked first (torch knows what a bare
+# pointer does not say): the dtype the call documents, contiguous, at least as many elements as the
+# call touches, and on the current device, whose stream the launch goes to.  Anything else raises
+# MoeError with MOE_ERR_INVALID before the library is called.  Integer device pointers pass as they are.
+# ---------------------------------------------------------------------------------------------
+
+def _check_tensors(fn: str, *args):
+    """args: (tensor, dtype, elements) triples; a tensor may be None or an integer pointer."""
+    import torch
+    device = None
+    for t, dtype, n in args:
+        if t is None or isinstance(t, int):
+            continue
+        if device is None:
+            device = torch.cuda.current_device() if t.is_cuda else None
+        if t.dtype is not dtype or not t.is_cuda or t.get_device() != device or t.numel() < n or not t.is_contiguous():
+            raise MoeError(fn, MOE_ERR_INVALID)
+
+
+def _act(act_dtype: int):
+    import torch
+    return torch.bfloat16 if act_dtype == MOE_DT_BF16 else torch.float32
+
+
+def _expert_rows(shape, T: int) -> int:
+    return T * (shape.top_k + shape.n_shared)
+
+
+def moe_dispatch(shape, x, T: int, pick_pos, xs, stream=None):
+    import torch
+    act, d = _act(shape.act_dtype), shape.d_model
+    _check_tensors("moe_dispatch", (x, act, T * d), (pick_pos, torch.int32, T * shape.top_k),
+                   (xs, act, _expert_rows(shape, T) * d))
+    _check("moe_dispatch", _lib.moe_dispatch(ctypes.byref(shape), _ptr(x), T, _ptr(pick_pos), _ptr(xs),
+                                             _stream(stream)))
+
+
+def moe_dispatch_backward(shape, dxs, T: int, pick_pos, dx, stream=None):
+    import torch
+    act, d = _act(shape.act_dtype), shape.d_model
+    _check_tensors("moe_dispatch_backward", (dxs, act, _expert_rows(shape, T) * d),
+                   (pick_pos, torch.int32, T * shape.top_k), (dx, act, T * d))
+    _check("moe_dispatch_backward", _lib.moe_dispatch_backward(ctypes.byref(shape), _ptr(dxs), T, _ptr(pick_pos),
+                                                               _ptr(dx), _stream(stream)))
+
+
+def moe_combine_backward(shape, dy, o, topk_w, pick_pos, T: int, d_o, d_w, stream=None):
+    import torch
+    f32, d, P, rows = torch.float32, shape.d_model, T * shape.top_k, _expert_rows(shape, T)
+    _check_tensors("moe_combine_backward", (dy, _act(shape.act_dtype), T * d), (o, f32, rows * d), (topk_w, f32, P),
+                   (pick_pos, torch.int32, P), (d_o, f32, rows * d), (d_w, f32, P))
+    _check("moe_combine_backward", _lib.moe_combine_backward(ctypes.byref(shape), _ptr(dy), _ptr(o), _ptr(topk_w),
+                                                             _ptr(pick_pos), T, _ptr(d_o), _ptr(d_w),
+                                                             _stream(stream)))
+
+
+def _gate_check(shape, T: int, gate, gate_kind: int):
+    import torch
+    token = gate_kind == MOE_GATE_TOKEN
+    return gate, torch.float32 if token else _act(shape.act_dtype), T if token else T * shape.d_model
+
+
+def moe_block_norm(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
+                   eps: float, x_out, normed, stream=None):
+    import torch
+    f32, act, d = torch.float32, _act(shape.act_dtype), shape.d_model
+    n = T * d
+    _check_tensors("moe_block_norm", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
+                   _gate_check(shape, T, gate, gate_kind), (x_out, act, n), (normed, act, n))
+    _check("moe_block_norm", _lib.moe_block_norm(ctypes.byref(shape), _ptr(x), _ptr(y), T, _ptr(post_gamma),
+                                                 _ptr(pre_gamma), _ptr(gate), gate_kind, residual_scale, eps,
+                                                 _ptr(x_out), _ptr(normed), _stream(stream)))
+
+
+def moe_combine_norm(shape, o, topk_w, pick_pos, x, T: int, post_gamma, pre_gamma, gate, gate_kind: int,
+                     residual_scale: float, eps: float, x_out, normed, stream=None):
+    import torch
+    f32, act, d, P = torch.float32, _act(shape.act_dtype), shape.d_model, T * shape.top_k
+    n = T * d
+    _check_tensors("moe_combine_norm", (o, f32, _expert_rows(shape, T) * d), (topk_w, f32, P),
+                   (pick_pos, torch.int32, P), (x, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
+                   _gate_check(shape, T, gate, gate_kind), (x_out, act, n), (normed, act, n))
+    _check("moe_combine_norm", _lib.moe_combine_norm(ctypes.byref(shape), _ptr(o), _ptr(topk_w), _ptr(pick_pos),
+                                                     _ptr(x), T, _ptr(post_gamma), _ptr(pre_gamma), _ptr(gate),
+                                                     gate_kind, residual_scale, eps, _ptr(x_out), _ptr(normed),
+                                                     _stream(stream)))
+
+
+def moe_block_norm_backward(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
+                            eps: float, d_x_out, d_normed, dx, dy, d_gate, d_post_gamma, d_pre_gamma, ws,
+                            ws_bytes=None, stream=None):
+    import torch
+    f32, act, d = torch.float32, _act(shape.act_dtype), shape.d_model
+    n = T * d
+    _check_tensors("moe_block_norm_backward", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
+                   _gate_check(shape, T, gate, gate_kind), (d_x_out, act, n), (d_normed, act, n), (dx, act, n),
+                   (dy, act, n), _gate_check(shape, T, d_gate, gate_kind), (d_post_gamma, f32, d), (d_pre_gamma, f32, d))
+    ws_bytes = (0 if ws is None else _nbytes(ws)) if ws_bytes is None else ws_bytes
+    _check("moe_block_norm_backward", _lib.moe_block_norm_backward(
+        ctypes.byref(shape), _ptr(x), _ptr(y), T, _ptr(post_gamma), _ptr(pre_gamma), _ptr(gate), gate_kind,
+        residual_scale, eps, _ptr(d_x_out), _ptr(d_normed), _ptr(dx), _ptr(dy), _ptr(d_gate), _ptr(d_post_gamma),
+        _ptr(d_pre_gamma), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def make_matrix(rows: int, cols: int, wformat: int = MOE_WF_MXFP4, act_dtype: int = MOE_DT_BF16) -> moe_matrix:
+    return moe_matrix(rows, cols, wformat, act_dtype)
+
+
+def moe_linear(matrix, q, s, tensor_scale: float, x, T: int, bias, y, stream=None):
+    import torch
+    act, N, K = _act(matrix.act_dtype), matrix.rows, matrix.cols
+    u8, block = torch.uint8, 32 if matrix.wformat == MOE_WF_MXFP4 else 16
+    _check_tensors("moe_linear", (q, u8, N * K // 2), (s, u8, N * K // block), (x, act, T * K),
+                   (bias, torch.float32, N), (y, act, T * N))
+    _check("moe_linear", _lib.moe_linear(ctypes.byref(matrix), _ptr(q), _ptr(s), tensor_scale, _ptr(x), T, _ptr(bias),
+                                         _ptr(y), _stream(stream)))

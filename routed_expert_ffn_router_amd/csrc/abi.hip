@@ -99,7 +99,9 @@ WsLayout ws_layout(const moe_shape* s, int32_t T, bool slots_for_any_shape) {
         L.stage_n = take(4);
         L.stage_ranges = take(8 * ((E + kStageGroup - 1) / kStageGroup));
     }
-    L.total = o;
+    L.norm = L.sink;         // the norms' gradient partials, after the header and the hand-over slots
+    const size_t norm_end = L.norm + align256(8 * (size_t)norm_grad_groups(T) * d);
+    L.total = o > norm_end ? o : norm_end;
     return L;
 }
 
@@ -283,6 +285,46 @@ static moe_status layer_launches(const moe_shape* s, const void* x, int32_t T, c
                                  const void* residual, void* y, int32_t* topk_idx_out, float* topk_w_out,
                                  uint8_t* w8, const WsLayout& L, hipStream_t stream);
 
+static NormArgs norm_args(const moe_shape* s, const void* x, int32_t T, const float* post, const float* pre,
+                          const void* gate, int32_t gate_kind, float residual_scale, float eps) {
+    NormArgs a;
+    memset(&a, 0, sizeof a);
+    a.T = T;
+    a.d = s->d_model;
+    a.x = x;
+    a.k = s->top_k;
+    a.shared = s->n_shared;
+    a.scaling = s->routed_scaling;
+    a.post = post;
+    a.pre = pre;
+    a.gate = gate;
+    a.gate_kind = gate_kind;
+    a.alpha = residual_scale;
+    a.eps = eps;
+    return a;
+}
+
+// values of the norms' calls, whatever the token count
+static moe_status check_norm(const NormArgs& a) {
+    if (!isfinite(a.eps) || !(a.eps > 0.0f) || !isfinite(a.alpha)) return MOE_ERR_INVALID;
+    if (a.gate_kind < MOE_GATE_NONE || a.gate_kind > MOE_GATE_ELEMENT) return MOE_ERR_INVALID;
+    if (a.T > 0 && (a.gate_kind != MOE_GATE_NONE) != (a.gate != nullptr)) return MOE_ERR_INVALID;
+    if (a.d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// pointers of a forward call; has_y: the block's output is given (as y, or by the combine)
+static moe_status check_norm_rows(const NormArgs& a, bool has_y) {
+    if (!a.x || (!a.x_out && !a.normed) || a.x_out == a.normed) return MOE_ERR_INVALID;
+    if ((a.normed != nullptr) != (a.pre != nullptr)) return MOE_ERR_INVALID;
+    if (!has_y && (a.post || a.gate)) return MOE_ERR_INVALID;
+    const void* rows[] = {a.x, a.y, a.x_out, a.normed, a.post, a.pre,
+                          a.gate_kind == MOE_GATE_ELEMENT ? a.gate : nullptr};
+    for (const void* p : rows)
+        if (p && !aligned(p, 16)) return MOE_ERR_INVALID;
+    return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -404,6 +446,133 @@ moe_status moe_combine(const moe_shape* s, const float* o, const float* topk_w, 
     if (!o || !topk_w || !pick_pos || !y) return MOE_ERR_INVALID;
     if (!aligned(o, 16) || !aligned(y, 16) || (residual && !aligned(residual, 16))) return MOE_ERR_INVALID;
     return hip_status(launch_combine(s, o, topk_w, pick_pos, T, residual, y, stream));
+}
+
+moe_status moe_dispatch(const moe_shape* s, const void* x, int32_t T, const int32_t* pick_pos, void* xs,
+                        hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    if (T == 0) return MOE_OK;
+    if (!x || !pick_pos || !xs || x == xs) return MOE_ERR_INVALID;
+    if (!aligned(x, 16) || !aligned(xs, 16)) return MOE_ERR_INVALID;
+    return hip_status(launch_dispatch(s, x, T, pick_pos, xs, stream));
+}
+
+moe_status moe_dispatch_backward(const moe_shape* s, const void* dxs, int32_t T, const int32_t* pick_pos, void* dx,
+                                 hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    if (T == 0) return MOE_OK;
+    if (!dxs || !pick_pos || !dx || dx == dxs) return MOE_ERR_INVALID;
+    if (!aligned(dxs, 16) || !aligned(dx, 16)) return MOE_ERR_INVALID;
+    return hip_status(launch_dispatch_backward(s, dxs, T, pick_pos, dx, stream));
+}
+
+moe_status moe_combine_backward(const moe_shape* s, const void* dy, const float* o, const float* topk_w,
+                                const int32_t* pick_pos, int32_t T, float* d_o, float* d_w, hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    if (T == 0) return MOE_OK;
+    if (!dy || !pick_pos || (!d_o && !d_w)) return MOE_ERR_INVALID;
+    if ((d_w && !o) || (d_o && !topk_w)) return MOE_ERR_INVALID;
+    if (!aligned(dy, 16) || (o && !aligned(o, 16)) || (d_o && !aligned(d_o, 16))) return MOE_ERR_INVALID;
+    if (dy == d_o || dy == d_w || (d_o && d_o == d_w) || (d_w && (d_w == o || d_w == topk_w))) return MOE_ERR_INVALID;
+    return hip_status(launch_combine_backward(s, dy, o, topk_w, pick_pos, T, d_o, d_w, stream));
+}
+
+moe_status moe_block_norm(const moe_shape* s, const void* x, const void* y, int32_t T, const float* post_gamma,
+                          const float* pre_gamma, const void* gate, int32_t gate_kind, float residual_scale, float eps,
+                          void* x_out, void* normed, hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    NormArgs a = norm_args(s, x, T, post_gamma, pre_gamma, gate, gate_kind, residual_scale, eps);
+    a.y = y;
+    a.x_out = x_out;
+    a.normed = normed;
+    MOE_TRY(check_norm(a));
+    if (T == 0) return MOE_OK;
+    MOE_TRY(check_norm_rows(a, y != nullptr));
+    return hip_status(launch_block_norm(s, a, stream));
+}
+
+moe_status moe_combine_norm(const moe_shape* s, const float* o, const float* topk_w, const int32_t* pick_pos,
+                            const void* x, int32_t T, const float* post_gamma, const float* pre_gamma, const void* gate,
+                            int32_t gate_kind, float residual_scale, float eps, void* x_out, void* normed,
+                            hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    NormArgs a = norm_args(s, x, T, post_gamma, pre_gamma, gate, gate_kind, residual_scale, eps);
+    a.o = o;
+    a.w = topk_w;
+    a.pick_pos = pick_pos;
+    a.x_out = x_out;
+    a.normed = normed;
+    MOE_TRY(check_norm(a));
+    if (T == 0) return MOE_OK;
+    if (!o || !topk_w || !pick_pos || !aligned(o, 16)) return MOE_ERR_INVALID;
+    if (x_out == o || normed == o) return MOE_ERR_INVALID;
+    MOE_TRY(check_norm_rows(a, true));
+    return hip_status(launch_block_norm(s, a, stream));
+}
+
+moe_status moe_block_norm_backward(const moe_shape* s, const void* x, const void* y, int32_t T, const float* post_gamma,
+                                   const float* pre_gamma, const void* gate, int32_t gate_kind, float residual_scale,
+                                   float eps, const void* d_x_out, const void* d_normed, void* dx, void* dy,
+                                   void* d_gate, float* d_post_gamma, float* d_pre_gamma, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    NormArgs a = norm_args(s, x, T, post_gamma, pre_gamma, gate, gate_kind, residual_scale, eps);
+    a.y = y;
+    MOE_TRY(check_norm(a));
+    NormGradArgs g;
+    memset(&g, 0, sizeof g);
+    g.d_x_out = d_x_out;
+    g.d_normed = d_normed;
+    g.dx = dx;
+    g.dy = dy;
+    g.d_gate = d_gate;
+    g.d_post = d_post_gamma;
+    g.d_pre = d_pre_gamma;
+    if (T == 0 && !d_post_gamma && !d_pre_gamma) return MOE_OK;
+    if (T > 0) {
+        if (!x || !ws || (!d_x_out && !d_normed)) return MOE_ERR_INVALID;
+        const void* in[] = {x, y, d_x_out, d_normed, gate_kind == MOE_GATE_ELEMENT ? gate : nullptr, dx, dy,
+                            gate_kind == MOE_GATE_ELEMENT ? d_gate : nullptr, post_gamma, pre_gamma, d_post_gamma,
+                            d_pre_gamma};
+        for (const void* p : in)
+            if (p && !aligned(p, 16)) return MOE_ERR_INVALID;
+        if (!aligned(ws, 256)) return MOE_ERR_INVALID;
+        const void* out[] = {dx, dy, d_gate, d_post_gamma, d_pre_gamma};
+        int given = 0;
+        for (int i = 0; i < 5; ++i) {
+            given += out[i] != nullptr;
+            for (int j = 0; j < i; ++j)
+                if (out[i] && out[i] == out[j]) return MOE_ERR_INVALID;
+        }
+        if (!given) return MOE_ERR_INVALID;
+        if ((pre_gamma != nullptr) != (d_normed != nullptr) || (d_pre_gamma && !pre_gamma)) return MOE_ERR_INVALID;
+        if ((dy && !y) || (d_gate && !gate) || (d_post_gamma && !post_gamma)) return MOE_ERR_INVALID;
+        if (!y && (post_gamma || gate)) return MOE_ERR_INVALID;
+        const WsLayout L = ws_layout(s, T);
+        if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+        g.part = (float*)((uint8_t*)ws + L.norm);
+    }
+    return hip_status(launch_block_norm_backward(s, a, g, stream));
+}
+
+moe_status moe_linear(const moe_matrix* m, const uint8_t* q, const uint8_t* s, float tensor_scale, const void* x,
+                      int32_t T, const float* bias, void* y, hipStream_t stream) {
+    if (!m || m->rows <= 0 || m->cols <= 0 || T < 0) return MOE_ERR_INVALID;
+    if (m->wformat != MOE_WF_MXFP4 && m->wformat != MOE_WF_NVFP4) return MOE_ERR_INVALID;
+    if (m->act_dtype != MOE_DT_F32 && m->act_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (!isfinite(tensor_scale)) return MOE_ERR_INVALID;
+    if (m->cols % 128 != 0 || m->rows > (1 << 24) || (long long)m->rows * m->cols > (1LL << 34) || T > kLinearMaxT) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!q || !s || !x || !y || x == y) return MOE_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(s, 16) || !aligned(x, 16) || !aligned(y, 16) || (bias && !aligned(bias, 4)))
+        return MOE_ERR_INVALID;
+    return hip_status(launch_linear(m, q, s, tensor_scale, x, T, bias, y, stream));
 }
 
 moe_status moe_layer(const moe_shape* s, const void* x, int32_t T, const float* w_router,

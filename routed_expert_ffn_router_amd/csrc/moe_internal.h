@@ -52,6 +52,22 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return readlane_f64(v, 63);
 }
 
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ float dpp_add_f32(float v) {
+    return v + __uint_as_float(dpp_u32<CTRL, ROWMASK>(0u, __float_as_uint(v)));
+}
+
+// the same sum in fp32
+__device__ __forceinline__ float wave_sum_f32(float v) {
+    v = dpp_add_f32<kDppXor1, 0xF>(v);
+    v = dpp_add_f32<kDppXor2, 0xF>(v);
+    v = dpp_add_f32<kDppHalfMirror, 0xF>(v);
+    v = dpp_add_f32<kDppMirror, 0xF>(v);
+    v = dpp_add_f32<kDppBcast15, 0xA>(v);
+    v = dpp_add_f32<kDppBcast31, 0xC>(v);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
 // maximum over each 16-lane row, returned in every lane of the row
 __device__ __forceinline__ float row16_max(float m) {
     m = fmaxf(m, __uint_as_float(dpp_u32<kDppXor1, 0xF>(__float_as_uint(m), __float_as_uint(m))));
@@ -230,6 +246,42 @@ __device__ __forceinline__ void store_act<float>(float* p, size_t i, float v) { 
 template <>
 __device__ __forceinline__ void store_act<uint16_t>(uint16_t* p, size_t i, float v) { p[i] = f32_to_bf16_bits(v); }
 
+// eight consecutive activations at a multiple of eight, as one or two 16-byte accesses (the
+// hardware's bf16 conversion rounds to nearest even and keeps NaN)
+struct f32x8 {
+    float v[8];
+};
+template <typename XT>
+__device__ __forceinline__ f32x8 load_act8(const XT* p, size_t i) {
+    f32x8 r;
+    if constexpr (sizeof(XT) == 4) {
+        const float4 a = *(const float4*)(p + i), b = *(const float4*)(p + i + 4);
+        r = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    } else {
+        const uint4 u = *(const uint4*)(p + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            r.v[2 * j] = __uint_as_float(w[j] << 16);
+            r.v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+    return r;
+}
+template <typename XT>
+__device__ __forceinline__ void store_act8(XT* p, size_t i, const f32x8& r) {
+    if constexpr (sizeof(XT) == 4) {
+        *(float4*)(p + i) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+        *(float4*)(p + i + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+    } else {
+        typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+        bf16x8 b;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = (__bf16)r.v[j];
+        *(bf16x8*)(p + i) = b;
+    }
+}
+
 // E4M3FN codes on the gfx950 conversion unit.  V_CVT_SCALEF32_PK_FP8_F32 writes the codes of
 // round-to-nearest-even(a / scale) and (b / scale) into the low (HI = false) or high 16 bits of
 // `old`; V_CVT_SCALEF32_PK_F32_FP8 returns code * scale for the two codes of the selected half.
@@ -386,6 +438,7 @@ struct WsLayout {
     size_t hdr, slots, sink, logits, idx, w, offsets, sorted_pick, pick_pos, perm_blocks, tiles, ntiles, desc, xq, xs,
         hq, hs, o;
     size_t stage_table, stage_list, stage_n, stage_ranges;   // NVFP4 staging (moe_layer)
+    size_t norm;   // the norms' gradient partials: over the intermediates, which those calls do not use
     size_t total;
     int nt;        // activation terms
     int max_tiles;
@@ -526,5 +579,50 @@ hipError_t launch_fill_table(const moe_shape* s, const uint8_t* base, size_t str
                              moe_expert* table, hipStream_t st);
 hipError_t launch_gather(const moe_shape* s, const moe_expert* table, const int32_t* list, int n,
                          uint8_t* staging, size_t stride, moe_expert* staged, hipStream_t st);
+
+// operators around the experts (sort.hip, norm.hip, linear.hip)
+hipError_t launch_dispatch(const moe_shape* s, const void* x, int T, const int32_t* pick_pos, void* xs,
+                           hipStream_t st);
+hipError_t launch_dispatch_backward(const moe_shape* s, const void* dxs, int T, const int32_t* pick_pos, void* dx,
+                                    hipStream_t st);
+hipError_t launch_combine_backward(const moe_shape* s, const void* dy, const float* o, const float* w,
+                                   const int32_t* pick_pos, int T, float* d_o, float* d_w, hipStream_t st);
+
+constexpr int kNormMaxD = 16384;
+struct NormArgs {
+    int T, d;
+    const void* x;
+    const void* y;            // or null; in the fused combine, o, w and pick_pos stand for it
+    const float* o;
+    const float* w;
+    const int32_t* pick_pos;
+    int k, shared;
+    float scaling;
+    const float* post;        // or null
+    const float* pre;         // or null
+    const void* gate;         // or null
+    int gate_kind;
+    float alpha, eps;         // residual scale, eps
+    void* x_out;              // or null
+    void* normed;             // or null
+};
+hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t st);   // a.o: fused with the combine
+
+struct NormGradArgs {
+    const void* d_x_out;      // or null
+    const void* d_normed;     // or null
+    void* dx;                 // outputs: each may be null
+    void* dy;
+    void* d_gate;
+    float* d_post;
+    float* d_pre;
+    float* part;              // [norm_grad_groups(T)][2][d] in the workspace
+};
+int norm_grad_groups(int T);  // groups of rows whose parameter gradients are summed apart
+hipError_t launch_block_norm_backward(const moe_shape* s, const NormArgs& a, const NormGradArgs& g, hipStream_t st);
+
+constexpr int kLinearMaxT = 64;
+hipError_t launch_linear(const moe_matrix* m, const uint8_t* q, const uint8_t* s, float ts, const void* x, int T,
+                         const float* bias, void* y, hipStream_t st);
 
 }  // namespace moe
