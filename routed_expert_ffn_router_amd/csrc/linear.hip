@@ -5,12 +5,23 @@
 // A code times its block scale is exact in bf16 (one bit of mantissa times a power of two, or times
 // the four bits of an E4M3 scale), so the weights enter the bf16 matrix cores exactly; a bf16 x does
 // too, and an fp32 x is the sum of three bf16 terms cut from it (8 + 8 + 8 bits, exact), each one more
-// MFMA into the same fp32 sums.
+// MFMA column or MFMA into the same fp32 sums.
 //
 // V_MFMA_F32_16X16X32_BF16: lane l supplies 8 consecutive K of weight row (A) or token (B) l % 16;
 // any assignment of K to the lane groups works when both operands share it.  A step covers 128 K of a
-// row: lane group g takes elements [32 g, 32 g + 32), 16 code bytes in one load, and MFMA h of the step
-// their elements [8 h, 8 h + 8).  C: lane l, register r is weight row 4 (l / 16) + r, token l % 16.
+// row: lane group g takes elements [32 g, 32 g + 32), 16 code bytes, and MFMA h of the step their
+// elements [8 h, 8 h + 8).  C: lane l, register r is weight row 4 (l / 16) + r, token l % 16.
+//
+// Three kernels.  The bytes are the weights', read once, so HBM is the floor; what a straight kernel
+// meets first is the vector L1, which serves a load one lane quad at a time: in the operand layout the
+// lanes of a quad hold four different rows, so a load of 16 bytes per lane costs as much as four that
+// are laid out along the rows, and a load of one scale byte per lane as much as one of 16 (taking the
+// scale or the x loads out of k_linear each saved 20 of 84 us at 65536 x 6144, 16 tokens).
+//   k_linear_ring    bf16 x, up to 16 tokens: codes, scales and x go straight to LDS (global_load_lds) in
+//                    row order, each wave into its own ring, so no wave waits for another before the sums;
+//   k_linear_stream  many rows: each wave keeps its K slice of x in registers for all the row tiles that
+//                    its workgroup takes, so x is read once per CU;
+//   k_linear         everything else, straight from global memory to registers.
 #include "moe_internal.h"
 
 namespace moe {
@@ -18,6 +29,7 @@ namespace moe {
 typedef __bf16 lin_bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 lin_bf16x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t lin_u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ lin_bf16x8 lin_as_bf16x8(const uint4& v) {
     lin_bf16x8 r;
@@ -25,47 +37,52 @@ __device__ __forceinline__ lin_bf16x8 lin_as_bf16x8(const uint4& v) {
     return r;
 }
 
-// 8 codes (one dword, element 2i in the low nibble of byte i) times a scale, exact in bf16
-__device__ __forceinline__ lin_bf16x8 lin_weights(uint32_t codes, float scale) {
-    lin_bf16x8 r;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const v2f_t v = b == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0)
-                      : b == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1)
-                      : b == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2)
-                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
-        r[2 * b] = (__bf16)(v[0] * scale);
-        r[2 * b + 1] = (__bf16)(v[1] * scale);
-    }
-    return r;
+// 8 codes (one dword, element 2i in the low nibble of byte i) times their block scale, exact in bf16.
+// MXFP4: the conversion unit's scale operand is a float read as a power of two (its exponent field, the
+// E8M0 byte; 255 makes every value NaN).
+__device__ __forceinline__ lin_bf16x8 lin_weights_mx(uint32_t codes, float scale) {
+    const lin_bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0),
+                     b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1),
+                     c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2),
+                     d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+    return lin_bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// NVFP4: codes at scale 1, times the E4M3 scale in fp32, rounded to bf16 (all exact)
+__device__ __forceinline__ lin_bf16x8 lin_weights_nv(uint32_t codes, float scale) {
+    const v2f_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0),
+                b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1),
+                c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2),
+                d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
+    return lin_bf16x8{(__bf16)(a[0] * scale), (__bf16)(a[1] * scale), (__bf16)(b[0] * scale), (__bf16)(b[1] * scale),
+                      (__bf16)(c[0] * scale), (__bf16)(c[1] * scale), (__bf16)(d[0] * scale), (__bf16)(d[1] * scale)};
 }
 
-// E8M0 byte -> 2^(b - 127) (b = 0 is a subnormal float; b = 255 is NaN)
-__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
-    return __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : b << 23);
-}
-
-// x's operand of one MFMA: NT bf16 terms of 8 consecutive elements
+// x's operand of one MFMA: NT bf16 terms of 8 consecutive elements, held as loaded until they are used
 template <typename XT>
-struct LinX {
-    static constexpr int NT = sizeof(XT) == 4 ? 3 : 1;
-    lin_bf16x8 t[NT];
+struct LinX;
+template <>
+struct LinX<uint16_t> {
+    static constexpr int NT = 1;
+    uint4 raw;
+    __device__ __forceinline__ void load(const uint16_t* p) { raw = gload16(p); }
+    __device__ __forceinline__ void terms(lin_bf16x8 (&t)[1]) const { t[0] = lin_as_bf16x8(raw); }
 };
-
-template <typename XT>
-__device__ __forceinline__ LinX<XT> lin_load_x(const XT* p, bool valid) {
-    LinX<XT> r;
-    if constexpr (sizeof(XT) == 2) {
-        r.t[0] = lin_as_bf16x8(valid ? *(const uint4*)p : make_uint4(0, 0, 0, 0));
-    } else {
-        // cut, not rounded: the first term of a large value never becomes infinite; an infinite
-        // value is its own first term
-        f32x8 v = {};
-        if (valid) v = load_act8(p, 0);
+template <>
+struct LinX<float> {
+    static constexpr int NT = 3;
+    uint4 raw[2];
+    __device__ __forceinline__ void load(const float* p) {
+        raw[0] = gload16(p);
+        raw[1] = gload16(p + 4);
+    }
+    // cut, not rounded: the first term of a large value never becomes infinite; an infinite value is
+    // its own first term
+    __device__ __forceinline__ void terms(lin_bf16x8 (&t)[3]) const {
+        const uint32_t v[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
         uint32_t w[3][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float rest = v.v[e];
+            float rest = __uint_as_float(v[e]);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const uint32_t cut = __float_as_uint(rest) & 0xffff0000u;
@@ -75,10 +92,26 @@ __device__ __forceinline__ LinX<XT> lin_load_x(const XT* p, bool valid) {
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            r.t[i] = lin_as_bf16x8(make_uint4(w[i][0] >> 16 | w[i][1], w[i][2] >> 16 | w[i][3], w[i][4] >> 16 | w[i][5],
-                                              w[i][6] >> 16 | w[i][7]));
+            t[i] = lin_as_bf16x8(make_uint4(w[i][0] >> 16 | w[i][1], w[i][2] >> 16 | w[i][3], w[i][4] >> 16 | w[i][5],
+                                            w[i][6] >> 16 | w[i][7]));
     }
-    return r;
+};
+
+// a step's scale byte(s) as factors of its first and last 16 elements
+template <int WF>
+__device__ __forceinline__ void lin_scales(uint32_t raw, float (&s)[2]) {
+    if constexpr (WF == MOE_WF_MXFP4) {
+        s[0] = s[1] = __uint_as_float(raw << 23);
+    } else {
+        const v2f_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(raw, 1.0f, false);
+        s[0] = v[0];
+        s[1] = v[1];
+    }
+}
+template <int WF>
+__device__ __forceinline__ lin_bf16x8 lin_weights(uint32_t codes, float scale) {
+    if constexpr (WF == MOE_WF_MXFP4) return lin_weights_mx(codes, scale);
+    else return lin_weights_nv(codes, scale);
 }
 
 struct LinArgs {
@@ -91,68 +124,113 @@ struct LinArgs {
     void* y;
 };
 
+// rows row .. row + 3 of token t
+template <typename XT>
+__device__ __forceinline__ void lin_store(const LinArgs& a, int t, int row, const lin_f32x4& v) {
+    float o[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = fmaf(v[r], a.ts, a.bias && row + r < a.N ? a.bias[row + r] : 0.0f);
+    XT* y = (XT*)a.y + (size_t)t * a.N + row;
+    if ((a.N & 3) == 0 && row < a.N) {           // row is a multiple of four: the four are there, and aligned
+        if constexpr (sizeof(XT) == 4) *(float4*)y = make_float4(o[0], o[1], o[2], o[3]);
+        else *(uint2*)y = make_uint2(f32_to_bf16_bits(o[0]) | (uint32_t)f32_to_bf16_bits(o[1]) << 16,
+                                     f32_to_bf16_bits(o[2]) | (uint32_t)f32_to_bf16_bits(o[3]) << 16);
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (row + r < a.N) store_act(y, (size_t)r, o[r]);
+}
+
+// what a wave loads for one step: codes and scale bytes of F row fragments, x of C token fragments
+template <typename XT, int F, int C>
+struct LinStep {
+    uint4 code[F];
+    uint32_t sc[F];
+    LinX<XT> x[C][4];
+};
+
 // A workgroup of W waves owns 16 F rows and 16 C tokens; its waves share out K, and their sums are
-// added through LDS in wave order.
-template <typename XT, int WF, int F, int C, int W>
+// added through LDS in wave order.  A wave keeps D steps of loads in flight, in a ring of registers.
+template <typename XT, int WF, int F, int C, int W, int D>
 __global__ __launch_bounds__(64 * W) void k_linear(LinArgs a) {
     __shared__ lin_f32x4 part[W][F * C][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int n0 = blockIdx.x * 16 * F, t0 = blockIdx.y * 16 * C;
     const int NS = a.K / 128;
-    const int s0 = wave * NS / W, s1 = (wave + 1) * NS / W;
+    const int s0 = wave * NS / W, n = (wave + 1) * NS / W - s0;
     constexpr int SB = WF == MOE_WF_MXFP4 ? 32 : 16;          // weights per scale
     const uint8_t* q[F];
     const uint8_t* s[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
         const int row = n0 + 16 * f + li < a.N ? n0 + 16 * f + li : a.N - 1;
-        q[f] = a.q + (size_t)row * (a.K / 2) + lg * 16;
-        s[f] = a.s + (size_t)row * (a.K / SB) + lg * (32 / SB);
+        q[f] = a.q + (size_t)row * (a.K / 2) + (size_t)s0 * 64 + lg * 16;
+        s[f] = a.s + (size_t)row * (a.K / SB) + (size_t)s0 * (128 / SB) + lg * (32 / SB);
     }
-    const XT* x[C];
-    bool tok[C];
+    const XT* x[C];                                            // columns past the last token repeat it
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        tok[c] = t0 + 16 * c + li < a.T;
-        x[c] = (const XT*)a.x + (size_t)(tok[c] ? t0 + 16 * c + li : 0) * a.K + lg * 32;
+        const int t = t0 + 16 * c + li < a.T ? t0 + 16 * c + li : a.T - 1;
+        x[c] = (const XT*)a.x + (size_t)t * a.K + (size_t)s0 * 128 + lg * 32;
     }
     lin_f32x4 acc[F][C];
 #pragma unroll
     for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[f][c] = lin_f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int ks = s0; ks < s1; ++ks) {
-        uint4 code[F];
-        float sc[F][2];
+
+    LinStep<XT, F, C> ring[D];
+    auto request = [&](LinStep<XT, F, C>& r, int k) {
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            code[f] = gload16(q[f] + (size_t)ks * 64);
-            if constexpr (WF == MOE_WF_MXFP4) {
-                sc[f][0] = sc[f][1] = e8m0_to_f32(s[f][(size_t)ks * 4]);
-            } else {
-                const v2f_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(*(const uint16_t*)(s[f] + (size_t)ks * 8), 1.0f, false);
-                sc[f][0] = v[0];
-                sc[f][1] = v[1];
-            }
+            r.code[f] = gload16(q[f] + (size_t)k * 64);
+            if constexpr (WF == MOE_WF_MXFP4) r.sc[f] = *(__attribute__((address_space(1))) const uint8_t*)(s[f] + (size_t)k * 4);
+            else r.sc[f] = *(__attribute__((address_space(1))) const uint16_t*)(s[f] + (size_t)k * 8);
         }
-        LinX<XT> xv[C][4];
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) xv[c][h] = lin_load_x(x[c] + (size_t)ks * 128 + 8 * h, tok[c]);
+            for (int h = 0; h < 4; ++h) r.x[c][h].load(x[c] + (size_t)k * 128 + 8 * h);
+    };
+    auto multiply = [&](const LinStep<XT, F, C>& r) {
+        float sc[F][2];
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int f = 0; f < F; ++f) {
+            lin_scales<WF>(r.sc[f], sc[f]);
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            lin_bf16x8 xt[C][LinX<XT>::NT];
+#pragma unroll
+            for (int c = 0; c < C; ++c) r.x[c][h].terms(xt[c]);
 #pragma unroll
             for (int f = 0; f < F; ++f) {
-                const uint32_t word = h == 0 ? code[f].x : h == 1 ? code[f].y : h == 2 ? code[f].z : code[f].w;
-                const lin_bf16x8 wv = lin_weights(word, sc[f][h / 2]);
+                const uint32_t word = h == 0 ? r.code[f].x : h == 1 ? r.code[f].y : h == 2 ? r.code[f].z : r.code[f].w;
+                const lin_bf16x8 wv = lin_weights<WF>(word, sc[f][h / 2]);
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll
                     for (int i = 0; i < LinX<XT>::NT; ++i)
-                        acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv[c][h].t[i], acc[f][c], 0, 0, 0);
+                        acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xt[c][i], acc[f][c], 0, 0, 0);
             }
+        }
+    };
+    if (n > 0) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) request(ring[i], i < n ? i : n - 1);
+        int k = 0;
+        for (; k + D < n; k += D) {          // steps past the last load the last one again
+#pragma unroll
+            for (int i = 0; i < D; ++i) {
+                multiply(ring[i]);
+                request(ring[i], k + i + D < n ? k + i + D : n - 1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+            if (k + i < n) multiply(ring[i]);
     }
 #pragma unroll
     for (int f = 0; f < F; ++f)
@@ -164,21 +242,371 @@ __global__ __launch_bounds__(64 * W) void k_linear(LinArgs a) {
     __syncthreads();
     for (int i = threadIdx.x; i < F * C * 64; i += 64 * W) {
         const int fc = i >> 6, l = i & 63;
-        const int t = t0 + 16 * (fc % C) + (l & 15), n = n0 + 16 * (fc / C) + 4 * (l >> 4);
+        const int t = t0 + 16 * (fc % C) + (l & 15), row = n0 + 16 * (fc / C) + 4 * (l >> 4);
         if (t >= a.T) continue;
         lin_f32x4 v = part[0][fc][l];
 #pragma unroll
         for (int w = 1; w < W; ++w) v += part[w][fc][l];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (n + r < a.N)
-                store_act((XT*)a.y, (size_t)t * a.N + n + r, fmaf(v[r], a.ts, a.bias ? a.bias[n + r] : 0.0f));
+        lin_store<XT>(a, t, row, v);
     }
+}
+
+// ---------------------------------------------------------------------------------------------
+// direct loads to LDS.  A row fragment's step is 16 rows x 64 code bytes, one instruction of 16 bytes
+// per lane, a lane quad per row; its 16-byte parts are swizzled by row so that the operand reads meet no
+// bank conflict.  Scales: 16 rows x 16 bytes, one instruction of 4 bytes per lane, for 2 (NVFP4) or 4
+// (MXFP4) steps.  Rows past the last repeat it, and so do scale bytes past a row's end.
+//
+// The loads in flight are counted by hand (wait_vm), and LDS is read in asm blocks that wait for their
+// own reads: a read that the compiler sees would make it wait for every direct load.
+// ---------------------------------------------------------------------------------------------
+// Term i (0, 1, 2) of 8 fp32 values as bf16, m1 = i > 0 and m2 = i > 1 as masks of the upper half: what the
+// terms before it leave, cut off.  Terms 1 and 2 of an infinite or NaN value come out NaN; the sum over
+// term 0 is then not finite and alone gives the result (lin_sum_terms).
+__device__ __forceinline__ lin_bf16x8 lin_f32_term(const lin_u32x4& a, const lin_u32x4& b, uint32_t m1, uint32_t m2) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t v = e < 4 ? a[e] : b[e - 4];
+        const float r = __uint_as_float(v) - __uint_as_float(v & m1);
+        w[e] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & m2));
+    }
+    return lin_as_bf16x8(make_uint4(__builtin_amdgcn_perm(w[1], w[0], 0x07060302), __builtin_amdgcn_perm(w[3], w[2], 0x07060302),
+                                    __builtin_amdgcn_perm(w[5], w[4], 0x07060302), __builtin_amdgcn_perm(w[7], w[6], 0x07060302)));
+}
+__device__ __forceinline__ lin_f32x4 lin_sum_terms(const lin_f32x4& s0, const lin_f32x4& s1, const lin_f32x4& s2) {
+    lin_f32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __builtin_isfinite(s0[i]) ? s0[i] + (s1[i] + s2[i]) : s0[i];
+    return r;
+}
+// tokens of one pass over the weights (blockIdx.y): sixteen columns, or five tokens of three columns
+// (column 3 t + i is term i of token t)
+template <typename XT>
+constexpr int kLinPass = sizeof(XT) == 4 ? 5 : 16;
+
+constexpr int kLinDmaMaxK = 8192;         // 8 steps for each of 8 waves
+typedef __attribute__((address_space(3))) uint8_t* lin_lds_t;
+
+__device__ __forceinline__ uint32_t lin_lds_offset(const uint8_t* p) { return (uint32_t)(uintptr_t)(lin_lds_t)p; }
+__device__ __forceinline__ int lin_swz(int r) { return ((r >> 2) ^ (r >> 1)) & 3; }
+
+template <int WF>
+struct LinFmt {
+    static constexpr int UB = WF == MOE_WF_MXFP4 ? 4 : 8;      // scale bytes of a row and step
+    static constexpr int SPD = 16 / UB;                        // steps of one scale load
+};
+
+// wait until at most `left` of this wave's vector-memory operations are in flight
+template <int M>
+__device__ __forceinline__ void lin_wait_upto(int left) {
+    if constexpr (M > 0) {
+        if (left < M) {
+            lin_wait_upto<M - 1>(left);
+            return;
+        }
+    }
+    wait_vm<M>();
+}
+
+// the source of a lane's direct loads of codes: its part of its row, from step s0 on
+__device__ __forceinline__ const uint8_t* lin_src(const LinArgs& a, int tile, int s0, int lane) {
+    const int r = lane >> 2, row = tile * 16 + r < a.N ? tile * 16 + r : a.N - 1;
+    return a.q + (size_t)row * (a.K / 2) + (size_t)s0 * 64 + ((lane & 3) ^ lin_swz(r)) * 16;
+}
+template <int WF>
+__device__ __forceinline__ void lin_dma_scales(const LinArgs& a, int tile, int s0, int i, int lane, uint8_t* dst) {
+    const int SR = a.K / 128 * LinFmt<WF>::UB;
+    const int r = lane >> 2, row = tile * 16 + r < a.N ? tile * 16 + r : a.N - 1;
+    const int off = s0 * LinFmt<WF>::UB + i * 16 + (lane & 3) * 4;
+    dma4(a.s + (size_t)row * SR + (off < SR ? off : SR - 4), dst);
+}
+
+// the waves' sums of a tile, in wave order, and over a token's terms: a lane's rows of token lane % 16
+template <typename XT, int W>
+__device__ __forceinline__ lin_f32x4 lin_sum_waves(const lin_f32x4* part, int lane) {
+    if constexpr (sizeof(XT) == 2) {
+        lin_f32x4 v = part[lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += part[w * 64 + lane];
+        return v;
+    } else {
+        const int at = (lane & 48) + 3 * (lane & 15);          // lanes of tokens 0 .. 4
+        lin_f32x4 v[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            v[i] = part[at + i];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v[i] += part[w * 64 + at + i];
+        }
+        return lin_sum_terms(v[0], v[1], v[2]);
+    }
+}
+
+// One tile of 16 rows per workgroup, K shared out over W waves of at most NMAX steps; NX direct loads
+// bring x's step (four bf16 or two fp32 tokens each), swizzled by token.  D steps of codes and x in flight.
+template <typename XT, int WF, int NX, int W, int D, int NMAX>
+__global__ __launch_bounds__(64 * W) void k_linear_ring(LinArgs a) {
+    constexpr int UB = LinFmt<WF>::UB, SPD = LinFmt<WF>::SPD;
+    constexpr int STG = (1 + NX) * 1024, SCB = NMAX / SPD * 256, WB = SCB + D * STG;
+    constexpr bool F32 = sizeof(XT) == 4;
+    constexpr int TB = 128 * (int)sizeof(XT), TPL = 1024 / TB;  // bytes of a token's step, tokens of one load
+    static_assert(NMAX % SPD == 0 && WB >= 1024, "a wave's sums fit into its ring");
+    __shared__ __align__(16) uint8_t ring[W * WB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int tile = blockIdx.x, NS = a.K / 128;
+    const int s0 = wave * NS / W, n = (wave + 1) * NS / W - s0;
+    const int t0 = blockIdx.y * kLinPass<XT>, nt = a.T - t0 < kLinPass<XT> ? a.T - t0 : kLinPass<XT>;
+    uint8_t* mine = ring + wave * WB;
+    const uint8_t* qs = lin_src(a, tile, s0, lane);
+    const uint8_t* xs[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        const int t = TPL * i + lane / (64 / TPL), tok = t0 + (t < nt ? t : nt - 1);
+        xs[i] = (const uint8_t*)a.x + ((size_t)tok * a.K + (size_t)s0 * 128) * sizeof(XT) + ((lane % (64 / TPL)) ^ t) * 16;
+    }
+    auto issue = [&](int k, int slot) {
+        uint8_t* st = mine + SCB + slot * STG;
+        dma16(qs + (size_t)k * 64, st);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) dma16(xs[i] + (size_t)k * TB, st + (1 + i) * 1024);
+    };
+    for (int i = 0; i * SPD < n; ++i) lin_dma_scales<WF>(a, tile, s0, i, lane, mine + i * 256);
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+        if (i < n) issue(i, i);
+    const uint32_t base = lin_lds_offset(mine);
+    const uint32_t qa = base + SCB + li * 64 + (lg ^ lin_swz(li)) * 16, sa = base + li * 16 + lg * (UB / 4);
+    uint32_t xa[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {                              // columns past the last repeat a token
+        const int t = F32 ? li / 3 % (TPL * NX) : li % (TPL * NX);
+        xa[h] = base + SCB + 1024 + t * TB + ((F32 ? 8 * lg + 2 * h : 4 * lg + h) ^ t) * 16;
+    }
+    const uint32_t m1 = li % 3 > 0 ? 0xffff0000u : 0u, m2 = li % 3 > 1 ? 0xffff0000u : 0u;
+    lin_f32x4 acc[2] = {lin_f32x4{0.f, 0.f, 0.f, 0.f}, lin_f32x4{0.f, 0.f, 0.f, 0.f}};
+    int slot = 0;
+    for (int k = 0; k < n; ++k) {
+        lin_wait_upto<(D - 1) * (1 + NX)>((n - 1 - k < D - 1 ? n - 1 - k : D - 1) * (1 + NX));
+        lin_u32x4 code, x[4], x2[4];
+        uint32_t sc;
+        const uint32_t so = slot * STG, sk = sa + k / SPD * 256 + k % SPD * UB;
+        if constexpr (F32)             // the other 16 bytes of a lane's 8 values are in the neighbouring slot
+            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(x2[0]), "=&v"(x2[1]), "=&v"(x2[2]), "=&v"(x2[3])
+                         : "v"((xa[0] + so) ^ 16), "v"((xa[1] + so) ^ 16), "v"((xa[2] + so) ^ 16), "v"((xa[3] + so) ^ 16)
+                         : "memory");
+        if constexpr (WF == MOE_WF_MXFP4)
+            asm volatile("ds_read_b128 %0, %6\n\tds_read_u8 %1, %7\n\tds_read_b128 %2, %8\n\tds_read_b128 %3, %9\n\t"
+                         "ds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(code), "=&v"(sc), "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+                         : "v"(qa + so), "v"(sk), "v"(xa[0] + so), "v"(xa[1] + so), "v"(xa[2] + so), "v"(xa[3] + so)
+                         : "memory");
+        else
+            asm volatile("ds_read_b128 %0, %6\n\tds_read_u16 %1, %7\n\tds_read_b128 %2, %8\n\tds_read_b128 %3, %9\n\t"
+                         "ds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(code), "=&v"(sc), "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+                         : "v"(qa + so), "v"(sk), "v"(xa[0] + so), "v"(xa[1] + so), "v"(xa[2] + so), "v"(xa[3] + so)
+                         : "memory");
+        if (k + D < n) issue(k + D, slot);
+        slot = slot + 1 == D ? 0 : slot + 1;
+        float s2[2];
+        lin_scales<WF>(sc, s2);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            lin_bf16x8 xv;
+            if constexpr (F32) xv = lin_f32_term(x[h], x2[h], m1, m2);
+            else __builtin_memcpy(&xv, &x[h], 16);
+            acc[h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lin_weights<WF>(code[h], s2[h / 2]), xv, acc[h & 1], 0, 0, 0);
+        }
+    }
+    acc[0] += acc[1];
+    mfma_results_here(acc[0]);
+    __syncthreads();
+    lin_f32x4* part = (lin_f32x4*)ring;
+    part[wave * 64 + lane] = acc[0];
+    __syncthreads();
+    if (wave == 0 && li < nt) lin_store<XT>(a, t0 + li, tile * 16 + 4 * lg, lin_sum_waves<XT, W>(part, lane));
+}
+
+// Tiles of 16 rows blockIdx.x, blockIdx.x + G, .. (G workgroups); wave w of 8 takes K slice w of every
+// tile and keeps x's slice in registers.  A wave's ring holds two tiles of its slice.  The waves' sums of
+// kLinRound tiles meet in LDS between two barriers, one wave adding up each tile in wave order.
+// Rounds: sums of 1, 2, 3 tiles at a time in two buffers, one barrier a round, took 65, 56 and 53 us at
+// 65536 x 6144 NVFP4 and 16 tokens; one buffer of 4 tiles with two barriers 53, one of 6 52.
+constexpr int kLinWaves = 8;
+
+template <typename XT, int WF, int NSW>
+__global__ __launch_bounds__(64 * kLinWaves) void k_linear_stream(LinArgs a, int ntiles) {
+    constexpr int W = kLinWaves, R = NSW <= 6 ? 4 : 2;          // (8 steps leave LDS for the sums of two)
+    constexpr int UB = LinFmt<WF>::UB, SPD = LinFmt<WF>::SPD, NSC = (NSW + SPD - 1) / SPD;
+    constexpr int STG = NSW * 1024 + NSC * 256;
+    constexpr bool F32 = sizeof(XT) == 4;
+    static_assert(NSW % 2 == 0 && STG >= 4096, "steps are read in pairs; a slot of the ring holds a step of x");
+    __shared__ __align__(16) uint8_t ring[W * 2 * STG];
+    __shared__ lin_f32x4 part[R][W][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int NS = a.K / 128, G = gridDim.x;
+    const int s0 = wave * NS / W, n = (wave + 1) * NS / W - s0, nsc = (n + SPD - 1) / SPD;
+    const int t0 = blockIdx.y * kLinPass<XT>, nt = a.T - t0 < kLinPass<XT> ? a.T - t0 : kLinPass<XT>;
+    uint8_t* mine = ring + wave * 2 * STG;
+    auto issue = [&](int tile, int slot) {
+        const uint8_t* q = lin_src(a, tile, s0, lane);
+        uint8_t* st = mine + slot * STG;
+#pragma unroll
+        for (int i = 0; i < NSW; ++i)
+            if (i < n) dma16(q + i * 64, st + i * 1024);
+#pragma unroll
+        for (int i = 0; i < NSC; ++i)
+            if (i < nsc) lin_dma_scales<WF>(a, tile, s0, i, lane, st + NSW * 1024 + i * 256);
+    };
+    int tile = blockIdx.x;
+    issue(tile, 0);
+    lin_bf16x8 x[NSW][4];
+    if constexpr (F32) {
+        // this lane's token and term
+        const int t = t0 + (li / 3 < nt ? li / 3 : nt - 1);
+        const float* xr = (const float*)a.x + (size_t)t * a.K + lg * 32;
+        const uint32_t m1 = li % 3 > 0 ? 0xffff0000u : 0u, m2 = li % 3 > 1 ? 0xffff0000u : 0u;
+#pragma unroll
+        for (int i = 0; i < NSW; ++i) {
+            const int k = s0 + i < NS ? s0 + i : NS - 1;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                lin_u32x4 v[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 u = gload16(xr + (size_t)k * 128 + 8 * h + 4 * j);
+                    v[j] = lin_u32x4{u.x, u.y, u.z, u.w};
+                }
+                x[i][h] = lin_f32_term(v[0], v[1], m1, m2);
+            }
+        }
+    } else {
+        // in row order (four tokens x 256 bytes a load), then through the ring's second slot to the
+        // operand layout
+        uint4 raw[NSW][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = 4 * j + lg, tok = t < nt ? t : nt - 1;
+            const uint16_t* xr = (const uint16_t*)a.x + (size_t)(t0 + tok) * a.K + (li ^ t) * 8;
+#pragma unroll
+            for (int i = 0; i < NSW; ++i) raw[i][j] = gload16(xr + (size_t)(s0 + i < NS ? s0 + i : NS - 1) * 128);
+        }
+        uint4* stage = (uint4*)(mine + STG);
+#pragma unroll
+        for (int i = 0; i < NSW; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) stage[j * 64 + lane] = raw[i][j];
+            asm volatile("" ::: "memory");                    // one wave's own reads and writes, in order
+#pragma unroll
+            for (int h = 0; h < 4; ++h) x[i][h] = lin_as_bf16x8(stage[li * 16 + ((lg * 4 + h) ^ li)]);
+            asm volatile("" ::: "memory");
+        }
+    }
+    // x is here (and the first tile) before the loop, whose waits count the ring's loads alone
+    wait_vm<0>();
+#pragma unroll
+    for (int i = 0; i < NSW; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) asm volatile("" : "+v"(x[i][h]));
+    if (tile + G < ntiles) issue(tile + G, 1);                 // the slot's reads are over: their values are used above
+
+    const uint32_t base = lin_lds_offset(mine);
+    const uint32_t qa = base + li * 64 + (lg ^ lin_swz(li)) * 16, sa = base + NSW * 1024 + li * 16 + lg * (UB / 4);
+    for (int it = 0; tile < ntiles; tile += G, ++it) {
+        const bool more = tile + G < ntiles;
+        // the next tile's loads may be in flight (a store of y counts as one more, which only waits longer)
+        lin_wait_upto<NSW + NSC>(more ? n + nsc : 0);
+        const uint32_t so = (it & 1) * STG;
+        lin_u32x4 code[NSW];
+        uint32_t sc[NSW];
+#pragma unroll
+        for (int i = 0; i < NSW; i += 2) {
+            const uint32_t sk = sa + so + (i / SPD) * 256 + (i % SPD) * UB;
+            if constexpr (WF == MOE_WF_MXFP4)
+                asm volatile("ds_read_b128 %0, %4\n\tds_read_u8 %2, %5\n\tds_read_b128 %1, %4 offset:1024\n\t"
+                             "ds_read_u8 %3, %5 offset:4\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(code[i]), "=&v"(code[i + 1]), "=&v"(sc[i]), "=&v"(sc[i + 1])
+                             : "v"(qa + so + i * 1024), "v"(sk) : "memory");
+            else
+                asm volatile("ds_read_b128 %0, %4\n\tds_read_u16 %2, %5\n\tds_read_b128 %1, %4 offset:1024\n\t"
+                             "ds_read_u16 %3, %5 offset:8\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(code[i]), "=&v"(code[i + 1]), "=&v"(sc[i]), "=&v"(sc[i + 1])
+                             : "v"(qa + so + i * 1024), "v"(sk) : "memory");
+        }
+        if (tile + 2 * G < ntiles) issue(tile + 2 * G, it & 1);
+        lin_f32x4 acc[2] = {lin_f32x4{0.f, 0.f, 0.f, 0.f}, lin_f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < NSW; ++i) {
+            if (i >= n) continue;
+            float s2[2];
+            lin_scales<WF>(sc[i], s2);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                acc[h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lin_weights<WF>(code[i][h], s2[h / 2]), x[i][h],
+                                                                     acc[h & 1], 0, 0, 0);
+        }
+        acc[0] += acc[1];
+        mfma_results_here(acc[0]);
+        part[it % R][wave][lane] = acc[0];
+        if (it % R != R - 1 && more) continue;
+        lds_barrier();
+        const int j = it / R * R + wave;                       // the round's tile that this wave adds up
+        if (j <= it && wave < R && li < nt)
+            lin_store<XT>(a, t0 + li, (blockIdx.x + j * G) * 16 + 4 * lg, lin_sum_waves<XT, W>(&part[wave][0][0], lane));
+        lds_barrier();                                         // the next round overwrites the sums
+    }
+}
+
+template <typename XT, int WF, int NX>
+static void ring_launch(const LinArgs& a, int passes, hipStream_t st) {
+    MOE_LAUNCH((k_linear_ring<XT, WF, NX, 8, 2, 8>), dim3((a.N + 15) / 16, passes), dim3(512), 0, st, a);
+}
+
+template <typename XT, int WF>
+static void stream_launch(const LinArgs& a, int passes, hipStream_t st) {
+    const int ntiles = (a.N + 15) / 16, n = (a.K / 128 + kLinWaves - 1) / kLinWaves;
+    const dim3 grid(ntiles < 256 ? ntiles : 256, passes), block(64 * kLinWaves);          // a workgroup per CU
+    if (n <= 4) MOE_LAUNCH((k_linear_stream<XT, WF, 4>), grid, block, 0, st, a, ntiles);
+    else if (n <= 6) MOE_LAUNCH((k_linear_stream<XT, WF, 6>), grid, block, 0, st, a, ntiles);
+    else MOE_LAUNCH((k_linear_stream<XT, WF, 8>), grid, block, 0, st, a, ntiles);
+}
+
+template <typename XT, int WF, int F, int C, int W, int D>
+static void plain_launch(const LinArgs& a, hipStream_t st) {
+    MOE_LAUNCH((k_linear<XT, WF, F, C, W, D>), dim3((a.N + 16 * F - 1) / (16 * F), (a.T + 16 * C - 1) / (16 * C)),
+               dim3(64 * W), 0, st, a);
 }
 
 template <typename XT, int WF>
 static void linear_launch(const LinArgs& a, hipStream_t st) {
-    MOE_LAUNCH((k_linear<XT, WF, 1, 1, 8>), dim3((a.N + 15) / 16, (a.T + 15) / 16), dim3(512), 0, st, a);
+    const bool many = a.N >= 16384;
+    const int passes = (a.T + kLinPass<XT> - 1) / kLinPass<XT>;
+    if (a.K <= kLinDmaMaxK) {
+        if constexpr (sizeof(XT) == 2) {
+            if (many && a.T > 4) stream_launch<XT, WF>(a, passes, st);
+            else if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
+            else if (a.T <= 8) ring_launch<XT, WF, 2>(a, 1, st);
+            else ring_launch<XT, WF, 4>(a, passes, st);
+            return;
+        } else if (!many) {
+            if (a.T <= 2) ring_launch<XT, WF, 1>(a, 1, st);
+            else if (a.T <= 4) ring_launch<XT, WF, 2>(a, 1, st);
+            else ring_launch<XT, WF, 3>(a, passes, st);
+            return;
+        } else if (passes <= 2) {
+            stream_launch<XT, WF>(a, passes, st);
+            return;
+        }
+    }
+    if (a.T > 32) plain_launch<XT, WF, 2, 4, 4, 1>(a, st);
+    else if (a.T > 16) plain_launch<XT, WF, 2, 2, 4, 1>(a, st);
+    else if (many) plain_launch<XT, WF, 4, 1, 8, 1>(a, st);
+    else plain_launch<XT, WF, 1, 1, 8, 2>(a, st);
 }
 
 hipError_t launch_linear(const moe_matrix* m, const uint8_t* q, const uint8_t* s, float ts, const void* x, int T,

@@ -341,6 +341,7 @@ def quantised(g, N, K, wf):
 LINEAR = [  # N, K, T
     (1, 128, 1), (15, 256, 1), (16, 128, 2), (33, 384, 3), (128, 4096, 1), (100, 1152, 5), (257, 640, 16), (64, 2048, 17),
     (48, 512, 33), (31, 896, 64), (5000, 256, 7), (2048, 6144, 4), (4096, 512, 12), (40000, 128, 1), (9000, 384, 40), (515, 8192, 9),
+    (20000, 640, 6), (16399, 8192, 13), (16384, 6144, 5), (33000, 256, 16), (300, 8320, 5), (16400, 8320, 3),
 ]
 
 
@@ -381,9 +382,9 @@ def test_linear_scale_bytes(act):
 def test_linear_values_outside_the_numbers():
     """Infinity and NaN in x reach the rows whose weights see them, in that token alone."""
     g = gen(12)
-    N, K, T = 40, 256, 3
-    q, s, _ = quantised(g, N, K, 0)
-    for act in (BF16, F32):
+    K, T = 256, 3
+    for N, act in ((40, BF16), (40, F32), (16390, BF16), (16390, F32)):
+        q, s, _ = quantised(g, N, K, 0)
         x = rand(g, T, K, dtype=act)
         mat = m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32)
         y, z = torch.empty(T, N, dtype=act, device="cuda"), torch.empty(T, N, dtype=act, device="cuda")
@@ -395,7 +396,7 @@ def test_linear_values_outside_the_numbers():
         assert torch.equal(torch.isnan(z[0]), w == 0)        # 0 times infinity
         assert torch.equal(z[0][w != 0], (torch.sign(w) * float("inf")).to(act)[w != 0])
         # the largest finite values stay finite on the way
-        if act == F32:
+        if act == F32 and N == 40:
             x = torch.zeros(1, K, device="cuda")
             x[0, 7] = torch.finfo(F32).max
             small_s = torch.full_like(s, 100)
