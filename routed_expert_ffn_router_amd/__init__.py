@@ -155,10 +155,17 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream of the current device; torch.cuda.current_stream() builds a Stream object
+        # around this handle, which takes 2.5 us, half of a small call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -278,102 +285,105 @@ def moe_layer_noalloc(shape, x, T: int, w_router, logit_bias, d_table, residual,
 # MoeError with MOE_ERR_INVALID before the library is called.  Integer device pointers pass as they are.
 # ---------------------------------------------------------------------------------------------
 
-def _check_tensors(fn: str, *args):
-    """args: (tensor, dtype, elements) triples; a tensor may be None or an integer pointer."""
-    import torch
+def _pointers(fn: str, *args) -> list:
+    """Device pointers of (tensor, dtype, elements) triples, checked; a tensor may be None or a pointer."""
+    out = []
     device = None
     for t, dtype, n in args:
         if t is None or isinstance(t, int):
+            out.append(t)
             continue
+        on = t.get_device()
         if device is None:
-            device = torch.cuda.current_device() if t.is_cuda else None
-        if t.dtype is not dtype or not t.is_cuda or t.get_device() != device or t.numel() < n or not t.is_contiguous():
+            device = on
+        if on != device or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
             raise MoeError(fn, MOE_ERR_INVALID)
+        out.append(t.data_ptr())
+    if device is not None and (device < 0 or device != _current_device()):
+        raise MoeError(fn, MOE_ERR_INVALID)
+    return out
 
 
-def _act(act_dtype: int):
-    import torch
-    return torch.bfloat16 if act_dtype == MOE_DT_BF16 else torch.float32
+_DTYPES = None
 
 
-def _expert_rows(shape, T: int) -> int:
-    return T * (shape.top_k + shape.n_shared)
+def _dtypes(act_dtype: int):
+    """(act_dtype's, fp32, int32, uint8) torch dtypes."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        rest = (torch.float32, torch.int32, torch.uint8)
+        _DTYPES = {MOE_DT_F32: (torch.float32, *rest), MOE_DT_BF16: (torch.bfloat16, *rest)}
+    return _DTYPES.get(act_dtype, _DTYPES[MOE_DT_F32])
 
 
 def moe_dispatch(shape, x, T: int, pick_pos, xs, stream=None):
-    import torch
-    act, d = _act(shape.act_dtype), shape.d_model
-    _check_tensors("moe_dispatch", (x, act, T * d), (pick_pos, torch.int32, T * shape.top_k),
-                   (xs, act, _expert_rows(shape, T) * d))
-    _check("moe_dispatch", _lib.moe_dispatch(ctypes.byref(shape), _ptr(x), T, _ptr(pick_pos), _ptr(xs),
-                                             _stream(stream)))
+    act, _, i32, _ = _dtypes(shape.act_dtype)
+    d, k = shape.d_model, shape.top_k
+    px, pp, pxs = _pointers("moe_dispatch", (x, act, T * d), (pick_pos, i32, T * k),
+                            (xs, act, T * (k + shape.n_shared) * d))
+    _check("moe_dispatch", _lib.moe_dispatch(ctypes.byref(shape), px, T, pp, pxs, _stream(stream)))
 
 
 def moe_dispatch_backward(shape, dxs, T: int, pick_pos, dx, stream=None):
-    import torch
-    act, d = _act(shape.act_dtype), shape.d_model
-    _check_tensors("moe_dispatch_backward", (dxs, act, _expert_rows(shape, T) * d),
-                   (pick_pos, torch.int32, T * shape.top_k), (dx, act, T * d))
-    _check("moe_dispatch_backward", _lib.moe_dispatch_backward(ctypes.byref(shape), _ptr(dxs), T, _ptr(pick_pos),
-                                                               _ptr(dx), _stream(stream)))
+    act, _, i32, _ = _dtypes(shape.act_dtype)
+    d, k = shape.d_model, shape.top_k
+    pdxs, pp, pdx = _pointers("moe_dispatch_backward", (dxs, act, T * (k + shape.n_shared) * d), (pick_pos, i32, T * k),
+                              (dx, act, T * d))
+    _check("moe_dispatch_backward", _lib.moe_dispatch_backward(ctypes.byref(shape), pdxs, T, pp, pdx, _stream(stream)))
 
 
 def moe_combine_backward(shape, dy, o, topk_w, pick_pos, T: int, d_o, d_w, stream=None):
-    import torch
-    f32, d, P, rows = torch.float32, shape.d_model, T * shape.top_k, _expert_rows(shape, T)
-    _check_tensors("moe_combine_backward", (dy, _act(shape.act_dtype), T * d), (o, f32, rows * d), (topk_w, f32, P),
-                   (pick_pos, torch.int32, P), (d_o, f32, rows * d), (d_w, f32, P))
-    _check("moe_combine_backward", _lib.moe_combine_backward(ctypes.byref(shape), _ptr(dy), _ptr(o), _ptr(topk_w),
-                                                             _ptr(pick_pos), T, _ptr(d_o), _ptr(d_w),
+    act, f32, i32, _ = _dtypes(shape.act_dtype)
+    d, P = shape.d_model, T * shape.top_k
+    n = (P + T * shape.n_shared) * d
+    pdy, po, pw, pp, pdo, pdw = _pointers("moe_combine_backward", (dy, act, T * d), (o, f32, n), (topk_w, f32, P),
+                                          (pick_pos, i32, P), (d_o, f32, n), (d_w, f32, P))
+    _check("moe_combine_backward", _lib.moe_combine_backward(ctypes.byref(shape), pdy, po, pw, pp, T, pdo, pdw,
                                                              _stream(stream)))
-
-
-def _gate_check(shape, T: int, gate, gate_kind: int):
-    import torch
-    token = gate_kind == MOE_GATE_TOKEN
-    return gate, torch.float32 if token else _act(shape.act_dtype), T if token else T * shape.d_model
 
 
 def moe_block_norm(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
                    eps: float, x_out, normed, stream=None):
-    import torch
-    f32, act, d = torch.float32, _act(shape.act_dtype), shape.d_model
+    act, f32, _, _ = _dtypes(shape.act_dtype)
+    d = shape.d_model
     n = T * d
-    _check_tensors("moe_block_norm", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
-                   _gate_check(shape, T, gate, gate_kind), (x_out, act, n), (normed, act, n))
-    _check("moe_block_norm", _lib.moe_block_norm(ctypes.byref(shape), _ptr(x), _ptr(y), T, _ptr(post_gamma),
-                                                 _ptr(pre_gamma), _ptr(gate), gate_kind, residual_scale, eps,
-                                                 _ptr(x_out), _ptr(normed), _stream(stream)))
+    px, py, ppost, ppre, pg, pxo, pn = _pointers(
+        "moe_block_norm", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
+        (gate, f32, T) if gate_kind == MOE_GATE_TOKEN else (gate, act, n), (x_out, act, n), (normed, act, n))
+    _check("moe_block_norm", _lib.moe_block_norm(ctypes.byref(shape), px, py, T, ppost, ppre, pg, gate_kind,
+                                                 residual_scale, eps, pxo, pn, _stream(stream)))
 
 
 def moe_combine_norm(shape, o, topk_w, pick_pos, x, T: int, post_gamma, pre_gamma, gate, gate_kind: int,
                      residual_scale: float, eps: float, x_out, normed, stream=None):
-    import torch
-    f32, act, d, P = torch.float32, _act(shape.act_dtype), shape.d_model, T * shape.top_k
+    act, f32, i32, _ = _dtypes(shape.act_dtype)
+    d, P = shape.d_model, T * shape.top_k
     n = T * d
-    _check_tensors("moe_combine_norm", (o, f32, _expert_rows(shape, T) * d), (topk_w, f32, P),
-                   (pick_pos, torch.int32, P), (x, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
-                   _gate_check(shape, T, gate, gate_kind), (x_out, act, n), (normed, act, n))
-    _check("moe_combine_norm", _lib.moe_combine_norm(ctypes.byref(shape), _ptr(o), _ptr(topk_w), _ptr(pick_pos),
-                                                     _ptr(x), T, _ptr(post_gamma), _ptr(pre_gamma), _ptr(gate),
-                                                     gate_kind, residual_scale, eps, _ptr(x_out), _ptr(normed),
-                                                     _stream(stream)))
+    po, pw, pp, px, ppost, ppre, pg, pxo, pn = _pointers(
+        "moe_combine_norm", (o, f32, (P + T * shape.n_shared) * d), (topk_w, f32, P), (pick_pos, i32, P), (x, act, n),
+        (post_gamma, f32, d), (pre_gamma, f32, d),
+        (gate, f32, T) if gate_kind == MOE_GATE_TOKEN else (gate, act, n), (x_out, act, n), (normed, act, n))
+    _check("moe_combine_norm", _lib.moe_combine_norm(ctypes.byref(shape), po, pw, pp, px, T, ppost, ppre, pg, gate_kind,
+                                                     residual_scale, eps, pxo, pn, _stream(stream)))
 
 
 def moe_block_norm_backward(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
                             eps: float, d_x_out, d_normed, dx, dy, d_gate, d_post_gamma, d_pre_gamma, ws,
                             ws_bytes=None, stream=None):
-    import torch
-    f32, act, d = torch.float32, _act(shape.act_dtype), shape.d_model
+    act, f32, _, u8 = _dtypes(shape.act_dtype)
+    d = shape.d_model
     n = T * d
-    _check_tensors("moe_block_norm_backward", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
-                   _gate_check(shape, T, gate, gate_kind), (d_x_out, act, n), (d_normed, act, n), (dx, act, n),
-                   (dy, act, n), _gate_check(shape, T, d_gate, gate_kind), (d_post_gamma, f32, d), (d_pre_gamma, f32, d))
-    ws_bytes = (0 if ws is None else _nbytes(ws)) if ws_bytes is None else ws_bytes
+    gate_type = (f32, T) if gate_kind == MOE_GATE_TOKEN else (act, n)
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else _nbytes(ws)
+    px, py, ppost, ppre, pg, pdxo, pdn, pdx, pdy, pdg, pdpost, pdpre, pws = _pointers(
+        "moe_block_norm_backward", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
+        (gate, *gate_type), (d_x_out, act, n), (d_normed, act, n), (dx, act, n), (dy, act, n), (d_gate, *gate_type),
+        (d_post_gamma, f32, d), (d_pre_gamma, f32, d), (ws, u8, ws_bytes))
     _check("moe_block_norm_backward", _lib.moe_block_norm_backward(
-        ctypes.byref(shape), _ptr(x), _ptr(y), T, _ptr(post_gamma), _ptr(pre_gamma), _ptr(gate), gate_kind,
-        residual_scale, eps, _ptr(d_x_out), _ptr(d_normed), _ptr(dx), _ptr(dy), _ptr(d_gate), _ptr(d_post_gamma),
-        _ptr(d_pre_gamma), _ptr(ws), ws_bytes, _stream(stream)))
+        ctypes.byref(shape), px, py, T, ppost, ppre, pg, gate_kind, residual_scale, eps, pdxo, pdn, pdx, pdy, pdg, pdpost,
+        pdpre, pws, ws_bytes, _stream(stream)))
 
 
 def make_matrix(rows: int, cols: int, wformat: int = MOE_WF_MXFP4, act_dtype: int = MOE_DT_BF16) -> moe_matrix:
@@ -381,10 +391,9 @@ def make_matrix(rows: int, cols: int, wformat: int = MOE_WF_MXFP4, act_dtype: in
 
 
 def moe_linear(matrix, q, s, tensor_scale: float, x, T: int, bias, y, stream=None):
-    import torch
-    act, N, K = _act(matrix.act_dtype), matrix.rows, matrix.cols
-    u8, block = torch.uint8, 32 if matrix.wformat == MOE_WF_MXFP4 else 16
-    _check_tensors("moe_linear", (q, u8, N * K // 2), (s, u8, N * K // block), (x, act, T * K),
-                   (bias, torch.float32, N), (y, act, T * N))
-    _check("moe_linear", _lib.moe_linear(ctypes.byref(matrix), _ptr(q), _ptr(s), tensor_scale, _ptr(x), T, _ptr(bias),
-                                         _ptr(y), _stream(stream)))
+    act, f32, _, u8 = _dtypes(matrix.act_dtype)
+    N, K = matrix.rows, matrix.cols
+    pq, ps, px, pb, py = _pointers("moe_linear", (q, u8, N * K // 2),
+                                   (s, u8, N * K // (32 if matrix.wformat == MOE_WF_MXFP4 else 16)), (x, act, T * K),
+                                   (bias, f32, N), (y, act, T * N))
+    _check("moe_linear", _lib.moe_linear(ctypes.byref(matrix), pq, ps, tensor_scale, px, T, pb, py, _stream(stream)))
