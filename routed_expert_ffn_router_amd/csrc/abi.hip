@@ -100,7 +100,7 @@ WsLayout ws_layout(const moe_shape* s, int32_t T, bool slots_for_any_shape) {
         L.stage_ranges = take(8 * ((E + kStageGroup - 1) / kStageGroup));
     }
     L.norm = L.sink;         // the norms' gradient partials, after the header and the hand-over slots
-    const size_t norm_end = L.norm + align256(8 * (size_t)norm_grad_groups(T) * d);
+    const size_t norm_end = L.norm + align256(8 * (size_t)norm_grad_groups(s, T) * d);
     L.total = o > norm_end ? o : norm_end;
     return L;
 }

@@ -246,39 +246,110 @@ __device__ __forceinline__ void store_act<float>(float* p, size_t i, float v) { 
 template <>
 __device__ __forceinline__ void store_act<uint16_t>(uint16_t* p, size_t i, float v) { p[i] = f32_to_bf16_bits(v); }
 
-// eight consecutive activations at a multiple of eight, as one or two 16-byte accesses (the
-// hardware's bf16 conversion rounds to nearest even and keeps NaN)
+// eight consecutive activations at a multiple of eight, as one or two 16-byte accesses (the hardware's
+// bf16 conversion rounds to nearest even and keeps NaN).  NT: a non-temporal access, for arrays that
+// are larger than the caches (kStreamBytes) and touched once.
 struct f32x8 {
     float v[8];
 };
+template <bool NT>
+__device__ __forceinline__ u32x4_t load16(const void* p) {
+    if constexpr (NT) return __builtin_nontemporal_load((const u32x4_t*)p);
+    else return *(const u32x4_t*)p;
+}
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, u32x4_t v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, (u32x4_t*)p);
+    else *(u32x4_t*)p = v;
+}
+// as loaded, until the values are wanted
 template <typename XT>
-__device__ __forceinline__ f32x8 load_act8(const XT* p, size_t i) {
-    f32x8 r;
-    if constexpr (sizeof(XT) == 4) {
-        const float4 a = *(const float4*)(p + i), b = *(const float4*)(p + i + 4);
-        r = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-    } else {
-        const uint4 u = *(const uint4*)(p + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw8 {
+    u32x4_t w[sizeof(XT) / 2];
+    __device__ __forceinline__ void clear() {
+        for (auto& q : w) q = u32x4_t{0, 0, 0, 0};
+    }
+    template <bool NT = false>
+    __device__ __forceinline__ void load(const XT* p, size_t i) {
+        w[0] = load16<NT>(p + i);
+        if constexpr (sizeof(XT) == 4) w[1] = load16<NT>(p + i + 4);
+    }
+    __device__ __forceinline__ f32x8 values() const {
+        f32x8 r;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            r.v[2 * j] = __uint_as_float(w[j] << 16);
-            r.v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            if constexpr (sizeof(XT) == 4) {
+                r.v[j] = __uint_as_float(w[0][j]);
+                r.v[4 + j] = __uint_as_float(w[1][j]);
+            } else {
+                r.v[2 * j] = __uint_as_float(w[0][j] << 16);
+                r.v[2 * j + 1] = __uint_as_float(w[0][j] & 0xffff0000u);
+            }
         }
+        return r;
     }
-    return r;
+};
+template <bool NT = false, typename XT>
+__device__ __forceinline__ f32x8 load_act8(const XT* p, size_t i) {
+    Raw8<XT> r;
+    r.template load<NT>(p, i);
+    return r.values();
 }
-template <typename XT>
+template <bool NT = false, typename XT>
 __device__ __forceinline__ void store_act8(XT* p, size_t i, const f32x8& r) {
+    u32x4_t w[sizeof(XT) / 2];
     if constexpr (sizeof(XT) == 4) {
-        *(float4*)(p + i) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-        *(float4*)(p + i + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j / 4][j % 4] = __float_as_uint(r.v[j]);
+        store16<NT>(p + i + 4, w[1]);
     } else {
         typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
         bf16x8 b;
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[j] = (__bf16)r.v[j];
-        *(bf16x8*)(p + i) = b;
+        __builtin_memcpy(&w[0], &b, 16);
+    }
+    store16<NT>(p + i, w[0]);
+}
+// Bytes of an expert-side array from which its rows go past the caches: the last-level cache's size.  Below
+// it the next kernel finds them there (82 MB of rows read past the caches: 19.8 us instead of 14.6); above
+// it 4096 tokens' dispatch took 53.5 us instead of 61.8 and its gradient 50.4 instead of 59.6 (d 4096,
+// 8 picks, bf16).
+constexpr size_t kStreamBytes = (size_t)256 << 20;
+
+// Workgroups go to the eight XCDs in turn, so work that repeats every eight jobs (tokens that keep as many
+// picks as the eighth before them) would load one XCD more than another: the jobs of each group of
+// eight are rotated by their group.  (Tokens keeping 1, 8, 7, .. picks in turn: 1001 tokens' combine and norm
+// at d 6144, fp32: 43.0 us, in plain order 44.8.)
+__device__ __forceinline__ size_t xcd_rotate(size_t job, size_t jobs) {
+    const size_t group = job >> 3;
+    return (group + 1) * 8 <= jobs ? group * 8 + ((job + group) & 7) : job;
+}
+
+// A token's picks in rank order, in groups whose rows are loaded together: f(N, row, has, j0) with N = MAXN
+// (8 or 4), half or a quarter of it (at least 2) picks j0 .. j0 + N - 1 (a StepPos).  pos: the token's k
+// positions, the same in every lane of the wave; positions outside [0, P) have no row.  Dropped picks are
+// the last ranks, so the groups end with the last pick that has one; a pick without a row inside a group
+// (has false) stands on another pick's row, which it reads from the cache and must not use.
+template <int MAXN, typename F>
+__device__ __forceinline__ void for_picks(const int32_t* __restrict__ pos, int k, int P, F&& f) {
+    for (int j0 = 0; j0 < k; j0 += MAXN) {
+        int row[MAXN], last = -1, any = 0;
+        bool has[MAXN];
+#pragma unroll
+        for (int i = 0; i < MAXN; ++i) {
+            row[i] = __builtin_amdgcn_readfirstlane(pos[j0 + i < k ? j0 + i : k - 1]);
+            has[i] = j0 + i < k && (unsigned)row[i] < (unsigned)P;
+            if (has[i]) {
+                last = i;
+                any = row[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MAXN; ++i) row[i] = has[i] ? row[i] : any;
+        if (MAXN > 4 && last >= 4) f(StepPos<MAXN>{}, row, has, j0);
+        else if (last >= 2) f(StepPos<4>{}, row, has, j0);
+        else if (last >= 0) f(StepPos<2>{}, row, has, j0);
     }
 }
 
@@ -616,9 +687,9 @@ struct NormGradArgs {
     void* d_gate;
     float* d_post;
     float* d_pre;
-    float* part;              // [norm_grad_groups(T)][2][d] in the workspace
+    float* part;              // [groups][2][d] in the workspace
 };
-int norm_grad_groups(int T);  // groups of rows whose parameter gradients are summed apart
+int norm_grad_groups(const moe_shape* s, int T);  // groups of rows whose parameter gradients are summed apart
 hipError_t launch_block_norm_backward(const moe_shape* s, const NormArgs& a, const NormGradArgs& g, hipStream_t st);
 
 constexpr int kLinearMaxT = 64;

@@ -37,31 +37,30 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
 }
 
 // the combine's sum for columns c .. c + 7 of token t, in k_combine's order
+template <int MAXN, bool NT>
 __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
     const int P = a.T * a.k;
     f32x8 acc = {};
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-        int row[8];
-        float wj[8];
-        f32x8 v[8];
+    for_picks<MAXN>(a.pick_pos + (size_t)t * a.k, a.k, P, [&](auto n, const int (&row)[MAXN], const bool (&has)[MAXN], int j0) {
+        constexpr int N = decltype(n)::value;
+        Raw8<float> v[N];
+        float w[N];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const size_t p = (size_t)t * a.k + j0 + i;
-            row[i] = j0 + i < a.k ? a.pick_pos[p] : -1;
-            wj[i] = j0 + i < a.k ? a.w[p] : 0.0f;
-            if ((unsigned)row[i] >= (unsigned)P) row[i] = -1;
+        for (int i = 0; i < N; ++i) {
+            v[i].template load<NT>(a.o, (size_t)row[i] * a.d + c);
+            w[i] = a.w[(size_t)t * a.k + (j0 + i < a.k ? j0 + i : j0)];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = load_act8(a.o, (size_t)(row[i] >= 0 ? row[i] : 0) * a.d + c);
+        for (int i = 0; i < N; ++i) {
+            const f32x8 o = v[i].values();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc.v[e] = row[i] >= 0 ? fmaf(wj[i], v[i].v[e], acc.v[e]) : acc.v[e];
-    }
+            for (int e = 0; e < 8; ++e) acc.v[e] = has[i] ? fmaf(w[i], o.v[e], acc.v[e]) : acc.v[e];
+        }
+    });
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc.v[e] *= a.scaling;
     if (a.shared) {
-        const f32x8 v = load_act8(a.o, ((size_t)P + t) * a.d + c);
+        const f32x8 v = load_act8<NT>(a.o, ((size_t)P + t) * a.d + c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc.v[e] += v.v[e];
     }
@@ -69,26 +68,33 @@ __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
 }
 
 // One row per workgroup; thread i holds columns 8 (i + n blockDim) .. + 7 for n < VPT.
-template <typename XT, int VPT, bool COMBINE>
+// COMBINE: 0, or the picks whose rows are loaded together.  LATE: the gate and the gammas are loaded when
+// they are used, which saves registers for more rows per CU; else with the row, before the first sum waits.
+template <typename XT, int VPT, int COMBINE, bool LATE, bool NT>
 __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
     __shared__ float s_post[16], s_pre[16];
-    const int t = blockIdx.x;
+    const int t = COMBINE ? (int)xcd_rotate(blockIdx.x, a.T) : blockIdx.x;
     const size_t base = (size_t)t * a.d;
-    const bool has_y = COMBINE || a.y;
-    f32x8 u[VPT], z[VPT], gate[VPT], post[VPT], pre[VPT];
+    const bool has_y = COMBINE || a.y, element = a.gate_kind == MOE_GATE_ELEMENT;
+    auto col = [&](int n) { return 8 * (int)(threadIdx.x + n * blockDim.x); };
+    f32x8 u[VPT], z[VPT], pre[VPT], post[VPT];
+    Raw8<XT> gate[VPT];
+    auto load_after = [&](int n) {            // what multiplies z
+        if (element) gate[n].template load<NT>((const XT*)a.gate, base + col(n));
+        if (a.post) post[n] = load_act8(a.post, (size_t)col(n));
+    };
     float sum[1] = {0.0f};
-    // every load of the row is requested before the first sum waits
 #pragma unroll
     for (int n = 0; n < VPT; ++n) {
-        const int c = 8 * (threadIdx.x + n * blockDim.x);
-        u[n] = z[n] = gate[n] = post[n] = pre[n] = f32x8{};
-        if (c >= a.d) continue;
-        u[n] = load_act8((const XT*)a.x, base + c);
-        if (a.gate_kind == MOE_GATE_ELEMENT) gate[n] = load_act8((const XT*)a.gate, base + c);
-        if (a.post) post[n] = load_act8(a.post, (size_t)c);
-        if (a.pre) pre[n] = load_act8(a.pre, (size_t)c);
-        if constexpr (COMBINE) z[n] = combine8(a, t, c);
-        else if (has_y) z[n] = load_act8((const XT*)a.y, base + c);
+        u[n] = z[n] = f32x8{};
+        if (col(n) >= a.d) continue;
+        u[n] = load_act8<NT>((const XT*)a.x, base + col(n));
+        if constexpr (!LATE) {
+            load_after(n);
+            if (a.pre) pre[n] = load_act8(a.pre, (size_t)col(n));
+        }
+        if constexpr (COMBINE > 0) z[n] = combine8<COMBINE, NT>(a, t, col(n));
+        else if (has_y) z[n] = load_act8<NT>((const XT*)a.y, base + col(n));
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[0] = fmaf(z[n].v[e], z[n].v[e], sum[0]);
     }
@@ -101,15 +107,16 @@ __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
         const float gt = a.alpha * (a.gate_kind == MOE_GATE_TOKEN ? ((const float*)a.gate)[t] : 1.0f);
 #pragma unroll
         for (int n = 0; n < VPT; ++n) {
-            const int c = 8 * (threadIdx.x + n * blockDim.x);
-            if (c >= a.d) continue;
+            if (col(n) >= a.d) continue;
+            if constexpr (LATE) load_after(n);
             if (a.post) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[n].v[e] *= r * post[n].v[e];
             }
-            if (a.gate_kind == MOE_GATE_ELEMENT) {
+            if (element) {
+                const f32x8 g = gate[n].values();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[n].v[e] *= gate[n].v[e];
+                for (int e = 0; e < 8; ++e) z[n].v[e] *= g.v[e];
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[n].v[e] = fmaf(gt, z[n].v[e], u[n].v[e]);
@@ -118,9 +125,8 @@ __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
     sum[0] = 0.0f;
 #pragma unroll
     for (int n = 0; n < VPT; ++n) {
-        const int c = 8 * (threadIdx.x + n * blockDim.x);
-        if (c >= a.d) continue;
-        if (a.x_out) store_act8((XT*)a.x_out, base + c, u[n]);
+        if (col(n) >= a.d) continue;
+        if (a.x_out) store_act8<NT>((XT*)a.x_out, base + col(n), u[n]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[0] = fmaf(u[n].v[e], u[n].v[e], sum[0]);
     }
@@ -129,13 +135,16 @@ __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
     const float r = inv_rms(sum[0], a.d, a.eps);
 #pragma unroll
     for (int n = 0; n < VPT; ++n) {
-        const int c = 8 * (threadIdx.x + n * blockDim.x);
-        if (c >= a.d) continue;
+        if (col(n) >= a.d) continue;
+        if constexpr (LATE) pre[n] = load_act8(a.pre, (size_t)col(n));
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[n].v[e] *= r * pre[n].v[e];
-        store_act8((XT*)a.normed, base + c, u[n]);
+        store_act8<NT>((XT*)a.normed, base + col(n), u[n]);
     }
 }
+
+// bytes of one row array from which its rows go past the caches (the eight L2s together)
+constexpr size_t kStreamRows = (size_t)32 << 20;
 
 // threads of a workgroup for rows of d columns, eight per thread and vector
 static int norm_threads(int d, int* vpt) {
@@ -145,20 +154,32 @@ static int norm_threads(int d, int* vpt) {
     return (per + 63) / 64 * 64;
 }
 
-template <typename XT, int VPT>
-static void norm_launch(const NormArgs& a, int threads, hipStream_t st) {
-    if (a.o) MOE_LAUNCH((k_block_norm<XT, VPT, true>), dim3(a.T), dim3(threads), 0, st, a);
-    else MOE_LAUNCH((k_block_norm<XT, VPT, false>), dim3(a.T), dim3(threads), 0, st, a);
+template <typename XT>
+static void norm_launch(const NormArgs& a, hipStream_t st) {
+    int vpt;
+    const dim3 grid(a.T), block(norm_threads(a.d, &vpt));
+    // the combine: with more rows than CUs, four picks at a time and late loads; past the caches once
+    // its rows are larger than they are
+    const bool many = a.T > 256 || vpt == 2, nt = 4 * (size_t)a.T * a.d * (a.k + a.shared) >= kStreamBytes;
+    if (a.o) {
+        if (vpt == 2) MOE_LAUNCH((k_block_norm<XT, 2, 4, true, false>), grid, block, 0, st, a);
+        else if (many && nt) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, true>), grid, block, 0, st, a);
+        else if (many) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, false>), grid, block, 0, st, a);
+        else MOE_LAUNCH((k_block_norm<XT, 1, 8, false, false>), grid, block, 0, st, a);
+    } else if (vpt == 2) {
+        MOE_LAUNCH((k_block_norm<XT, 2, 0, true, false>), grid, block, 0, st, a);
+    } else if ((size_t)a.T * a.d * sizeof(XT) >= kStreamRows) {
+        MOE_LAUNCH((k_block_norm<XT, 1, 0, false, true>), grid, block, 0, st, a);
+    } else {
+        MOE_LAUNCH((k_block_norm<XT, 1, 0, false, false>), grid, block, 0, st, a);
+    }
 }
 
 hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t st) {
     const char* name = a.o ? "combine_norm" : "block_norm";
     trace(name, 0, st);
-    int vpt;
-    const int threads = norm_threads(a.d, &vpt);
-    const bool bf = s->act_dtype == MOE_DT_BF16;
-    if (vpt == 1) bf ? norm_launch<uint16_t, 1>(a, threads, st) : norm_launch<float, 1>(a, threads, st);
-    else bf ? norm_launch<uint16_t, 2>(a, threads, st) : norm_launch<float, 2>(a, threads, st);
+    if (s->act_dtype == MOE_DT_BF16) norm_launch<uint16_t>(a, st);
+    else norm_launch<float>(a, st);
     trace(name, 1, st);
     return hipGetLastError();
 }
@@ -169,57 +190,142 @@ hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t 
 //   dz = a gate du;   d_gate = a du z (its row sum for a gate per token);   d_post = sum_t dz yn;
 //   dy = r(y) (dz post - yn mean(dz post yn)),  or dz without a post-norm.
 // A workgroup takes rows b, b + G, ... (G workgroups) and keeps its columns' sums of d_post and d_pre
-// in registers; k_norm_grad_sums adds the workgroups' sums in order.
+// itself; k_norm_grad_sums adds the workgroups' sums in order.
 // ---------------------------------------------------------------------------------------------
-constexpr int kNormGroups = 512;
+// Groups: a row's chain of three sums takes about 2 us, so a CU needs some 64 KB of rows at once to keep its
+// share of HBM busy: one workgroup per CU for long rows, up to eight for short ones.  More only add partial sums
+// to write and read (4096 rows, 256 / 512 groups: d 4096 bf16 55 / 60 us, d 1024 41 / 28).  Up to four
+// rows one workgroup takes them all and no second kernel runs.
+int norm_grad_groups(const moe_shape* s, int T) {
+    if (T <= 4) return 1;
+    const int row = 8 * s->d_model * (s->act_dtype == MOE_DT_BF16 ? 2 : 4);       // bytes of a row, in and out
+    const int per_cu = row >= 65536 ? 1 : 65536 / row < 8 ? (65536 + row - 1) / row : 8;
+    const int rows = (T + 256 * per_cu - 1) / (256 * per_cu);
+    return (T + rows - 1) / rows;
+}
 
-int norm_grad_groups(int T) { return T < kNormGroups ? T : kNormGroups; }
-
+// One row's loads, as they come: requested for the next row while this one is worked on
 template <typename XT, int VPT>
-__global__ __launch_bounds__(1024) void k_block_norm_backward(NormArgs a, NormGradArgs g) {
+struct NormRow {
+    Raw8<XT> x[VPT], y[VPT], du[VPT], dn[VPT], gate[VPT];
+};
+
+template <typename XT, int VPT, int THREADS, bool NT>
+__global__ __launch_bounds__(THREADS, 4) void k_block_norm_backward(NormArgs a, NormGradArgs g) {
+    constexpr bool AHEAD = VPT == 1;          // (two vectors per thread leave no registers for the next row)
     // two sets, for odd and even rows: with one sum a row, a wave may still read the last row's
     __shared__ float s_y[2][16], s_u[2][32], s_d[2][32];
-    int odd = 0;
-    f32x8 acc_post[VPT], acc_pre[VPT];
+    const bool element = a.gate_kind == MOE_GATE_ELEMENT, token = a.gate_kind == MOE_GATE_TOKEN;
+    auto col = [&](int n) { return 8 * (int)(threadIdx.x + n * blockDim.x); };
+    auto load_row = [&](int t, NormRow<XT, VPT>& r) {
+        const size_t base = (size_t)t * a.d;
 #pragma unroll
-    for (int n = 0; n < VPT; ++n) acc_post[n] = acc_pre[n] = f32x8{};
+        for (int n = 0; n < VPT; ++n) {
+            r.x[n].clear();
+            r.y[n].clear();
+            r.du[n].clear();
+            r.dn[n].clear();
+            r.gate[n].clear();
+            if (col(n) >= a.d) continue;
+            const size_t i = base + col(n);
+            r.x[n].template load<NT>((const XT*)a.x, i);
+            if (a.y) r.y[n].template load<NT>((const XT*)a.y, i);
+            if (g.d_x_out) r.du[n].template load<NT>((const XT*)g.d_x_out, i);
+            if (g.d_normed) r.dn[n].template load<NT>((const XT*)g.d_normed, i);
+            if (element) r.gate[n].template load<NT>((const XT*)a.gate, i);
+        }
+    };
+    auto gamma = [&](const float* p, int n) {
+        f32x8 r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.v[e] = 1.0f;
+        if (p && col(n) < a.d) r = load_act8(p, (size_t)col(n));
+        return r;
+    };
+    // LDS that only its own thread reads and writes: the gammas of its columns, or, with two vectors per
+    // thread, their sums (the sums of one vector stay in registers)
+    __shared__ float s_own[2][8 * THREADS * VPT];
+    auto own = [&](int w, int n) { return &s_own[w][8 * (threadIdx.x + n * THREADS)]; };
+    auto get = [&](int w, int n) {
+        const float4 p = *(const float4*)own(w, n), q = *(const float4*)(own(w, n) + 4);
+        return f32x8{{p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}};
+    };
+    auto put = [&](int w, int n, const f32x8& r) {
+        *(float4*)own(w, n) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+        *(float4*)(own(w, n) + 4) = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
+    };
+    auto post_of = [&](int n) { return VPT == 1 ? get(0, n) : gamma(a.post, n); };
+    auto pre_of = [&](int n) { return VPT == 1 ? get(1, n) : gamma(a.pre, n); };
+    f32x8 acc_post = {}, acc_pre = {};
+    if constexpr (VPT == 1) {
+        put(0, 0, gamma(a.post, 0));
+        put(1, 0, gamma(a.pre, 0));
+    } else {
+#pragma unroll
+        for (int n = 0; n < VPT; ++n) {
+            put(0, n, f32x8{});
+            put(1, n, f32x8{});
+        }
+    }
+    auto add_post = [&](int n, const f32x8& p, const f32x8& q) {          // sums += p q
+        f32x8 s = VPT == 1 ? acc_post : get(0, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s.v[e] = fmaf(p.v[e], q.v[e], s.v[e]);
+        if constexpr (VPT == 1) acc_post = s;
+        else put(0, n, s);
+    };
+    auto add_pre = [&](int n, const f32x8& p, const f32x8& q) {
+        f32x8 s = VPT == 1 ? acc_pre : get(1, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s.v[e] = fmaf(p.v[e], q.v[e], s.v[e]);
+        if constexpr (VPT == 1) acc_pre = s;
+        else put(1, n, s);
+    };
+    NormRow<XT, VPT> row;
+    if (AHEAD) load_row(blockIdx.x, row);
+    int odd = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, odd ^= 1) {
         const size_t base = (size_t)t * a.d;
-        f32x8 x[VPT], y[VPT], du[VPT], dn[VPT], gate[VPT], pre[VPT], post[VPT];
+        if (!AHEAD) load_row(t, row);
+        f32x8 x[VPT], y[VPT], du[VPT], dn[VPT];
+        Raw8<XT> gate_raw[VPT];
+        const float gt = a.alpha * (token ? ((const float*)a.gate)[t] : 1.0f);
         float sy[1] = {0.0f};
 #pragma unroll
         for (int n = 0; n < VPT; ++n) {
-            const int c = 8 * (threadIdx.x + n * blockDim.x);
-            x[n] = y[n] = du[n] = dn[n] = gate[n] = pre[n] = post[n] = f32x8{};
-            if (c >= a.d) continue;
-            x[n] = load_act8((const XT*)a.x, base + c);
-            if (a.y) y[n] = load_act8((const XT*)a.y, base + c);
-            if (g.d_x_out) du[n] = load_act8((const XT*)g.d_x_out, base + c);
-            if (g.d_normed) dn[n] = load_act8((const XT*)g.d_normed, base + c);
-            if (a.gate_kind == MOE_GATE_ELEMENT) gate[n] = load_act8((const XT*)a.gate, base + c);
-            if (a.pre) pre[n] = load_act8(a.pre, (size_t)c);
-            if (a.post) post[n] = load_act8(a.post, (size_t)c);
+            x[n] = row.x[n].values();
+            y[n] = row.y[n].values();
+            du[n] = row.du[n].values();
+            dn[n] = row.dn[n].values();
+            gate_raw[n] = row.gate[n];
 #pragma unroll
             for (int e = 0; e < 8; ++e) sy[0] = fmaf(y[n].v[e], y[n].v[e], sy[0]);
         }
-        const float gt = a.gate_kind == MOE_GATE_TOKEN ? ((const float*)a.gate)[t] : 1.0f;
+        if (AHEAD && t + (int)gridDim.x < a.T) load_row(t + gridDim.x, row);
+        // a gate of column vector n
+        auto gate_of = [&](int n) {
+            f32x8 r = gate_raw[n].values();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.v[e] = element ? a.alpha * r.v[e] : gt;
+            return r;
+        };
         float ry = 1.0f;
         if (a.post) {
             block_sums(sy, s_y[odd]);
             ry = inv_rms(sy[0], a.d, a.eps);
         }
-        // y becomes yn (or stays y), x becomes u, gate becomes a gate
+        // y becomes yn (or stays y), x becomes u, dn becomes gn
         float su[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < VPT; ++n) {
+            const f32x8 post = post_of(n), pre = pre_of(n);
+            const f32x8 ag = gate_of(n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 y[n].v[e] *= ry;
-                if (!a.post) post[n].v[e] = 1.0f;
-                gate[n].v[e] = a.alpha * (a.gate_kind == MOE_GATE_ELEMENT ? gate[n].v[e] : gt);
-                x[n].v[e] = fmaf(gate[n].v[e], y[n].v[e] * post[n].v[e], x[n].v[e]);
+                x[n].v[e] = fmaf(ag.v[e], y[n].v[e] * post.v[e], x[n].v[e]);
                 su[0] = fmaf(x[n].v[e], x[n].v[e], su[0]);
-                su[1] = fmaf(dn[n].v[e] * pre[n].v[e], x[n].v[e], su[1]);
+                su[1] = fmaf(dn[n].v[e] * pre.v[e], x[n].v[e], su[1]);
             }
         }
         if (g.d_normed) {
@@ -227,85 +333,96 @@ __global__ __launch_bounds__(1024) void k_block_norm_backward(NormArgs a, NormGr
             const float ru = inv_rms(su[0], a.d, a.eps);
             const float q = su[1] * ru / (float)a.d;
 #pragma unroll
-            for (int n = 0; n < VPT; ++n)
+            for (int n = 0; n < VPT; ++n) {
+                const f32x8 pre = pre_of(n);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float un = x[n].v[e] * ru;
-                    acc_pre[n].v[e] = fmaf(dn[n].v[e], un, acc_pre[n].v[e]);
-                    du[n].v[e] = fmaf(ru, fmaf(-un, q, dn[n].v[e] * pre[n].v[e]), du[n].v[e]);
-                }
+                for (int e = 0; e < 8; ++e) x[n].v[e] *= ru;                 // un
+                add_pre(n, dn[n], x[n]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    du[n].v[e] = fmaf(ru, fmaf(-x[n].v[e], q, dn[n].v[e] * pre.v[e]), du[n].v[e]);
+            }
         }
         // dn becomes dz post; sums of dz post yn and of du z
         float sd[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int n = 0; n < VPT; ++n) {
-            const int c = 8 * (threadIdx.x + n * blockDim.x);
+            const f32x8 post = post_of(n), ag = gate_of(n);
+            f32x8 dg, dz;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dz.v[e] = ag.v[e] * du[n].v[e];
+            add_post(n, dz, y[n]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float dz = gate[n].v[e] * du[n].v[e];
-                acc_post[n].v[e] = fmaf(dz, y[n].v[e], acc_post[n].v[e]);
-                dn[n].v[e] = dz * post[n].v[e];
+                dn[n].v[e] = dz.v[e] * post.v[e];
                 sd[0] = fmaf(dn[n].v[e], y[n].v[e], sd[0]);
-                gate[n].v[e] = du[n].v[e] * (y[n].v[e] * post[n].v[e]);
-                sd[1] += gate[n].v[e];
+                dg.v[e] = du[n].v[e] * (y[n].v[e] * post.v[e]);
+                sd[1] += dg.v[e];
             }
-            if (c >= a.d) continue;
-            if (g.dx) store_act8((XT*)g.dx, base + c, du[n]);
-            if (g.d_gate && a.gate_kind == MOE_GATE_ELEMENT) {
+            if (col(n) >= a.d) continue;
+            if (g.dx) store_act8<NT>((XT*)g.dx, base + col(n), du[n]);
+            if (g.d_gate && element) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) gate[n].v[e] *= a.alpha;
-                store_act8((XT*)g.d_gate, base + c, gate[n]);
+                for (int e = 0; e < 8; ++e) dg.v[e] *= a.alpha;
+                store_act8<NT>((XT*)g.d_gate, base + col(n), dg);
             }
         }
         if (!a.y) continue;
         float m = 0.0f;
-        if (a.post || (g.d_gate && a.gate_kind == MOE_GATE_TOKEN)) {
+        if (a.post || (g.d_gate && token)) {
             block_sums(sd, s_d[odd]);
             m = a.post ? sd[0] / (float)a.d : 0.0f;
-            if (g.d_gate && a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) ((float*)g.d_gate)[t] = a.alpha * sd[1];
+            if (g.d_gate && token && threadIdx.x == 0) ((float*)g.d_gate)[t] = a.alpha * sd[1];
         }
         if (!g.dy) continue;
 #pragma unroll
         for (int n = 0; n < VPT; ++n) {
-            const int c = 8 * (threadIdx.x + n * blockDim.x);
-            if (c >= a.d) continue;
+            if (col(n) >= a.d) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) dn[n].v[e] = ry * fmaf(-y[n].v[e], m, dn[n].v[e]);
-            store_act8((XT*)g.dy, base + c, dn[n]);
+            store_act8<NT>((XT*)g.dy, base + col(n), dn[n]);
         }
     }
     if (!g.d_post && !g.d_pre) return;
+    // one group's sums are the gradients; the others' go to the workspace
     float* part = g.part + (size_t)blockIdx.x * 2 * a.d;
+    float* post_out = gridDim.x == 1 ? g.d_post : part;
+    float* pre_out = gridDim.x == 1 ? g.d_pre : part + a.d;
 #pragma unroll
     for (int n = 0; n < VPT; ++n) {
-        const int c = 8 * (threadIdx.x + n * blockDim.x);
-        if (c >= a.d) continue;
-        if (g.d_post) store_act8(part, (size_t)c, acc_post[n]);
-        if (g.d_pre) store_act8(part, (size_t)a.d + c, acc_pre[n]);
+        if (col(n) >= a.d) continue;
+        if (g.d_post) store_act8(post_out, (size_t)col(n), VPT == 1 ? acc_post : get(0, n));
+        if (g.d_pre) store_act8(pre_out, (size_t)col(n), VPT == 1 ? acc_pre : get(1, n));
     }
 }
 
-// d_post and d_pre from the groups' sums: a workgroup adds 64 columns (four per thread), sixteen
-// threads each a sixteenth of the groups, and then those sixteen sums, in order
+// d_post and d_pre from the groups' sums: a workgroup adds 32 columns (four per thread), 32 threads each
+// every 32nd group, eight loads in flight, and then those 32 sums, in order
 __global__ __launch_bounds__(256) void k_norm_grad_sums(const float* __restrict__ part, int groups, int d,
                                                         float* __restrict__ d_post, float* __restrict__ d_pre) {
-    __shared__ float4 s_sum[16][16];
-    const int col = (threadIdx.x & 15) * 4 + blockIdx.x * 64;         // of the 2 d columns; d % 64 = 0
-    const int q = threadIdx.x >> 4;
-    float* out = blockIdx.x * 64 < (unsigned)d ? d_post : d_pre;
+    __shared__ float4 s_sum[32][8];
+    const int col = (threadIdx.x & 7) * 4 + blockIdx.x * 32;          // of the 2 d columns; d % 32 = 0
+    const int q = threadIdx.x >> 3;
+    float* out = blockIdx.x * 32 < (unsigned)d ? d_post : d_pre;
     if (!out) return;                                                  // uniform
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = q; b < groups; b += 16) {
-        const float4 v = *(const float4*)(part + (size_t)b * 2 * d + col);
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+    for (int b0 = q; b0 < groups; b0 += 256) {
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = *(const float4*)(part + (size_t)(b0 + 32 * i < groups ? b0 + 32 * i : q) * 2 * d + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool in = b0 + 32 * i < groups;
+            s.x += in ? v[i].x : 0.0f;
+            s.y += in ? v[i].y : 0.0f;
+            s.z += in ? v[i].z : 0.0f;
+            s.w += in ? v[i].w : 0.0f;
+        }
     }
-    s_sum[q][threadIdx.x & 15] = s;
+    s_sum[q][threadIdx.x & 7] = s;
     __syncthreads();
     if (q) return;
-    for (int i = 1; i < 16; ++i) {
+    for (int i = 1; i < 32; ++i) {
         const float4 v = s_sum[i][threadIdx.x];
         s.x += v.x;
         s.y += v.y;
@@ -316,23 +433,28 @@ __global__ __launch_bounds__(256) void k_norm_grad_sums(const float* __restrict_
 }
 
 template <typename XT>
-static void norm_backward_launch(const NormArgs& a, const NormGradArgs& g, int vpt, int threads, hipStream_t st) {
-    const dim3 grid(norm_grad_groups(a.T));
-    if (vpt == 1) MOE_LAUNCH((k_block_norm_backward<XT, 1>), grid, dim3(threads), 0, st, a, g);
-    else MOE_LAUNCH((k_block_norm_backward<XT, 2>), grid, dim3(threads), 0, st, a, g);
+static void norm_backward_launch(const NormArgs& a, const NormGradArgs& g, int groups, hipStream_t st) {
+    int vpt;
+    const int threads = norm_threads(a.d, &vpt);
+    const dim3 grid(groups);
+    const bool nt = (size_t)a.T * a.d * sizeof(XT) >= kStreamRows;
+    if (vpt == 2) MOE_LAUNCH((k_block_norm_backward<XT, 2, 1024, false>), grid, dim3(threads), 0, st, a, g);
+    else if (threads > 512 && nt) MOE_LAUNCH((k_block_norm_backward<XT, 1, 1024, true>), grid, dim3(threads), 0, st, a, g);
+    else if (threads > 512) MOE_LAUNCH((k_block_norm_backward<XT, 1, 1024, false>), grid, dim3(threads), 0, st, a, g);
+    else if (nt) MOE_LAUNCH((k_block_norm_backward<XT, 1, 512, true>), grid, dim3(threads), 0, st, a, g);
+    else MOE_LAUNCH((k_block_norm_backward<XT, 1, 512, false>), grid, dim3(threads), 0, st, a, g);
 }
 
 hipError_t launch_block_norm_backward(const moe_shape* s, const NormArgs& a, const NormGradArgs& g, hipStream_t st) {
     trace("block_norm_backward", 0, st);
-    int vpt;
-    const int threads = norm_threads(a.d, &vpt);
-    if (a.T > 0) {
-        if (s->act_dtype == MOE_DT_BF16) norm_backward_launch<uint16_t>(a, g, vpt, threads, st);
-        else norm_backward_launch<float>(a, g, vpt, threads, st);
+    const int groups = a.T > 0 ? norm_grad_groups(s, a.T) : 0;
+    if (groups > 0) {
+        if (s->act_dtype == MOE_DT_BF16) norm_backward_launch<uint16_t>(a, g, groups, st);
+        else norm_backward_launch<float>(a, g, groups, st);
     }
-    if (g.d_post || g.d_pre)
-        MOE_LAUNCH(k_norm_grad_sums, dim3(2 * a.d / 64), dim3(256), 0, st, (const float*)g.part, norm_grad_groups(a.T),
-                   a.d, g.d_post, g.d_pre);
+    if ((g.d_post || g.d_pre) && groups != 1)
+        MOE_LAUNCH(k_norm_grad_sums, dim3(2 * a.d / 32), dim3(256), 0, st, (const float*)g.part, groups, a.d, g.d_post,
+                   g.d_pre);
     trace("block_norm_backward", 1, st);
     return hipGetLastError();
 }
