@@ -371,16 +371,17 @@ def moe_combine_norm(shape, o, topk_w, pick_pos, x, T: int, post_gamma, pre_gamm
 def moe_block_norm_backward(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
                             eps: float, d_x_out, d_normed, dx, dy, d_gate, d_post_gamma, d_pre_gamma, ws,
                             ws_bytes=None, stream=None):
-    act, f32, _, u8 = _dtypes(shape.act_dtype)
+    act, f32, _, _ = _dtypes(shape.act_dtype)
     d = shape.d_model
     n = T * d
     gate_type = (f32, T) if gate_kind == MOE_GATE_TOKEN else (act, n)
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else _nbytes(ws)
+    scratch = (ws, None, 0) if ws is None or isinstance(ws, int) else (ws, ws.dtype, -(-ws_bytes // ws.element_size()))
     px, py, ppost, ppre, pg, pdxo, pdn, pdx, pdy, pdg, pdpost, pdpre, pws = _pointers(
         "moe_block_norm_backward", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
         (gate, *gate_type), (d_x_out, act, n), (d_normed, act, n), (dx, act, n), (dy, act, n), (d_gate, *gate_type),
-        (d_post_gamma, f32, d), (d_pre_gamma, f32, d), (ws, u8, ws_bytes))
+        (d_post_gamma, f32, d), (d_pre_gamma, f32, d), scratch)
     _check("moe_block_norm_backward", _lib.moe_block_norm_backward(
         ctypes.byref(shape), px, py, T, ppost, ppre, pg, gate_kind, residual_scale, eps, pdxo, pdn, pdx, pdy, pdg, pdpost,
         pdpre, pws, ws_bytes, _stream(stream)))

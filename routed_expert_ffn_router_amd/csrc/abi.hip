@@ -100,8 +100,8 @@ WsLayout ws_layout(const moe_shape* s, int32_t T, bool slots_for_any_shape) {
         L.stage_ranges = take(8 * ((E + kStageGroup - 1) / kStageGroup));
     }
     L.norm = L.sink;         // the norms' gradient partials, after the header and the hand-over slots
-    const size_t norm_end = L.norm + align256(8 * (size_t)norm_grad_groups(s, T) * d);
-    L.total = o > norm_end ? o : norm_end;
+    L.norm_end = L.norm + align256(8 * (size_t)norm_grad_groups(s, T) * d);
+    L.total = o;
     return L;
 }
 
@@ -355,7 +355,8 @@ size_t moe_blob_stride(const moe_shape* s) {
 
 size_t moe_workspace_bytes(const moe_shape* s, int32_t T) {
     if (check_shape(s) != MOE_OK || check_T(s, T) != MOE_OK) return 0;
-    return ws_layout(s, T).total;
+    const WsLayout L = ws_layout(s, T);
+    return L.total > L.norm_end ? L.total : L.norm_end;
 }
 
 moe_status moe_workspace_init(const moe_shape* s, int32_t T, void* ws, size_t ws_bytes, int32_t poll_limit,
@@ -555,7 +556,7 @@ moe_status moe_block_norm_backward(const moe_shape* s, const void* x, const void
         if ((dy && !y) || (d_gate && !gate) || (d_post_gamma && !post_gamma)) return MOE_ERR_INVALID;
         if (!y && (post_gamma || gate)) return MOE_ERR_INVALID;
         const WsLayout L = ws_layout(s, T);
-        if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+        if (ws_bytes < L.norm_end) return MOE_ERR_WORKSPACE;
         g.part = (float*)((uint8_t*)ws + L.norm);
     }
     return hip_status(launch_block_norm_backward(s, a, g, stream));

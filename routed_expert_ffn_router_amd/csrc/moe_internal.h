@@ -509,8 +509,8 @@ struct WsLayout {
     size_t hdr, slots, sink, logits, idx, w, offsets, sorted_pick, pick_pos, perm_blocks, tiles, ntiles, desc, xq, xs,
         hq, hs, o;
     size_t stage_table, stage_list, stage_n, stage_ranges;   // NVFP4 staging (moe_layer)
-    size_t norm;   // the norms' gradient partials: over the intermediates, which those calls do not use
-    size_t total;
+    size_t norm, norm_end;   // the norms' gradient partials: over the intermediates, which those calls do not use
+    size_t total;            // of the layer's own calls
     int nt;        // activation terms
     int max_tiles;
 };

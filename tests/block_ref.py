@@ -99,8 +99,8 @@ def norm_backward(x, y, post, pre, gate, alpha, eps, d_x_out, d_normed, token_ga
         u = u + z * ag
     du = Val(torch.zeros_like(x) if d_x_out is None else d_x_out)
     out = dict.fromkeys(("dx", "dy", "d_gate", "d_post", "d_pre"))
-    rows = -(-T // min(T, 512)) if T else 0
-    cols = rows + 32 + 16                     # rows of one group, groups of a sixteenth, sixteenths
+    # a sum over the tokens: the rows of one group (of at least 256), at most 2048 groups by 32 threads, 32 sums
+    cols = -(-T // 256) + 64 + 32
     if d_normed is not None:
         dn = Val(d_normed)
         ru = inv_rms(u, eps)

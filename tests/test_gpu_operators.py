@@ -325,6 +325,49 @@ def test_combine_norm(T, d, k, E, act, shared, drop, gate, post):
         assert torch.equal(a, x_out) and torch.equal(b, normed)
 
 
+@pytest.mark.parametrize("act,T", [(BF16, 4099), (F32, 2051)])
+def test_rows_larger_than_the_caches(act, T):
+    """Arrays past the sizes from which the row kernels go round the caches: every operator on rows, in full."""
+    d, k = 4096, 8
+    g, sh = gen(17), shape(d, k, 64, act, n_shared=1, routed_scaling=2.5)
+    _, w, _, sp, pos = routing(g, sh, T, True)
+    i, wide = norm_inputs(g, T, d, act, 2, 1, 1)
+    o = rand(g, T * (k + 1), d, std=0.5)
+    tail = (i["post"], i["pre"], i["gate"], 2, ALPHA, EPS)
+    xs = torch.full((T * (k + 1), d), 7.5, dtype=act, device="cuda")
+    m.moe_dispatch(sh, i["x"], T, pos, xs)
+    want = torch.where((sp >= 0)[:, None], i["x"][(sp.clamp(min=0) // k).long()], torch.tensor(7.5, dtype=act, device="cuda"))
+    assert torch.equal(xs[:T * k], want) and torch.equal(xs[T * k:], i["x"])
+    del want
+    xs.mul_(torch.rand(T * (k + 1), 1, generator=g, device="cuda"))
+    dx = torch.empty_like(i["x"])
+    m.moe_dispatch_backward(sh, xs, T, pos, dx)
+    ref.check(dx, ref.dispatch_backward(xs, pos, 1), act, "dx")
+    del xs
+    d_o, d_w = torch.full_like(o, 7.5), torch.empty_like(w)
+    m.moe_combine_backward(sh, i["y"], o, w, pos, T, d_o, d_w)
+    ref.check(d_w, ref.combine_backward_weights(i["y"], o, pos, 2.5), F32, "d_w")
+    ok = pos >= 0
+    ref.check(d_o[pos[ok].long()], ref.combine_backward_rows(i["y"], w, 2.5)[ok], F32, "d_o")
+    assert torch.equal(d_o[T * k:], i["y"].float())
+    left = torch.ones(T * (k + 1), dtype=torch.bool, device="cuda")
+    left[pos[ok].long()], left[T * k:] = False, False
+    assert (d_o[left] == 7.5).all()
+    del d_o
+    a, b = torch.empty_like(i["x"]), torch.empty_like(i["x"])
+    m.moe_combine_norm(sh, o, w, pos, i["x"], T, *tail, a, b)
+    u, n = ref.norm_forward(i["x"], ref.combine(o, w, pos, 2.5, 1), i["post"], i["pre"], wide, ALPHA, EPS)
+    ref.check(a, u, act, "x_out of the combine")
+    ref.check(b, n, act, "normed of the combine")
+    del o
+    m.moe_block_norm(sh, i["x"], i["y"], T, *tail, a, b)
+    u, n = ref.norm_forward(i["x"], ref.Val(i["y"]), i["post"], i["pre"], wide, ALPHA, EPS)
+    ref.check(a, u, act, "x_out")
+    ref.check(b, n, act, "normed")
+    out = norm_gradients(sh, i, T, d, act, 2, 1, 1, a, b)
+    check_gradients(out, ref.norm_backward(i["x"], i["y"], i["post"], i["pre"], wide, ALPHA, EPS, a, b, False), act, 2)
+
+
 # ---------------------------------------------------------------------------------------------
 # 4-bit matrix-vector products
 # ---------------------------------------------------------------------------------------------
