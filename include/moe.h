@@ -327,7 +327,8 @@ moe_status moe_combine_backward(const moe_shape *shape, const void *dy, const fl
                                 float *d_w, hipStream_t stream);
 
 /* The norms before and after a block, with its gate and residual scale, in one pass.  With
- *   N(v; g)[i] = g[i] * v[i] / sqrt(mean_i v[i]^2 + eps)                 (RMS norm, fp32 sums),
+ *   N(v; g)[i] = g[i] * v[i] / sqrt(mean_i v[i]^2 + eps)     (RMS norm; squares summed in fp32, so
+ *                                                            a row of |v| past 1e18 gives 0),
  *   z[t] = N(y[t]; post_gamma), or y[t] when post_gamma is NULL,
  *   u[t] = x[t] + residual_scale * gate[t] * z[t],  or x[t] when y is NULL:
  *   x_out[t]  = u[t]                    rounded to act_dtype (the residual stream), and
@@ -349,7 +350,9 @@ moe_status moe_block_norm(const moe_shape *shape, const void *x, const void *y, 
 
 /* moe_combine and moe_block_norm in one pass: the same with
  *   y[t] = routed_scaling * sum_j topk_w[t,j] * o[pick_pos[t,j]] (+ o[T*top_k + t])
- * summed as in moe_combine (without its residual) and never rounded or written. */
+ * summed as in moe_combine (without its residual) and never rounded or written.  (For training,
+ * moe_combine and moe_block_norm, whose gradients are moe_block_norm_backward and then
+ * moe_combine_backward.) */
 moe_status moe_combine_norm(const moe_shape *shape, const float *o, const float *topk_w,
                             const int32_t *pick_pos, const void *x, int32_t T,
                             const float *post_gamma, const float *pre_gamma, const void *gate,
@@ -378,7 +381,8 @@ moe_status moe_block_norm_backward(const moe_shape *shape, const void *x, const 
  *   y[t,n] = tensor_scale * sum_k W[n,k] x[t,k] (+ bias[n]),
  * W dequantised on the fly from q ([rows][cols/2] codes) and s ([rows][cols/B] scales), as the
  * experts' sub-tensors are.  The weights and x enter the products exactly (fp32 x as three bf16
- * terms), sums are fp32, and y is rounded once.  1 <= rows <= 2^24, cols a multiple of 128,
+ * terms; a weight of 2^128 or more, under scale byte 253 or 254, is infinite), sums are fp32, and
+ * y is rounded once.  1 <= rows <= 2^24, cols a multiple of 128,
  * rows * cols <= 2^34, T <= 64 (MOE_ERR_UNSUPPORTED beyond).  tensor_scale is a host value, used
  * as given (1 for MXFP4).  x: [T][cols], y: [T][rows] act_dtype; bias: [rows] fp32 or NULL; q, s, x
  * and y 16-byte aligned; y may not alias x. */

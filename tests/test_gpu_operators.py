@@ -403,23 +403,28 @@ def test_linear(N, K, T, act, wf):
         assert (y[T * N:] == 7.5).all()                      # nothing behind the last row
 
 
-@pytest.mark.parametrize("act", [BF16, F32])
-def test_linear_scale_bytes(act):
-    """Every E8M0 byte whose products are normal fp32 numbers, and the NaN byte: a row has one code, 1.0, under
-    its own scale, and x one value, so y is that product."""
-    g = gen(11)
-    N, K = 256, 128
+@pytest.mark.parametrize("N,K,T,act", [(256, 128, 16, BF16), (256, 128, 16, F32), (16640, 128, 16, BF16), (16640, 128, 8, F32),
+                                       (256, 8320, 16, BF16), (256, 8320, 16, F32)])
+def test_linear_scale_bytes(N, K, T, act):
+    """Every code under every E8M0 byte whose weights are below 2^128, subnormal ones among them, and the NaN
+    byte: row n has all codes in block 1 under byte n, token t one value at code t, so y is that product (exact
+    where it is a normal number of the type)."""
     q = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
     s = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
-    q[:, 20] = 2                                             # element 40: code 2 is 1.0, block 1
-    s[:, 1] = torch.arange(256, device="cuda").to(torch.uint8)
-    x = torch.zeros(1, K, dtype=act, device="cuda")
-    x[0, 40] = 1.5
-    y = torch.empty(1, N, dtype=act, device="cuda")
-    m.moe_linear(m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32), q, s, 1.0, x, 1, None, y)
-    want = torch.ldexp(torch.tensor(1.5, dtype=torch.float64, device="cuda"), torch.arange(256, device="cuda") - 127).to(act)
-    assert torch.equal(y[0, 1:255], want[1:255])
-    assert torch.isnan(y[0, 255])
+    s[:, 1] = (torch.arange(N, device="cuda") % 256).to(torch.uint8)
+    for j in range(8):
+        q[:, 16 + j] = 2 * j | (2 * j + 1) << 4              # elements 32 .. 47: codes 0 .. 15
+    values = torch.tensor(ref.E2M1 + tuple(-v for v in ref.E2M1), dtype=torch.float64, device="cuda")[:T, None]
+    weight = values * torch.ldexp(torch.ones(N, dtype=torch.float64, device="cuda"), s[:, 1].int() - 127)
+    for e in (60, -60):
+        x = torch.zeros(T, K, dtype=act, device="cuda")
+        x[torch.arange(T), 32 + torch.arange(T)] = 2.0 ** e
+        y = torch.empty(T, N, dtype=act, device="cuda")
+        m.moe_linear(m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32), q, s, 1.0, x, T, None, y)
+        want = weight * 2.0 ** e
+        sure = (s[:, 1] < 253) & ((want == 0) | (want.abs() >= 2.0 ** -126))
+        assert torch.equal(y[sure], want.to(act)[sure])
+        assert torch.isnan(y[:, s[:, 1] == 255]).all()
 
 
 def test_linear_values_outside_the_numbers():
