@@ -345,6 +345,9 @@ __device__ __forceinline__ lin_f32x4 lin_sum_waves(const lin_f32x4* part, int la
 
 // One tile of 16 rows per workgroup, K shared out over W waves of at most NMAX steps; NX direct loads
 // bring x's step (four bf16 or two fp32 tokens each), swizzled by token.  D steps of codes and x in flight.
+// 4096 x 4096 MXFP4, one token: 4.0 us (8.9 MB; a kernel of one round trip to memory takes 2.0), 16 tokens
+// 5.1; eight waves and two steps were as fast or faster than 4 or 16 waves and one to four steps up to 4096
+// rows.  With many rows x is what costs (65536 x 6144, 16 tokens: 104 us).
 template <typename XT, int WF, int NX, int W, int D, int NMAX>
 __global__ __launch_bounds__(64 * W) void k_linear_ring(LinArgs a) {
     constexpr int UB = LinFmt<WF>::UB, SPD = LinFmt<WF>::SPD;
@@ -436,6 +439,8 @@ __global__ __launch_bounds__(64 * W) void k_linear_ring(LinArgs a) {
 // kLinRound tiles meet in LDS between two barriers, one wave adding up each tile in wave order.
 // Rounds: sums of 1, 2, 3 tiles at a time in two buffers, one barrier a round, took 65, 56 and 53 us at
 // 65536 x 6144 NVFP4 and 16 tokens; one buffer of 4 tiles with two barriers 53, one of 6 52.
+// Now 50 us there, 228 MB at 4.5 TB/s (MXFP4 43): bringing x's 196 KB to every CU takes about 5 of them before
+// the first product.  The decode does not bound it: fp16 weights at half the instructions took as long.
 constexpr int kLinWaves = 8;
 
 template <typename XT, int WF, int NSW>
@@ -584,11 +589,15 @@ static void plain_launch(const LinArgs& a, hipStream_t st) {
 
 template <typename XT, int WF>
 static void linear_launch(const LinArgs& a, hipStream_t st) {
+    // Many rows: x read once per CU (stream) against once per tile (ring), us, bf16.  8192 x 4096, 16 tokens:
+    // stream 9.6, ring 9.0; 16384 x 4096, 16 tokens 12.3, 19.5.  Four tokens, MXFP4: 16384 x 4096 10.2, 9.9;
+    // 32768 x 4096 16.3, 18.6; 65536 x 6144 41, 52.  One or two tokens: 18.0, 16.2 at 65536 x 2048, 41, 44 at
+    // 65536 x 6144 (NVFP4 50, 48).
     const bool many = a.N >= 16384;
     const int passes = (a.T + kLinPass<XT> - 1) / kLinPass<XT>;
     if (a.K <= kLinDmaMaxK) {
         if constexpr (sizeof(XT) == 2) {
-            if (many && a.T > 4) stream_launch<XT, WF>(a, passes, st);
+            if (many && (a.T > 4 || (a.T > 2 && (long long)a.N * a.K >= 1 << 27))) stream_launch<XT, WF>(a, passes, st);
             else if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
             else if (a.T <= 8) ring_launch<XT, WF, 2>(a, 1, st);
             else ring_launch<XT, WF, 4>(a, passes, st);

@@ -24,8 +24,9 @@ static int row_threads(size_t units, int most) {
     return (int)(((units + chunks - 1) / chunks + 63) / 64 * 64);
 }
 
-// xs[pick_pos[t,j]] = x[t]: one thread per 16 bytes of a token's row, which it reads once and stores
-// for every pick.
+// xs[pick_pos[t,j]] = x[t]: one thread per 16 bytes of a token's row, which it reads once and stores for
+// every pick (the other way round, a read per sorted row, would read x k times).  Bound by its stores:
+// 4096 tokens, d 4096, 8 picks, bf16: 54 us, 302 MB at 5.6 TB/s, the rate of a large copy; one token 2.0 us.
 template <bool NT>
 __global__ __launch_bounds__(512) void k_dispatch(const uint8_t* __restrict__ x, int T, int k, size_t row_bytes,
                                                   int chunks, int shared, const int32_t* __restrict__ pick_pos,
@@ -60,7 +61,10 @@ hipError_t launch_dispatch(const moe_shape* s, const void* x, int T, const int32
     return hipGetLastError();
 }
 
-// dx[t] = sum_j dxs[pick_pos[t,j]] (+ dxs[P + t]): one thread per 8 columns, added in rank order in fp32
+// dx[t] = sum_j dxs[pick_pos[t,j]] (+ dxs[P + t]): one thread per 8 columns, added in rank order in fp32;
+// read by token, so there are no atomics.  Bound by its loads, up to eight rows in flight; workgroups of two
+// waves, because larger ones leave CUs uneven when there are few tokens (333 tokens, d 6144, fp32: 13 us,
+// 384 threads 14).  4096 tokens, d 4096, 8 picks, bf16: 52 us, 302 MB at 5.8 TB/s.
 template <typename XT, bool NT>
 __global__ __launch_bounds__(128) void k_dispatch_backward(const XT* __restrict__ dxs, int T, int k, int d,
                                                            int chunks, int shared,
@@ -120,7 +124,10 @@ hipError_t launch_dispatch_backward(const moe_shape* s, const void* dxs, int T, 
 // W waves (1, or 4 when there are few picks) per (token, pick): d_o[pos] = s w dy[t] and
 // d_w = s <dy[t], o[pos]>, the products summed per lane in fp32 and over lanes and waves in a fixed order.
 // With a shared expert each token has one job more, which copies dy[t] to row P + t.  d_o may be o: a lane
-// reads its values of o before it writes them.
+// reads its values of o before it writes them.  Bound by HBM: o read and d_o written once, 4096 tokens,
+// d 4096, 8 picks: 220 us, 1.14 GB at 5.2 TB/s (dy comes twice, its eight picks lying in two workgroups;
+// one of eight waves took as long, and requesting the next loads before the stores gained 3% there and lost
+// 6% on short rows).
 template <typename XT, int W, bool NT>
 __global__ __launch_bounds__(256) void k_combine_backward(const XT* __restrict__ dy, const float* o,
                                                           const float* __restrict__ w,

@@ -385,6 +385,7 @@ LINEAR = [  # N, K, T
     (1, 128, 1), (15, 256, 1), (16, 128, 2), (33, 384, 3), (128, 4096, 1), (100, 1152, 5), (257, 640, 16), (64, 2048, 17),
     (48, 512, 33), (31, 896, 64), (5000, 256, 7), (2048, 6144, 4), (4096, 512, 12), (40000, 128, 1), (9000, 384, 40), (515, 8192, 9),
     (20000, 640, 6), (16399, 8192, 13), (16384, 6144, 5), (33000, 256, 16), (300, 8320, 5), (16400, 8320, 3),
+    (17000, 256, 20), (17000, 256, 40), (32770, 4096, 3), (300, 8320, 20), (300, 8320, 40),
 ]
 
 
