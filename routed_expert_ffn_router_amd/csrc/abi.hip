@@ -5,7 +5,7 @@
 
 #include <mutex>
 
-#include "moe_internal.h"
+#include "block_ops.h"
 
 namespace moe {
 
@@ -99,10 +99,15 @@ WsLayout ws_layout(const moe_shape* s, int32_t T, bool slots_for_any_shape) {
         L.stage_n = take(4);
         L.stage_ranges = take(8 * ((E + kStageGroup - 1) / kStageGroup));
     }
-    L.norm = L.sink;         // the norms' gradient partials, after the header and the hand-over slots
-    L.norm_end = L.norm + align256(8 * (size_t)norm_grad_groups(s, T) * d);
     L.total = o;
     return L;
+}
+
+// the norms' gradient keeps its partial sums after the header and the hand-over slots, over the layer's
+// intermediates, which that call does not use; the layer's own calls need L.total alone
+static size_t norm_scratch(const WsLayout& L) { return L.sink; }
+static size_t norm_scratch_bytes(const moe_shape* s, int32_t T) {
+    return align256(8 * (size_t)norm_grad_groups_most(s, T) * s->d_model);
 }
 
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -356,7 +361,8 @@ size_t moe_blob_stride(const moe_shape* s) {
 size_t moe_workspace_bytes(const moe_shape* s, int32_t T) {
     if (check_shape(s) != MOE_OK || check_T(s, T) != MOE_OK) return 0;
     const WsLayout L = ws_layout(s, T);
-    return L.total > L.norm_end ? L.total : L.norm_end;
+    const size_t norm_end = norm_scratch(L) + norm_scratch_bytes(s, T);
+    return L.total > norm_end ? L.total : norm_end;
 }
 
 moe_status moe_workspace_init(const moe_shape* s, int32_t T, void* ws, size_t ws_bytes, int32_t poll_limit,
@@ -556,8 +562,8 @@ moe_status moe_block_norm_backward(const moe_shape* s, const void* x, const void
         if ((dy && !y) || (d_gate && !gate) || (d_post_gamma && !post_gamma)) return MOE_ERR_INVALID;
         if (!y && (post_gamma || gate)) return MOE_ERR_INVALID;
         const WsLayout L = ws_layout(s, T);
-        if (ws_bytes < L.norm_end) return MOE_ERR_WORKSPACE;
-        g.part = (float*)((uint8_t*)ws + L.norm);
+        if (ws_bytes < norm_scratch(L) + norm_scratch_bytes(s, T)) return MOE_ERR_WORKSPACE;
+        g.part = (float*)((uint8_t*)ws + norm_scratch(L));
     }
     return hip_status(launch_block_norm_backward(s, a, g, stream));
 }

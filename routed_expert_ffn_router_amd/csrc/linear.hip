@@ -22,7 +22,7 @@
 //   k_linear_stream  many rows: each wave keeps its K slice of x in registers for all the row tiles that
 //                    its workgroup takes, so x is read once per CU;
 //   k_linear         everything else, straight from global memory to registers.
-#include "moe_internal.h"
+#include "block_ops.h"
 
 namespace moe {
 

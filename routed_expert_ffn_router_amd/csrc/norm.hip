@@ -9,7 +9,7 @@
 // are many rows (d 4096, bf16, with a gate: 4096 rows 32 us, 168 MB at 5.3 TB/s), by the chain load, sum,
 // sum, store where there are few (one row 2.6 us).  Two vectors per thread and half the threads, tried for
 // d 4096 to 8192, were slower (35 -> 39 us; the combine 45 -> 50).
-#include "moe_internal.h"
+#include "block_ops.h"
 
 namespace moe {
 
@@ -205,12 +205,20 @@ hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t 
 // share of HBM busy: one workgroup per CU for long rows, up to eight for short ones.  More only add partial sums
 // to write and read (4096 rows, 256 / 512 groups: d 4096 bf16 55 / 60 us, d 1024 41 / 28).  Up to four
 // rows one workgroup takes them all and no second kernel runs.
-int norm_grad_groups(const moe_shape* s, int T) {
-    if (T <= 4) return 1;
+static int norm_groups_cap(const moe_shape* s) {
     const int row = 8 * s->d_model * (s->act_dtype == MOE_DT_BF16 ? 2 : 4);       // bytes of a row, in and out
-    const int per_cu = row >= 65536 ? 1 : 65536 / row < 8 ? (65536 + row - 1) / row : 8;
-    const int rows = (T + 256 * per_cu - 1) / (256 * per_cu);
+    return 256 * (row >= 65536 ? 1 : 65536 / row < 8 ? (65536 + row - 1) / row : 8);
+}
+
+static int norm_grad_groups(const moe_shape* s, int T) {
+    if (T <= 4) return 1;
+    const int cap = norm_groups_cap(s), rows = (T + cap - 1) / cap;
     return (T + rows - 1) / rows;
+}
+
+int norm_grad_groups_most(const moe_shape* s, int T) {
+    const int cap = norm_groups_cap(s);
+    return T <= 4 ? 1 : T < cap ? T : cap;
 }
 
 // One row's loads, as they come: requested for the next row while this one is worked on

@@ -1,5 +1,5 @@
 // Tokens laid out by expert (dispatch), and the gradients of the dispatch and of the weighted combine.
-#include "moe_internal.h"
+#include "block_ops.h"
 
 namespace moe {
 

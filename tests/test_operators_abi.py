@@ -143,6 +143,14 @@ def test_workspace_holds_the_gradient_sums(k, T):
     assert m.moe_workspace_bytes(sh, T) >= 256 + 8 * 16 * 16 + (1 if T <= 4 else -(-T // -(-T // 2048))) * 8 * 256
 
 
+@pytest.mark.parametrize("d,act", [(128, 1), (640, 0), (2176, 1)])
+def test_a_workspace_serves_every_smaller_token_count(d, act):
+    """One pick of one expert per token: the gradient sums are the largest part for many token counts."""
+    sh = m.make_shape(d, 128, 1, 1, act_dtype=act)
+    sizes = [m.moe_workspace_bytes(sh, T) for T in range(1, 2600)]
+    assert sizes == sorted(sizes)
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     """A host tensor, another dtype, a strided view and a short tensor, before any launch."""
     d, T = SH.d_model, 2
