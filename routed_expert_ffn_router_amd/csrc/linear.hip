@@ -76,13 +76,13 @@ struct LinX<float> {
         raw[1] = gload16(p + 4);
     }
     // cut, not rounded: the first term of a large value never becomes infinite; an infinite value is
-    // its own first term
+    // its own first term, and a NaN is made quiet, so that the cut leaves one (0x7f800001 is cut to infinity)
     __device__ __forceinline__ void terms(lin_bf16x8 (&t)[3]) const {
         const uint32_t v[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
         uint32_t w[3][8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float rest = __uint_as_float(v[e]);
+            float rest = __builtin_canonicalizef(__uint_as_float(v[e]));
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const uint32_t cut = __float_as_uint(rest) & 0xffff0000u;

@@ -431,8 +431,8 @@ def test_linear_scale_bytes(N, K, T, act):
 def test_linear_values_outside_the_numbers():
     """Infinity and NaN in x reach the rows whose weights see them, in that token alone."""
     g = gen(12)
-    K, T = 256, 3
-    for N, act in ((40, BF16), (40, F32), (16390, BF16), (16390, F32)):
+    T = 3
+    for N, K, act in ((40, 256, BF16), (40, 256, F32), (16390, 256, BF16), (16390, 256, F32), (40, 8320, BF16), (40, 8320, F32)):
         q, s, _ = quantised(g, N, K, 0)
         x = rand(g, T, K, dtype=act)
         mat = m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32)
@@ -441,11 +441,15 @@ def test_linear_values_outside_the_numbers():
         x[0, 200], x[2, 3] = float("inf"), float("nan")
         m.moe_linear(mat, q, s, 1.0, x, T, None, z)
         assert torch.equal(z[1], y[1]) and torch.isnan(z[2]).all()
+        if act == F32:                                       # a NaN whose payload lies in the lower half
+            x.view(torch.int32)[2, 3] = 0x7f800001
+            m.moe_linear(mat, q, s, 1.0, x, T, None, z)
+            assert torch.equal(z[1], y[1]) and torch.isnan(z[2]).all()
         w = ref.weights(q, s, 0)[:, 200]
         assert torch.equal(torch.isnan(z[0]), w == 0)        # 0 times infinity
         assert torch.equal(z[0][w != 0], (torch.sign(w) * float("inf")).to(act)[w != 0])
         # the largest finite values stay finite on the way
-        if act == F32 and N == 40:
+        if act == F32 and N == 40 and K == 256:
             x = torch.zeros(1, K, device="cuda")
             x[0, 7] = torch.finfo(F32).max
             small_s = torch.full_like(s, 100)
