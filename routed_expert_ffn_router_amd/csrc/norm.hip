@@ -169,8 +169,8 @@ static void norm_launch(const NormArgs& a, hipStream_t st) {
     const bool many = a.T > 256 || vpt == 2, nt = 4 * (size_t)a.T * a.d * (a.k + a.shared) >= kStreamBytes;
     if (a.o) {
         if (vpt == 2) MOE_LAUNCH((k_block_norm<XT, 2, 4, true, false>), grid, block, 0, st, a);
-        else if (many && nt) MOE_LAUNCH((k_block_norm<XT, 1, 4, false, true>), grid, block, 0, st, a);
-        else if (many) MOE_LAUNCH((k_block_norm<XT, 1, 4, false, false>), grid, block, 0, st, a);
+        else if (many && nt) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, true>), grid, block, 0, st, a);
+        else if (many) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, false>), grid, block, 0, st, a);
         else MOE_LAUNCH((k_block_norm<XT, 1, 8, false, false>), grid, block, 0, st, a);
     } else if (vpt == 2) {
         MOE_LAUNCH((k_block_norm<XT, 2, 0, true, false>), grid, block, 0, st, a);
