@@ -293,9 +293,10 @@ moe_status moe_layer_noalloc(const moe_shape *shape, const void *x, int32_t T, c
 /* ---------------------------------------------------------------------------------------
  * Operators around the experts.  They take the same shape, types and grouping; every pointer is
  * device memory, 16-byte aligned where it holds rows of d_model values.  `pick_pos` is
- * moe_permute's: a pick whose position lies outside [0, T*top_k) - a dropped pick's is -1 - has no
- * row and is left out of every sum.  With n_shared = 1, rows T*top_k + t of the expert-side
- * arrays belong to the shared expert and token t, as in moe_expert_ffn's o.
+ * moe_permute's: no two picks share a position, and a pick whose position lies outside
+ * [0, T*top_k) - a dropped pick's is -1 - has no row and is left out of every sum.  With
+ * n_shared = 1, rows T*top_k + t of the expert-side arrays belong to the shared expert and token
+ * t, as in moe_expert_ffn's o.
  * --------------------------------------------------------------------------------------- */
 
 /* Tokens laid out by expert, for expert products of the caller's own (training, dense experts):

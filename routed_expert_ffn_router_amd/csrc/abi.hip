@@ -574,7 +574,8 @@ moe_status moe_linear(const moe_matrix* m, const uint8_t* q, const uint8_t* s, f
     if (m->wformat != MOE_WF_MXFP4 && m->wformat != MOE_WF_NVFP4) return MOE_ERR_INVALID;
     if (m->act_dtype != MOE_DT_F32 && m->act_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
     if (!isfinite(tensor_scale)) return MOE_ERR_INVALID;
-    if (m->cols % 128 != 0 || m->rows > (1 << 24) || (long long)m->rows * m->cols > (1LL << 34) || T > kLinearMaxT) return MOE_ERR_UNSUPPORTED;
+    if (m->cols % 128 != 0 || m->rows > (1 << 24) || (long long)m->rows * m->cols > (1LL << 34) || T > kLinearMaxT)
+        return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!q || !s || !x || !y || x == y) return MOE_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(s, 16) || !aligned(x, 16) || !aligned(y, 16) || (bias && !aligned(bias, 4)))
