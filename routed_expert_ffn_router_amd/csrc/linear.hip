@@ -12,16 +12,20 @@
 // row: lane group g takes elements [32 g, 32 g + 32), 16 code bytes, and MFMA h of the step their
 // elements [8 h, 8 h + 8).  C: lane l, register r is weight row 4 (l / 16) + r, token l % 16.
 //
-// Three kernels.  The bytes are the weights', read once, so HBM is the floor; what a straight kernel
+// Four kernels.  The bytes are the weights', read once, so HBM is the floor; what a straight kernel
 // meets first is the vector L1, which serves a load one lane quad at a time: in the operand layout the
 // lanes of a quad hold four different rows, so a load of 16 bytes per lane costs as much as four that
 // are laid out along the rows, and a load of one scale byte per lane as much as one of 16 (taking the
 // scale or the x loads out of k_linear each saved 20 of 84 us at 65536 x 6144, 16 tokens).
-//   k_linear_ring    bf16 x, up to 16 tokens: codes, scales and x go straight to LDS (global_load_lds) in
-//                    row order, each wave into its own ring, so no wave waits for another before the sums;
+//   k_linear_ring    up to 16384 rows, and few tokens: codes, scales and x go straight to LDS
+//                    (global_load_lds) in row order, each wave into its own ring, so no wave waits for
+//                    another before the sums;
 //   k_linear_stream  many rows: each wave keeps its K slice of x in registers for all the row tiles that
 //                    its workgroup takes, so x is read once per CU;
-//   k_linear         everything else, straight from global memory to registers.
+//   k_linear_tile    many rows and more tokens than the registers hold: the waves of a workgroup share x's
+//                    step in LDS;
+//   k_linear         many rows and up to 16 fp32 tokens past the stream's, straight from global memory to
+//                    registers.
 #include "block_ops.h"
 
 namespace moe {
@@ -57,45 +61,26 @@ __device__ __forceinline__ lin_bf16x8 lin_weights_nv(uint32_t codes, float scale
                       (__bf16)(c[0] * scale), (__bf16)(c[1] * scale), (__bf16)(d[0] * scale), (__bf16)(d[1] * scale)};
 }
 
-// x's operand of one MFMA: NT bf16 terms of 8 consecutive elements, held as loaded until they are used
-template <typename XT>
-struct LinX;
-template <>
-struct LinX<uint16_t> {
-    static constexpr int NT = 1;
-    uint4 raw;
-    __device__ __forceinline__ void load(const uint16_t* p) { raw = gload16(p); }
-    __device__ __forceinline__ void terms(lin_bf16x8 (&t)[1]) const { t[0] = lin_as_bf16x8(raw); }
-};
-template <>
-struct LinX<float> {
-    static constexpr int NT = 3;
-    uint4 raw[2];
-    __device__ __forceinline__ void load(const float* p) {
-        raw[0] = gload16(p);
-        raw[1] = gload16(p + 4);
-    }
-    // cut, not rounded: the first term of a large value never becomes infinite; an infinite value is
-    // its own first term, and a NaN is made quiet, so that the cut leaves one (0x7f800001 is cut to infinity)
-    __device__ __forceinline__ void terms(lin_bf16x8 (&t)[3]) const {
-        const uint32_t v[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
-        uint32_t w[3][8];
+// The three bf16 terms of 8 fp32 values.  Cut, not rounded: the first term of a large value never becomes infinite;
+// an infinite value is its own first term, and a NaN is made quiet, so that the cut leaves one (0x7f800001 is cut
+// to infinity).
+__device__ __forceinline__ void lin_f32_terms(const lin_u32x4& a, const lin_u32x4& b, lin_bf16x8 (&t)[3]) {
+    uint32_t w[3][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float rest = __builtin_canonicalizef(__uint_as_float(v[e]));
+    for (int e = 0; e < 8; ++e) {
+        float rest = __builtin_canonicalizef(__uint_as_float(e < 4 ? a[e] : b[e - 4]));
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const uint32_t cut = __float_as_uint(rest) & 0xffff0000u;
-                w[i][e] = cut;
-                rest = (cut & 0x7fffffffu) == 0x7f800000u ? 0.0f : rest - __uint_as_float(cut);
-            }
+        for (int i = 0; i < 3; ++i) {
+            const uint32_t cut = __float_as_uint(rest) & 0xffff0000u;
+            w[i][e] = cut;
+            rest = (cut & 0x7fffffffu) == 0x7f800000u ? 0.0f : rest - __uint_as_float(cut);
         }
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            t[i] = lin_as_bf16x8(make_uint4(w[i][0] >> 16 | w[i][1], w[i][2] >> 16 | w[i][3], w[i][4] >> 16 | w[i][5],
-                                            w[i][6] >> 16 | w[i][7]));
     }
-};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        t[i] = lin_as_bf16x8(make_uint4(w[i][0] >> 16 | w[i][1], w[i][2] >> 16 | w[i][3], w[i][4] >> 16 | w[i][5],
+                                        w[i][6] >> 16 | w[i][7]));
+}
 
 // a step's scale byte(s) as factors of its first and last 16 elements
 template <int WF>
@@ -142,22 +127,16 @@ __device__ __forceinline__ void lin_store(const LinArgs& a, int t, int row, cons
         if (row + r < a.N) store_act(y, (size_t)r, o[r]);
 }
 
-// what a wave loads for one step: codes and scale bytes of F row fragments, x of C token fragments
-template <typename XT, int F, int C>
-struct LinStep {
-    uint4 code[F];
-    uint32_t sc[F];
-    LinX<XT> x[C][4];
-};
-
-// A workgroup of W waves owns 16 F rows and 16 C tokens; its waves share out K, and their sums are
-// added through LDS in wave order.  A wave keeps D steps of loads in flight, in a ring of registers.
-template <typename XT, int WF, int F, int C, int W, int D>
-__global__ __launch_bounds__(64 * W) void k_linear(LinArgs a) {
-    __shared__ lin_f32x4 part[W][F * C][64];
+// A workgroup of eight waves owns 64 rows and 16 fp32 tokens; its waves share out K, and their sums are added
+// through LDS in wave order.  65536 x 6144 MXFP4, 16 tokens: 111 us, 16384 x 4096 21 (k_linear_tile 101 and 45,
+// k_linear_ring 224 and 42); one or two rows' fragments per wave and deeper prefetch were slower.
+template <int WF>
+__global__ __launch_bounds__(512) void k_linear(LinArgs a) {
+    constexpr int F = 4, W = 8;
+    __shared__ lin_f32x4 part[W][F][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lg = lane >> 4;
-    const int n0 = blockIdx.x * 16 * F, t0 = blockIdx.y * 16 * C;
+    const int n0 = blockIdx.x * 16 * F;
     const int NS = a.K / 128;
     const int s0 = wave * NS / W, n = (wave + 1) * NS / W - s0;
     constexpr int SB = WF == MOE_WF_MXFP4 ? 32 : 16;          // weights per scale
@@ -169,85 +148,62 @@ __global__ __launch_bounds__(64 * W) void k_linear(LinArgs a) {
         q[f] = a.q + (size_t)row * (a.K / 2) + (size_t)s0 * 64 + lg * 16;
         s[f] = a.s + (size_t)row * (a.K / SB) + (size_t)s0 * (128 / SB) + lg * (32 / SB);
     }
-    const XT* x[C];                                            // columns past the last token repeat it
+    const float* x = (const float*)a.x + (size_t)(li < a.T ? li : a.T - 1) * a.K + (size_t)s0 * 128 + lg * 32;
+    lin_f32x4 acc[F];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int t = t0 + 16 * c + li < a.T ? t0 + 16 * c + li : a.T - 1;
-        x[c] = (const XT*)a.x + (size_t)t * a.K + (size_t)s0 * 128 + lg * 32;
-    }
-    lin_f32x4 acc[F][C];
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[f][c] = lin_f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int f = 0; f < F; ++f) acc[f] = lin_f32x4{0.f, 0.f, 0.f, 0.f};
 
-    LinStep<XT, F, C> ring[D];
-    auto request = [&](LinStep<XT, F, C>& r, int k) {
+    uint4 code[F], xr[8];
+    uint32_t sc[F];
+    auto request = [&](int k) {
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            r.code[f] = gload16(q[f] + (size_t)k * 64);
-            if constexpr (WF == MOE_WF_MXFP4) r.sc[f] = *(__attribute__((address_space(1))) const uint8_t*)(s[f] + (size_t)k * 4);
-            else r.sc[f] = *(__attribute__((address_space(1))) const uint16_t*)(s[f] + (size_t)k * 8);
+            code[f] = gload16(q[f] + (size_t)k * 64);
+            if constexpr (WF == MOE_WF_MXFP4) sc[f] = *(__attribute__((address_space(1))) const uint8_t*)(s[f] + (size_t)k * 4);
+            else sc[f] = *(__attribute__((address_space(1))) const uint16_t*)(s[f] + (size_t)k * 8);
         }
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) r.x[c][h].load(x[c] + (size_t)k * 128 + 8 * h);
+        for (int i = 0; i < 8; ++i) xr[i] = gload16(x + (size_t)k * 128 + 4 * i);
     };
-    auto multiply = [&](const LinStep<XT, F, C>& r) {
-        float sc[F][2];
+    auto multiply = [&]() {
+        float s2[F][2];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            lin_scales<WF>(r.sc[f], sc[f]);
-        }
+        for (int f = 0; f < F; ++f) lin_scales<WF>(sc[f], s2[f]);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            lin_bf16x8 xt[C][LinX<XT>::NT];
-#pragma unroll
-            for (int c = 0; c < C; ++c) r.x[c][h].terms(xt[c]);
+            lin_bf16x8 xt[3];
+            lin_f32_terms(lin_u32x4{xr[2 * h].x, xr[2 * h].y, xr[2 * h].z, xr[2 * h].w},
+                          lin_u32x4{xr[2 * h + 1].x, xr[2 * h + 1].y, xr[2 * h + 1].z, xr[2 * h + 1].w}, xt);
 #pragma unroll
             for (int f = 0; f < F; ++f) {
-                const uint32_t word = h == 0 ? r.code[f].x : h == 1 ? r.code[f].y : h == 2 ? r.code[f].z : r.code[f].w;
-                const lin_bf16x8 wv = lin_weights<WF>(word, sc[f][h / 2]);
+                const uint32_t word = h == 0 ? code[f].x : h == 1 ? code[f].y : h == 2 ? code[f].z : code[f].w;
+                const lin_bf16x8 w = lin_weights<WF>(word, s2[f][h / 2]);
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int i = 0; i < LinX<XT>::NT; ++i)
-                        acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xt[c][i], acc[f][c], 0, 0, 0);
+                for (int i = 0; i < 3; ++i) acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xt[i], acc[f], 0, 0, 0);
             }
         }
     };
     if (n > 0) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) request(ring[i], i < n ? i : n - 1);
-        int k = 0;
-        for (; k + D < n; k += D) {          // steps past the last load the last one again
-#pragma unroll
-            for (int i = 0; i < D; ++i) {
-                multiply(ring[i]);
-                request(ring[i], k + i + D < n ? k + i + D : n - 1);
-            }
+        request(0);
+        for (int k = 1; k < n; ++k) {      // each register is requested again once its product is under way
+            multiply();
+            request(k);
         }
-#pragma unroll
-        for (int i = 0; i < D; ++i)
-            if (k + i < n) multiply(ring[i]);
+        multiply();
     }
 #pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            mfma_results_here(acc[f][c]);
-            part[wave][f * C + c][lane] = acc[f][c];
-        }
+    for (int f = 0; f < F; ++f) {
+        mfma_results_here(acc[f]);
+        part[wave][f][lane] = acc[f];
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < F * C * 64; i += 64 * W) {
-        const int fc = i >> 6, l = i & 63;
-        const int t = t0 + 16 * (fc % C) + (l & 15), row = n0 + 16 * (fc / C) + 4 * (l >> 4);
-        if (t >= a.T) continue;
-        lin_f32x4 v = part[0][fc][l];
+    for (int i = threadIdx.x; i < F * 64; i += 64 * W) {
+        const int f = i >> 6, l = i & 63;
+        if ((l & 15) >= a.T) continue;
+        lin_f32x4 v = part[0][f][l];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += part[w][fc][l];
-        lin_store<XT>(a, t, row, v);
+        for (int w = 1; w < W; ++w) v += part[w][f][l];
+        lin_store<float>(a, l & 15, n0 + 16 * f + 4 * (l >> 4), v);
     }
 }
 
@@ -285,7 +241,7 @@ __device__ __forceinline__ lin_f32x4 lin_sum_terms(const lin_f32x4& s0, const li
 template <typename XT>
 constexpr int kLinPass = sizeof(XT) == 4 ? 5 : 16;
 
-constexpr int kLinDmaMaxK = 8192;         // 8 steps for each of 8 waves
+constexpr int kLinStreamMaxK = 8192;      // x in registers: 8 steps for each of 8 waves
 typedef __attribute__((address_space(3))) uint8_t* lin_lds_t;
 
 __device__ __forceinline__ uint32_t lin_lds_offset(const uint8_t* p) { return (uint32_t)(uintptr_t)(lin_lds_t)p; }
@@ -322,10 +278,11 @@ __device__ __forceinline__ void lin_dma_scales(const LinArgs& a, int tile, int s
     dma4(a.s + (size_t)row * SR + (off < SR ? off : SR - 4), dst);
 }
 
-// the waves' sums of a tile, in wave order, and over a token's terms: a lane's rows of token lane % 16
-template <typename XT, int W>
+// the waves' sums of a tile, in wave order, and over a token's terms where those are columns: a lane's rows of
+// token lane % 16
+template <bool TERMS, int W>
 __device__ __forceinline__ lin_f32x4 lin_sum_waves(const lin_f32x4* part, int lane) {
-    if constexpr (sizeof(XT) == 2) {
+    if constexpr (!TERMS) {
         lin_f32x4 v = part[lane];
 #pragma unroll
         for (int w = 1; w < W; ++w) v += part[w * 64 + lane];
@@ -343,64 +300,73 @@ __device__ __forceinline__ lin_f32x4 lin_sum_waves(const lin_f32x4* part, int la
     }
 }
 
-// One tile of 16 rows per workgroup, K shared out over W waves of at most NMAX steps; NX direct loads
-// bring x's step (four bf16 or two fp32 tokens each), swizzled by token.  D steps of codes and x in flight.
-// 4096 x 4096 MXFP4, one token: 4.0 us (8.9 MB; a kernel of one round trip to memory takes 2.0), 16 tokens
-// 5.1; eight waves and two steps were as fast or faster than 4 or 16 waves and one to four steps up to 4096
-// rows.  With many rows x is what costs (65536 x 6144, 16 tokens: 104 us).
-template <typename XT, int WF, int NX, int W, int D, int NMAX>
+// One tile of 16 rows per workgroup, K shared out over W waves.  NX direct loads bring x's step (four bf16 or two
+// fp32 tokens each), swizzled by token.  Two steps of codes and x in flight, scales with the first step that
+// they serve.  bf16: 16 columns of tokens, or twice 16 (NX = 8).  fp32: up to five tokens of three columns, or
+// (NX = 8) 16 columns of tokens, multiplied by each term in turn.
+// 4096 x 4096 MXFP4, one token: 4.2 us (8.9 MB; a kernel of one round trip to memory takes 2.0), 16 tokens 5.1, 32
+// 6.9; 4096 x 16384 8.6, 14.7 and 20.  Eight waves and two steps were as fast or faster than 4 or 16 waves and one
+// to four steps up to 4096 rows.  With many rows x is what costs (65536 x 6144, 16 tokens: 92 us).
+template <typename XT, int WF, int NX, int W>
 __global__ __launch_bounds__(64 * W) void k_linear_ring(LinArgs a) {
     constexpr int UB = LinFmt<WF>::UB, SPD = LinFmt<WF>::SPD;
-    constexpr int STG = (1 + NX) * 1024, SCB = NMAX / SPD * 256, WB = SCB + D * STG;
-    constexpr bool F32 = sizeof(XT) == 4;
+    constexpr int STG = (1 + NX) * 1024, SCB = 2 * 256, WB = SCB + 2 * STG;
+    constexpr bool F32 = sizeof(XT) == 4, TERMS = F32 && NX <= 3;
     constexpr int TB = 128 * (int)sizeof(XT), TPL = 1024 / TB;  // bytes of a token's step, tokens of one load
-    static_assert(NMAX % SPD == 0 && WB >= 1024, "a wave's sums fit into its ring");
-    __shared__ __align__(16) uint8_t ring[W * WB];
+    constexpr int C = !F32 && NX > 4 ? 2 : 1, PASS = TERMS ? 5 : 16 * C;
+    static_assert(SPD >= 2 && WB >= 1024 * C, "scales outlast the steps in flight; a wave's sums fit into its ring");
+    __shared__ __align__(32) uint8_t ring[W * WB];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int tile = blockIdx.x, NS = a.K / 128;
     const int s0 = wave * NS / W, n = (wave + 1) * NS / W - s0;
-    const int t0 = blockIdx.y * kLinPass<XT>, nt = a.T - t0 < kLinPass<XT> ? a.T - t0 : kLinPass<XT>;
+    const int t0 = blockIdx.y * PASS, nt = a.T - t0 < PASS ? a.T - t0 : PASS;
     uint8_t* mine = ring + wave * WB;
     const uint8_t* qs = lin_src(a, tile, s0, lane);
     const uint8_t* xs[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
         const int t = TPL * i + lane / (64 / TPL), tok = t0 + (t < nt ? t : nt - 1);
-        xs[i] = (const uint8_t*)a.x + ((size_t)tok * a.K + (size_t)s0 * 128) * sizeof(XT) + ((lane % (64 / TPL)) ^ t) * 16;
+        xs[i] = (const uint8_t*)a.x + ((size_t)tok * a.K + (size_t)s0 * 128) * sizeof(XT) + ((lane % (64 / TPL)) ^ (t & 15)) * 16;
     }
-    auto issue = [&](int k, int slot) {
-        uint8_t* st = mine + SCB + slot * STG;
+    auto issue = [&](int k) {
+        uint8_t* st = mine + SCB + (k & 1) * STG;
+        if (k % SPD == 0) lin_dma_scales<WF>(a, tile, s0, k / SPD, lane, mine + (k / SPD & 1) * 256);
         dma16(qs + (size_t)k * 64, st);
 #pragma unroll
         for (int i = 0; i < NX; ++i) dma16(xs[i] + (size_t)k * TB, st + (1 + i) * 1024);
     };
-    for (int i = 0; i * SPD < n; ++i) lin_dma_scales<WF>(a, tile, s0, i, lane, mine + i * 256);
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-        if (i < n) issue(i, i);
+    if (n > 0) issue(0);
+    if (n > 1) issue(1);
     const uint32_t base = lin_lds_offset(mine);
     const uint32_t qa = base + SCB + li * 64 + (lg ^ lin_swz(li)) * 16, sa = base + li * 16 + lg * (UB / 4);
     uint32_t xa[4];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {                              // columns past the last repeat a token
-        const int t = F32 ? li / 3 % (TPL * NX) : li % (TPL * NX);
+        const int t = TERMS ? li / 3 % (TPL * NX) : li % (TPL * NX);
         xa[h] = base + SCB + 1024 + t * TB + ((F32 ? 8 * lg + 2 * h : 4 * lg + h) ^ t) * 16;
     }
     const uint32_t m1 = li % 3 > 0 ? 0xffff0000u : 0u, m2 = li % 3 > 1 ? 0xffff0000u : 0u;
-    lin_f32x4 acc[2] = {lin_f32x4{0.f, 0.f, 0.f, 0.f}, lin_f32x4{0.f, 0.f, 0.f, 0.f}};
-    int slot = 0;
+    lin_f32x4 acc[C][2];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c][0] = acc[c][1] = lin_f32x4{0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < n; ++k) {
-        lin_wait_upto<(D - 1) * (1 + NX)>((n - 1 - k < D - 1 ? n - 1 - k : D - 1) * (1 + NX));
+        if (k + 1 == n) wait_vm<0>();                          // all but the next step's loads are here
+        else if ((k + 1) % SPD == 0) wait_vm<2 + NX>();
+        else wait_vm<1 + NX>();
         lin_u32x4 code, x[4], x2[4];
         uint32_t sc;
-        const uint32_t so = slot * STG, sk = sa + k / SPD * 256 + k % SPD * UB;
-        if constexpr (F32)             // the other 16 bytes of a lane's 8 values are in the neighbouring slot
+        const uint32_t so = (k & 1) * STG, sk = sa + (k / SPD & 1) * 256 + k % SPD * UB;
+        if constexpr (F32 || C == 2) {
+            // the other 16 bytes of a lane's 8 fp32 values are in the neighbouring slot, the other 16 tokens a
+            // step of 16 tokens on
+            const uint32_t f = F32 ? 16 : 0, o = so + (C == 2 ? 16 * TB : 0);
             asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
                          "s_waitcnt lgkmcnt(0)"
                          : "=&v"(x2[0]), "=&v"(x2[1]), "=&v"(x2[2]), "=&v"(x2[3])
-                         : "v"((xa[0] + so) ^ 16), "v"((xa[1] + so) ^ 16), "v"((xa[2] + so) ^ 16), "v"((xa[3] + so) ^ 16)
+                         : "v"((xa[0] + o) ^ f), "v"((xa[1] + o) ^ f), "v"((xa[2] + o) ^ f), "v"((xa[3] + o) ^ f)
                          : "memory");
+        }
         if constexpr (WF == MOE_WF_MXFP4)
             asm volatile("ds_read_b128 %0, %6\n\tds_read_u8 %1, %7\n\tds_read_b128 %2, %8\n\tds_read_b128 %3, %9\n\t"
                          "ds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\ts_waitcnt lgkmcnt(0)"
@@ -413,25 +379,41 @@ __global__ __launch_bounds__(64 * W) void k_linear_ring(LinArgs a) {
                          : "=&v"(code), "=&v"(sc), "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
                          : "v"(qa + so), "v"(sk), "v"(xa[0] + so), "v"(xa[1] + so), "v"(xa[2] + so), "v"(xa[3] + so)
                          : "memory");
-        if (k + D < n) issue(k + D, slot);
-        slot = slot + 1 == D ? 0 : slot + 1;
+        if (k + 2 < n) issue(k + 2);
         float s2[2];
         lin_scales<WF>(sc, s2);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            lin_bf16x8 xv;
-            if constexpr (F32) xv = lin_f32_term(x[h], x2[h], m1, m2);
-            else __builtin_memcpy(&xv, &x[h], 16);
-            acc[h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lin_weights<WF>(code[h], s2[h / 2]), xv, acc[h & 1], 0, 0, 0);
+            const lin_bf16x8 w = lin_weights<WF>(code[h], s2[h / 2]);
+            if constexpr (TERMS) {
+                acc[0][h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, lin_f32_term(x[h], x2[h], m1, m2), acc[0][h & 1], 0, 0, 0);
+            } else if constexpr (F32) {
+                lin_bf16x8 t[3];
+                lin_f32_terms(x[h], x2[h], t);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) acc[0][h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, t[i], acc[0][h & 1], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    lin_bf16x8 xv;
+                    __builtin_memcpy(&xv, c ? &x2[h] : &x[h], 16);
+                    acc[c][h & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xv, acc[c][h & 1], 0, 0, 0);
+                }
+            }
         }
     }
-    acc[0] += acc[1];
-    mfma_results_here(acc[0]);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        acc[c][0] += acc[c][1];
+        mfma_results_here(acc[c][0]);
+    }
     __syncthreads();
     lin_f32x4* part = (lin_f32x4*)ring;
-    part[wave * 64 + lane] = acc[0];
+#pragma unroll
+    for (int c = 0; c < C; ++c) part[(c * W + wave) * 64 + lane] = acc[c][0];
     __syncthreads();
-    if (wave == 0 && li < nt) lin_store<XT>(a, t0 + li, tile * 16 + 4 * lg, lin_sum_waves<XT, W>(part, lane));
+    if (wave < C && 16 * wave + li < nt)
+        lin_store<XT>(a, t0 + 16 * wave + li, tile * 16 + 4 * lg, lin_sum_waves<TERMS, W>(part + wave * W * 64, lane));
 }
 
 // Tiles of 16 rows blockIdx.x, blockIdx.x + G, .. (G workgroups); wave w of 8 takes K slice w of every
@@ -562,14 +544,161 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear_stream(LinArgs a, int
         lds_barrier();
         const int j = it / R * R + wave;                       // the round's tile that this wave adds up
         if (j <= it && wave < R && li < nt)
-            lin_store<XT>(a, t0 + li, (blockIdx.x + j * G) * 16 + 4 * lg, lin_sum_waves<XT, W>(&part[wave][0][0], lane));
+            lin_store<XT>(a, t0 + li, (blockIdx.x + j * G) * 16 + 4 * lg, lin_sum_waves<F32, W>(&part[wave][0][0], lane));
         lds_barrier();                                         // the next round overwrites the sums
     }
 }
 
+// N 16-byte reads of LDS, STRIDE apart
+template <int N, int STRIDE>
+__device__ __forceinline__ void lin_read(uint32_t at, lin_u32x4 (&v)[N]) {
+    static_assert(N == 2 || N == 4 || N == 6, "numbers of reads that the tile kernel makes");
+    if constexpr (N == 2)
+        asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0]), "=&v"(v[1]) : "v"(at), "n"(STRIDE) : "memory");
+    else if constexpr (N == 4)
+        asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%5\n\tds_read_b128 %2, %4 offset:%6\n\t"
+                     "ds_read_b128 %3, %4 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                     : "v"(at), "n"(STRIDE), "n"(2 * STRIDE), "n"(3 * STRIDE) : "memory");
+    else
+        asm volatile("ds_read_b128 %0, %6\n\tds_read_b128 %1, %6 offset:%7\n\tds_read_b128 %2, %6 offset:%8\n\t"
+                     "ds_read_b128 %3, %6 offset:%9\n\tds_read_b128 %4, %6 offset:%10\n\tds_read_b128 %5, %6 offset:%11\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5])
+                     : "v"(at), "n"(STRIDE), "n"(2 * STRIDE), "n"(3 * STRIDE), "n"(4 * STRIDE), "n"(5 * STRIDE) : "memory");
+}
+
+// Many rows and many tokens: 16 F rows per wave, eight waves over rows, and 16 C tokens, whose step of x the
+// waves share in LDS; each wave has its own ring of codes and scales.  S steps alive, one barrier a step.
+// fp32 x is cut into its terms once per workgroup and step, each wave the part that it loaded.
+// 65536 x 6144 MXFP4, bf16: 32 tokens 50 us, 64 68; fp32: 102 and 199 (at the matrix cores' 1.23 PFLOP/s 63 and
+// 126).  With the workgroups' rows on few CUs a step's chain of LDS reads, decode, products and barrier (0.5 us)
+// bounds it: steps of 256 K, all of a step's reads at once or four stages for three took as long; sixteen waves
+// that share out a step's K took 22 us for 27 at 16384 x 4096 and 64 tokens, but 82 for 68 at 65536 x 6144.
+template <typename XT, int WF, int C, int F, int S>
+__global__ __launch_bounds__(512) void k_linear_tile(LinArgs a) {
+    constexpr int UB = LinFmt<WF>::UB, SPD = LinFmt<WF>::SPD, W = 8;
+    constexpr bool F32 = sizeof(XT) == 4;
+    constexpr int NT = F32 ? 3 : 1;
+    constexpr int TB = 128 * (int)sizeof(XT), TPL = 1024 / TB;  // bytes of a token's step, tokens of one load
+    constexpr int XL = 16 * C / TPL / W;                        // loads of x per wave and step
+    constexpr int XSTG = 16 * C * TB, TERMS = F32 ? NT * C * 4096 : 0;
+    constexpr int SL = S == 3 ? 2 : 4;                          // loads of scales that are alive
+    constexpr int CW = S * F * 1024 + SL * F * 256, P = F + XL;
+    static_assert(XL >= 1 && (!F32 || XL == 2) && SPD >= 2 && (S == 3 || S == 4), "shares of the loads; scales outlast them");
+    __shared__ __align__(1024) uint8_t lds[S * XSTG + 2 * TERMS + W * CW];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int tile = (blockIdx.x * W + wave) * F, n = a.K / 128;
+    const int t0 = blockIdx.y * 16 * C, nt = a.T - t0 < 16 * C ? a.T - t0 : 16 * C;
+    uint8_t* mine = lds + S * XSTG + 2 * TERMS + wave * CW;
+    const uint8_t* qs[F];
+    const uint8_t* xs[XL];
+#pragma unroll
+    for (int f = 0; f < F; ++f) qs[f] = lin_src(a, tile + f, 0, lane);
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {                              // fp32 in order, bf16 swizzled by token
+        const int t = (wave * XL + i) * TPL + lane / (64 / TPL), tok = t0 + (t < nt ? t : nt - 1);
+        xs[i] = (const uint8_t*)a.x + (size_t)tok * a.K * sizeof(XT) + (F32 ? lane % 32 : (lane % 16) ^ (t & 15)) * 16;
+    }
+    int slot_in = 0;                                           // of the next step to request
+    auto issue = [&](int k) {
+        if (k % SPD == 0)
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+                lin_dma_scales<WF>(a, tile + f, 0, k / SPD, lane, mine + S * F * 1024 + ((k / SPD % SL) * F + f) * 256);
+#pragma unroll
+        for (int f = 0; f < F; ++f) dma16(qs[f] + (size_t)k * 64, mine + (slot_in * F + f) * 1024);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) dma16(xs[i] + (size_t)k * TB, lds + slot_in * XSTG + (wave * XL + i) * 1024);
+        slot_in = slot_in + 1 == S ? 0 : slot_in + 1;
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        if (k < n) issue(k);
+    const uint32_t base = lin_lds_offset(lds), my = lin_lds_offset(mine);
+    const uint32_t qa = my + li * 64 + (lg ^ lin_swz(li)) * 16, sa = my + S * F * 1024 + li * 16 + lg * (UB / 4);
+    uint32_t xa[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) xa[h] = base + (F32 ? S * XSTG : 0) + li * 256 + ((4 * lg + h) ^ li) * 16;
+    lin_f32x4 acc[F][C];
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[f][c] = lin_f32x4{0.f, 0.f, 0.f, 0.f};
+    int slot = 0;
+    for (int k = 0; k < n; ++k) {
+        if (k + S - 2 >= n) wait_vm<0>();                      // all but the loads of the steps behind are here
+        else if constexpr (S == 3) {
+            if ((k + 1) % SPD == 0) wait_vm<P + F>();
+            else wait_vm<P>();
+        } else {
+            if ((k + 1) % SPD == 0 || (k + 2) % SPD == 0) wait_vm<2 * P + F>();
+            else wait_vm<2 * P>();
+        }
+        if constexpr (F32) {
+            const uint32_t raw = base + slot * XSTG + wave * 2048 + lane * 32;
+            lin_u32x4 v[2];
+            lin_read<2, 16>(raw, v);
+            lin_bf16x8 t[3];
+            lin_f32_terms(v[0], v[1], t);
+            const int tk = 4 * wave + lg;                      // the lane's token and 8 values
+            const uint32_t to = base + S * XSTG + (k & 1) * TERMS + tk * 256 + (li ^ (tk & 15)) * 16;
+            lin_u32x4 w[3];
+            __builtin_memcpy(w, t, 48);
+            asm volatile("ds_write_b128 %0, %1\n\tds_write_b128 %0, %2 offset:%4\n\tds_write_b128 %0, %3 offset:%5\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         :: "v"(to), "v"(w[0]), "v"(w[1]), "v"(w[2]), "n"(C * 4096), "n"(2 * C * 4096) : "memory");
+        }
+        lds_barrier();
+        if (k + S - 1 < n) issue(k + S - 1);
+        const uint32_t xo = F32 ? (k & 1) * TERMS : slot * XSTG;
+        lin_u32x4 code[F];
+        float s2[F][2];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            uint32_t sc;
+            const uint32_t sk = sa + ((k / SPD % SL) * F + f) * 256 + k % SPD * UB;
+            if constexpr (WF == MOE_WF_MXFP4)
+                asm volatile("ds_read_b128 %0, %2\n\tds_read_u8 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(code[f]), "=&v"(sc) : "v"(qa + (slot * F + f) * 1024), "v"(sk) : "memory");
+            else
+                asm volatile("ds_read_b128 %0, %2\n\tds_read_u16 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                             : "=&v"(code[f]), "=&v"(sc) : "v"(qa + (slot * F + f) * 1024), "v"(sk) : "memory");
+            lin_scales<WF>(sc, s2[f]);
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            lin_u32x4 x[C * NT];
+            lin_read<C * NT, 4096>(xa[h] + xo, x);
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const lin_bf16x8 w = lin_weights<WF>(code[f][h], s2[f][h / 2]);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        lin_bf16x8 xv;
+                        __builtin_memcpy(&xv, &x[i * C + c], 16);
+                        acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xv, acc[f][c], 0, 0, 0);
+                    }
+            }
+        }
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            mfma_results_here(acc[f][c]);
+            if (16 * c + li < nt) lin_store<XT>(a, t0 + 16 * c + li, (tile + f) * 16 + 4 * lg, acc[f][c]);
+        }
+}
+
 template <typename XT, int WF, int NX>
 static void ring_launch(const LinArgs& a, int passes, hipStream_t st) {
-    MOE_LAUNCH((k_linear_ring<XT, WF, NX, 8, 2, 8>), dim3((a.N + 15) / 16, passes), dim3(512), 0, st, a);
+    MOE_LAUNCH((k_linear_ring<XT, WF, NX, 8>), dim3((a.N + 15) / 16, passes), dim3(512), 0, st, a);
 }
 
 template <typename XT, int WF>
@@ -581,41 +710,54 @@ static void stream_launch(const LinArgs& a, int passes, hipStream_t st) {
     else MOE_LAUNCH((k_linear_stream<XT, WF, 8>), grid, block, 0, st, a, ntiles);
 }
 
-template <typename XT, int WF, int F, int C, int W, int D>
-static void plain_launch(const LinArgs& a, hipStream_t st) {
-    MOE_LAUNCH((k_linear<XT, WF, F, C, W, D>), dim3((a.N + 16 * F - 1) / (16 * F), (a.T + 16 * C - 1) / (16 * C)),
-               dim3(64 * W), 0, st, a);
+template <typename XT, int WF, int C, int S>
+static void tile_launch_columns(const LinArgs& a, hipStream_t st) {
+    const int passes = (a.T + 16 * C - 1) / (16 * C);
+    if ((long long)(a.N + 255) / 256 * passes >= 256)
+        MOE_LAUNCH((k_linear_tile<XT, WF, C, 2, S>), dim3((a.N + 255) / 256, passes), dim3(512), 0, st, a);
+    else
+        MOE_LAUNCH((k_linear_tile<XT, WF, C, 1, S>), dim3((a.N + 127) / 128, passes), dim3(512), 0, st, a);
+}
+template <typename XT, int WF>
+static void tile_launch(const LinArgs& a, hipStream_t st) {
+    if constexpr (sizeof(XT) == 4) tile_launch_columns<XT, WF, 2, 3>(a, st);
+    else if (a.T <= 32) tile_launch_columns<XT, WF, 2, 4>(a, st);
+    else tile_launch_columns<XT, WF, 4, 4>(a, st);
 }
 
 template <typename XT, int WF>
 static void linear_launch(const LinArgs& a, hipStream_t st) {
-    // Many rows: x read once per CU (stream) against once per tile (ring), us, bf16.  8192 x 4096, 16 tokens:
-    // stream 9.6, ring 9.0; 16384 x 4096, 16 tokens 12.3, 19.5.  Four tokens, MXFP4: 16384 x 4096 10.2, 9.9;
-    // 32768 x 4096 16.3, 18.6; 65536 x 6144 41, 52.  One or two tokens: 18.0, 16.2 at 65536 x 2048, 41, 44 at
-    // 65536 x 6144 (NVFP4 50, 48).
-    const bool many = a.N >= 16384;
-    const int passes = (a.T + kLinPass<XT> - 1) / kLinPass<XT>;
-    if (a.K <= kLinDmaMaxK) {
-        if constexpr (sizeof(XT) == 2) {
-            if (many && (a.T > 4 || (a.T > 2 && (long long)a.N * a.K >= 1 << 27))) stream_launch<XT, WF>(a, passes, st);
-            else if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
-            else if (a.T <= 8) ring_launch<XT, WF, 2>(a, 1, st);
-            else ring_launch<XT, WF, 4>(a, passes, st);
-            return;
-        } else if (!many) {
-            if (a.T <= 2) ring_launch<XT, WF, 1>(a, 1, st);
-            else if (a.T <= 4) ring_launch<XT, WF, 2>(a, 1, st);
-            else ring_launch<XT, WF, 3>(a, passes, st);
-            return;
-        } else if (passes <= 2) {
-            stream_launch<XT, WF>(a, passes, st);
-            return;
-        }
+    // Many rows: x read once per CU (stream), once per workgroup of 128 or 256 rows (tile) or once per 16 rows
+    // (ring), us, MXFP4.  bf16, 16 tokens: 8192 x 4096 stream 9.6, ring 9.0; 16384 x 4096 10, 16; four tokens
+    // 32768 x 4096 16.3, 18.6; 65536 x 6144 41, 52; one or two tokens as fast either way.  32 tokens:
+    // 16384 x 4096 stream 17, tile 18; 32768 x 4096 tile 21; 65536 x 6144 71, 50; 64 tokens 16384 x 4096 31, 27.
+    // 32768 x 12288: 8 tokens ring 61, tile 52; 16 tokens 84, 51.  fp32, 8192 x 4096: 32 tokens ring 41, tile 45;
+    // 64 tokens 79, 45.
+    // Two fragments of 16 rows per wave once that fills the CUs: 65536 x 6144, 64 tokens 68 for 81, fp32 199
+    // for 258; 16384 x 4096 38 for 27, fp32 61 for 45.
+    // Few rows: 32 tokens in one pass, or 16 fp32 tokens (terms in turn) for five, once the passes no longer
+    // run side by side: 4096 x 4096, 32 tokens 6.9 for 7.8, 16 fp32 tokens 11.7 for 14.6; 512 x 2048 4.2 for 3.4
+    // and 6.7 for 4.2.
+    const int tiles = (a.N + 15) / 16;
+    const bool many = a.N >= 16384, most = a.N >= 32768, fit = a.K <= kLinStreamMaxK;
+    if constexpr (sizeof(XT) == 2) {
+        const int passes = (a.T + 15) / 16;
+        if (many && (a.T > 32 || (a.T > 16 && (most || !fit)) || (a.T > 8 && most && !fit))) tile_launch<XT, WF>(a, st);
+        else if (many && fit && (a.T > 4 || (a.T > 2 && (long long)a.N * a.K >= 1 << 27))) stream_launch<XT, WF>(a, passes, st);
+        else if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
+        else if (a.T <= 8) ring_launch<XT, WF, 2>(a, 1, st);
+        else if (a.T <= 16 || tiles * passes <= 256) ring_launch<XT, WF, 4>(a, passes, st);
+        else ring_launch<XT, WF, 8>(a, (a.T + 31) / 32, st);
+    } else {
+        const int passes = (a.T + 4) / 5;
+        if ((many && a.T > 16) || (a.N >= 8192 && a.T > 32)) tile_launch<XT, WF>(a, st);
+        else if (many && fit && a.T <= 10) stream_launch<XT, WF>(a, passes, st);
+        else if (many && a.T > 5) MOE_LAUNCH((k_linear<WF>), dim3((a.N + 63) / 64), dim3(512), 0, st, a);
+        else if (a.T <= 2) ring_launch<XT, WF, 1>(a, 1, st);
+        else if (a.T <= 4) ring_launch<XT, WF, 2>(a, 1, st);
+        else if (a.T <= 10 || tiles * passes <= 512) ring_launch<XT, WF, 3>(a, passes, st);
+        else ring_launch<XT, WF, 8>(a, (a.T + 15) / 16, st);
     }
-    if (a.T > 32) plain_launch<XT, WF, 2, 4, 4, 1>(a, st);
-    else if (a.T > 16) plain_launch<XT, WF, 2, 2, 4, 1>(a, st);
-    else if (many) plain_launch<XT, WF, 4, 1, 8, 1>(a, st);
-    else plain_launch<XT, WF, 1, 1, 8, 2>(a, st);
 }
 
 hipError_t launch_linear(const moe_matrix* m, const uint8_t* q, const uint8_t* s, float ts, const void* x, int T,

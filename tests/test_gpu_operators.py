@@ -386,6 +386,8 @@ LINEAR = [  # N, K, T
     (48, 512, 33), (31, 896, 64), (5000, 256, 7), (2048, 6144, 4), (4096, 512, 12), (40000, 128, 1), (9000, 384, 40), (515, 8192, 9),
     (20000, 640, 6), (16399, 8192, 13), (16384, 6144, 5), (33000, 256, 16), (300, 8320, 5), (16400, 8320, 3),
     (17000, 256, 20), (17000, 256, 40), (32770, 4096, 3), (300, 8320, 20), (300, 8320, 40),
+    (4100, 512, 64), (4099, 256, 16), (5000, 8448, 33), (16390, 1024, 16), (16400, 8320, 16), (17003, 1152, 40), (33001, 640, 25),
+    (32900, 256, 64), (65540, 384, 33), (65539, 128, 20), (32771, 8320, 9), (32768, 2432, 49),
 ]
 
 
@@ -405,21 +407,23 @@ def test_linear(N, K, T, act, wf):
 
 
 @pytest.mark.parametrize("N,K,T,act", [(256, 128, 16, BF16), (256, 128, 16, F32), (16640, 128, 16, BF16), (16640, 128, 8, F32),
-                                       (256, 8320, 16, BF16), (256, 8320, 16, F32)])
+                                       (256, 8320, 16, BF16), (256, 8320, 16, F32), (4352, 128, 32, BF16), (4352, 128, 16, F32),
+                                       (16640, 128, 16, F32), (32768, 8320, 16, BF16), (16640, 128, 48, BF16),
+                                       (16640, 128, 20, F32), (65536, 128, 40, BF16), (65536, 128, 32, F32)])
 def test_linear_scale_bytes(N, K, T, act):
     """Every code under every E8M0 byte whose weights are below 2^128, subnormal ones among them, and the NaN
-    byte: row n has all codes in block 1 under byte n, token t one value at code t, so y is that product (exact
+    byte: row n has all codes in block 1 under byte n, token t one value at code t % 16, so y is that product (exact
     where it is a normal number of the type)."""
     q = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
     s = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
     s[:, 1] = (torch.arange(N, device="cuda") % 256).to(torch.uint8)
     for j in range(8):
         q[:, 16 + j] = 2 * j | (2 * j + 1) << 4              # elements 32 .. 47: codes 0 .. 15
-    values = torch.tensor(ref.E2M1 + tuple(-v for v in ref.E2M1), dtype=torch.float64, device="cuda")[:T, None]
+    values = torch.tensor(ref.E2M1 + tuple(-v for v in ref.E2M1), dtype=torch.float64, device="cuda")[torch.arange(T) % 16, None]
     weight = values * torch.ldexp(torch.ones(N, dtype=torch.float64, device="cuda"), s[:, 1].int() - 127)
     for e in (60, -60):
         x = torch.zeros(T, K, dtype=act, device="cuda")
-        x[torch.arange(T), 32 + torch.arange(T)] = 2.0 ** e
+        x[torch.arange(T), 32 + torch.arange(T) % 16] = 2.0 ** e
         y = torch.empty(T, N, dtype=act, device="cuda")
         m.moe_linear(m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32), q, s, 1.0, x, T, None, y)
         want = weight * 2.0 ** e
@@ -431,8 +435,9 @@ def test_linear_scale_bytes(N, K, T, act):
 def test_linear_values_outside_the_numbers():
     """Infinity and NaN in x reach the rows whose weights see them, in that token alone."""
     g = gen(12)
-    T = 3
-    for N, K, act in ((40, 256, BF16), (40, 256, F32), (16390, 256, BF16), (16390, 256, F32), (40, 8320, BF16), (40, 8320, F32)):
+    for N, K, T, act in ((40, 256, 3, BF16), (40, 256, 3, F32), (16390, 256, 3, BF16), (16390, 256, 3, F32), (40, 8320, 3, BF16),
+                         (40, 8320, 3, F32), (4352, 256, 20, BF16), (4352, 256, 16, F32), (16390, 256, 16, F32),
+                         (16390, 256, 40, BF16), (16390, 256, 20, F32)):
         q, s, _ = quantised(g, N, K, 0)
         x = rand(g, T, K, dtype=act)
         mat = m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32)
@@ -440,16 +445,16 @@ def test_linear_values_outside_the_numbers():
         m.moe_linear(mat, q, s, 1.0, x, T, None, y)
         x[0, 200], x[2, 3] = float("inf"), float("nan")
         m.moe_linear(mat, q, s, 1.0, x, T, None, z)
-        assert torch.equal(z[1], y[1]) and torch.isnan(z[2]).all()
+        assert torch.equal(z[1], y[1]) and torch.equal(z[3:], y[3:]) and torch.isnan(z[2]).all()
         if act == F32:                                       # a NaN whose payload lies in the lower half
             x.view(torch.int32)[2, 3] = 0x7f800001
             m.moe_linear(mat, q, s, 1.0, x, T, None, z)
-            assert torch.equal(z[1], y[1]) and torch.isnan(z[2]).all()
+            assert torch.equal(z[1], y[1]) and torch.equal(z[3:], y[3:]) and torch.isnan(z[2]).all()
         w = ref.weights(q, s, 0)[:, 200]
         assert torch.equal(torch.isnan(z[0]), w == 0)        # 0 times infinity
         assert torch.equal(z[0][w != 0], (torch.sign(w) * float("inf")).to(act)[w != 0])
         # the largest finite values stay finite on the way
-        if act == F32 and N == 40 and K == 256:
+        if act == F32 and T == 3 and K == 256 and N == 40:
             x = torch.zeros(1, K, device="cuda")
             x[0, 7] = torch.finfo(F32).max
             small_s = torch.full_like(s, 100)
