@@ -24,8 +24,8 @@
 //                    its workgroup takes, so x is read once per CU;
 //   k_linear_tile    many rows and more tokens than the registers hold: the waves of a workgroup share x's
 //                    step in LDS;
-//   k_linear         many rows and up to 16 fp32 tokens past the stream's, straight from global memory to
-//                    registers.
+//   k_linear         many rows and up to 16 fp32 tokens, more than the stream's or of short rows, straight
+//                    from global memory to registers.
 #include "block_ops.h"
 
 namespace moe {
@@ -728,13 +728,16 @@ static void tile_launch(const LinArgs& a, hipStream_t st) {
 template <typename XT, int WF>
 static void linear_launch(const LinArgs& a, hipStream_t st) {
     // Many rows: x read once per CU (stream), once per workgroup of 128 or 256 rows (tile) or once per 16 rows
-    // (ring), us, MXFP4.  bf16, 16 tokens: 8192 x 4096 stream 9.6, ring 9.0; 16384 x 4096 10, 16; four tokens
-    // 32768 x 4096 16.3, 18.6; 65536 x 6144 41, 52; one or two tokens as fast either way.  32 tokens:
-    // 16384 x 4096 stream 17, tile 18; 32768 x 4096 tile 21; 65536 x 6144 71, 50; 64 tokens 16384 x 4096 31, 27.
-    // 32768 x 12288: 8 tokens ring 61, tile 52; 16 tokens 84, 51.  fp32, 8192 x 4096: 32 tokens ring 41, tile 45;
-    // 64 tokens 79, 45.
-    // Two fragments of 16 rows per wave once that fills the CUs: 65536 x 6144, 64 tokens 68 for 81, fp32 199
-    // for 258; 16384 x 4096 38 for 27, fp32 61 for 45.
+    // (ring), us, MXFP4.
+    //   bf16, 16 tokens: 8192 x 4096 stream 9.6, ring 9.0; 16384 x 4096 10, 16.  Four tokens: 32768 x 4096 16.3,
+    //   18.6; 65536 x 6144 41, 52; one or two as fast either way.  Eight tokens of short rows: 49699 x 768 12.8,
+    //   10.2; 65536 x 2048 18, 22.
+    //   32 tokens: 16384 x 4096 stream 17, tile 18; 65536 x 6144 71, 50; 64 tokens: 16384 x 4096 31, 27.
+    //   Long rows, 32768 x 12288: 8 tokens ring 61, tile 52; 16 tokens 84, 51.
+    //   fp32, eight tokens: 49699 x 768 stream 27, k_linear 13; 65536 x 2048 35, 39; five: 15, 12; 19, 35.
+    //   fp32, 8192 x 4096: 32 tokens ring 41, tile 45; 64 tokens 79, 45.
+    // Two fragments of 16 rows per wave of a tile once that fills the CUs: 65536 x 6144, 64 tokens 68 for 81, fp32
+    // 199 for 258; 16384 x 4096 38 for 27, fp32 61 for 45.
     // Few rows: 32 tokens in one pass, or 16 fp32 tokens (terms in turn) for five, once the passes no longer
     // run side by side: 4096 x 4096, 32 tokens 6.9 for 7.8, 16 fp32 tokens 11.7 for 14.6; 512 x 2048 4.2 for 3.4
     // and 6.7 for 4.2.
@@ -743,7 +746,8 @@ static void linear_launch(const LinArgs& a, hipStream_t st) {
     if constexpr (sizeof(XT) == 2) {
         const int passes = (a.T + 15) / 16;
         if (many && (a.T > 32 || (a.T > 16 && (most || !fit)) || (a.T > 8 && most && !fit))) tile_launch<XT, WF>(a, st);
-        else if (many && fit && (a.T > 4 || (a.T > 2 && (long long)a.N * a.K >= 1 << 27))) stream_launch<XT, WF>(a, passes, st);
+        else if (many && fit && (a.T > 8 || (a.T > 4 && a.K >= 2048) || (a.T > 2 && (long long)a.N * a.K >= 1 << 27)))
+            stream_launch<XT, WF>(a, passes, st);
         else if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
         else if (a.T <= 8) ring_launch<XT, WF, 2>(a, 1, st);
         else if (a.T <= 16 || tiles * passes <= 256) ring_launch<XT, WF, 4>(a, passes, st);
@@ -751,8 +755,8 @@ static void linear_launch(const LinArgs& a, hipStream_t st) {
     } else {
         const int passes = (a.T + 4) / 5;
         if ((many && a.T > 16) || (a.N >= 8192 && a.T > 32)) tile_launch<XT, WF>(a, st);
-        else if (many && fit && a.T <= 10) stream_launch<XT, WF>(a, passes, st);
-        else if (many && a.T > 5) MOE_LAUNCH((k_linear<WF>), dim3((a.N + 63) / 64), dim3(512), 0, st, a);
+        else if (many && fit && a.T <= 10 && a.K >= (a.T <= 5 ? 1024 : 2048)) stream_launch<XT, WF>(a, passes, st);
+        else if (many && (a.T > 5 || fit)) MOE_LAUNCH((k_linear<WF>), dim3((a.N + 63) / 64), dim3(512), 0, st, a);
         else if (a.T <= 2) ring_launch<XT, WF, 1>(a, 1, st);
         else if (a.T <= 4) ring_launch<XT, WF, 2>(a, 1, st);
         else if (a.T <= 10 || tiles * passes <= 512) ring_launch<XT, WF, 3>(a, passes, st);

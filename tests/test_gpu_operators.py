@@ -387,7 +387,7 @@ LINEAR = [  # N, K, T
     (20000, 640, 6), (16399, 8192, 13), (16384, 6144, 5), (33000, 256, 16), (300, 8320, 5), (16400, 8320, 3),
     (17000, 256, 20), (17000, 256, 40), (32770, 4096, 3), (300, 8320, 20), (300, 8320, 40),
     (4100, 512, 64), (4099, 256, 16), (5000, 8448, 33), (16390, 1024, 16), (16400, 8320, 16), (17003, 1152, 40), (33001, 640, 25),
-    (32900, 256, 64), (65540, 384, 33), (65539, 128, 20), (32771, 8320, 9), (32768, 2432, 49),
+    (32900, 256, 64), (65540, 384, 33), (65539, 128, 20), (32771, 8320, 9), (32768, 2432, 49), (16390, 2176, 8),
 ]
 
 
@@ -409,7 +409,8 @@ def test_linear(N, K, T, act, wf):
 @pytest.mark.parametrize("N,K,T,act", [(256, 128, 16, BF16), (256, 128, 16, F32), (16640, 128, 16, BF16), (16640, 128, 8, F32),
                                        (256, 8320, 16, BF16), (256, 8320, 16, F32), (4352, 128, 32, BF16), (4352, 128, 16, F32),
                                        (16640, 128, 16, F32), (32768, 8320, 16, BF16), (16640, 128, 48, BF16),
-                                       (16640, 128, 20, F32), (65536, 128, 40, BF16), (65536, 128, 32, F32)])
+                                       (16640, 128, 20, F32), (65536, 128, 40, BF16), (65536, 128, 32, F32),
+                                       (16640, 2048, 8, F32)])
 def test_linear_scale_bytes(N, K, T, act):
     """Every code under every E8M0 byte whose weights are below 2^128, subnormal ones among them, and the NaN
     byte: row n has all codes in block 1 under byte n, token t one value at code t % 16, so y is that product (exact
@@ -437,7 +438,7 @@ def test_linear_values_outside_the_numbers():
     g = gen(12)
     for N, K, T, act in ((40, 256, 3, BF16), (40, 256, 3, F32), (16390, 256, 3, BF16), (16390, 256, 3, F32), (40, 8320, 3, BF16),
                          (40, 8320, 3, F32), (4352, 256, 20, BF16), (4352, 256, 16, F32), (16390, 256, 16, F32),
-                         (16390, 256, 40, BF16), (16390, 256, 20, F32)):
+                         (16390, 256, 40, BF16), (16390, 256, 20, F32), (16390, 2048, 16, BF16), (16390, 2048, 8, F32)):
         q, s, _ = quantised(g, N, K, 0)
         x = rand(g, T, K, dtype=act)
         mat = m.make_matrix(N, K, 0, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32)
