@@ -203,22 +203,23 @@ hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t 
 // ---------------------------------------------------------------------------------------------
 // Groups: a row's chain of three sums takes about 2 us, so a CU needs some 64 KB of rows at once to keep its
 // share of HBM busy: one workgroup per CU for long rows, up to eight for short ones.  More only add partial sums
-// to write and read (4096 rows, 256 / 512 groups: d 4096 bf16 55 / 60 us, d 1024 41 / 28).  Up to four
-// rows one workgroup takes them all and no second kernel runs.
+// to write and read (4096 rows, 256 / 512 groups: d 4096 bf16 55 / 60 us, d 1024 41 / 28).  Up to two
+// rows one workgroup takes them all and no second kernel runs (d 4096 bf16: 2, 3, 4 rows 7.2, 9.5, 11.8 us, in
+// groups 7.7).
 static int norm_groups_cap(const moe_shape* s) {
     const int row = 8 * s->d_model * (s->act_dtype == MOE_DT_BF16 ? 2 : 4);       // bytes of a row, in and out
     return 256 * (row >= 65536 ? 1 : 65536 / row < 8 ? (65536 + row - 1) / row : 8);
 }
 
 static int norm_grad_groups(const moe_shape* s, int T) {
-    if (T <= 4) return 1;
+    if (T <= 2) return 1;
     const int cap = norm_groups_cap(s), rows = (T + cap - 1) / cap;
     return (T + rows - 1) / rows;
 }
 
 int norm_grad_groups_most(const moe_shape* s, int T) {
     const int cap = norm_groups_cap(s);
-    return T <= 4 ? 1 : T < cap ? T : cap;
+    return T <= 2 ? 1 : T < cap ? T : cap;
 }
 
 // One row's loads, as they come: requested for the next row while this one is worked on
