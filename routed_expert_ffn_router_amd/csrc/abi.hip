@@ -542,11 +542,13 @@ moe_status moe_block_norm_backward(const moe_shape* s, const void* x, const void
     g.d_post = d_post_gamma;
     g.d_pre = d_pre_gamma;
     if (T == 0 && !d_post_gamma && !d_pre_gamma) return MOE_OK;
+    // written whatever T is
+    if ((d_post_gamma && !aligned(d_post_gamma, 16)) || (d_pre_gamma && !aligned(d_pre_gamma, 16))) return MOE_ERR_INVALID;
+    if (d_post_gamma == d_pre_gamma && d_post_gamma) return MOE_ERR_INVALID;
     if (T > 0) {
         if (!x || !ws || (!d_x_out && !d_normed)) return MOE_ERR_INVALID;
         const void* in[] = {x, y, d_x_out, d_normed, gate_kind == MOE_GATE_ELEMENT ? gate : nullptr, dx, dy,
-                            gate_kind == MOE_GATE_ELEMENT ? d_gate : nullptr, post_gamma, pre_gamma, d_post_gamma,
-                            d_pre_gamma};
+                            gate_kind == MOE_GATE_ELEMENT ? d_gate : nullptr, post_gamma, pre_gamma};
         for (const void* p : in)
             if (p && !aligned(p, 16)) return MOE_ERR_INVALID;
         if (!aligned(ws, 256)) return MOE_ERR_INVALID;
