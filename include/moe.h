@@ -145,8 +145,9 @@ size_t moe_blob_stride(const moe_shape *shape);
 #define MOE_WS_ROUTE_TIMEOUT 0x1u
 #define MOE_WS_BAD_EXPERT_ID 0x2u
 
-/* Bytes of workspace the entry points need for T tokens (moe_layer needs the most; every
- * other call needs no more).  Returns 0 for a bad shape or T. */
+/* Bytes of workspace that any entry point needs for T tokens or fewer: the largest of moe_layer's
+ * (no other call needs more, but for moe_block_norm_backward, whose partial sums can, where rows are
+ * wide and top_k and d_ff small) over those token counts.  Returns 0 for a bad shape or T. */
 size_t moe_workspace_bytes(const moe_shape *shape, int32_t T);
 
 /* Prepare a workspace before its first use, or again after a nonzero status: clears the status

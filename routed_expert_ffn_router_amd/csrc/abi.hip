@@ -110,6 +110,20 @@ static size_t norm_scratch_bytes(const moe_shape* s, int32_t T) {
     return align256(8 * (size_t)norm_grad_groups_most(s, T) * s->d_model);
 }
 
+// bytes that the calls with T tokens need
+static size_t call_bytes(const moe_shape* s, int32_t T) {
+    const WsLayout L = ws_layout(s, T);
+    const size_t norm_end = norm_scratch(L) + norm_scratch_bytes(s, T);
+    return L.total > norm_end ? L.total : norm_end;
+}
+
+// Those bytes grow with the tokens in every range of token counts with one split of the router's sums and one tile
+// of the expert products, and may fall from one range to the next.
+static bool same_growth(const moe_shape* s, int32_t a, int32_t b) {
+    return logits_splits(s, a) == logits_splits(s, b) && gemm_variant(s, a) == gemm_variant(s, b) &&
+           (a <= kSmallTokens) == (b <= kSmallTokens);
+}
+
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 static moe_status check_shape(const moe_shape* s) {
@@ -360,9 +374,19 @@ size_t moe_blob_stride(const moe_shape* s) {
 
 size_t moe_workspace_bytes(const moe_shape* s, int32_t T) {
     if (check_shape(s) != MOE_OK || check_T(s, T) != MOE_OK) return 0;
-    const WsLayout L = ws_layout(s, T);
-    const size_t norm_end = norm_scratch(L) + norm_scratch_bytes(s, T);
-    return L.total > norm_end ? L.total : norm_end;
+    size_t most = call_bytes(s, T);
+    for (int t = T; t > 0;) {                  // the last token count of every other such range below T
+        int lo = 0, hi = t;                    // the first of t's range is in (lo, hi]
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (same_growth(s, mid, t)) hi = mid;
+            else lo = mid;
+        }
+        t = hi - 1;
+        const size_t n = call_bytes(s, t);
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 moe_status moe_workspace_init(const moe_shape* s, int32_t T, void* ws, size_t ws_bytes, int32_t poll_limit,
