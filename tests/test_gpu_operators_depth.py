@@ -1,0 +1,159 @@
+"""The operators around the experts where their loops run past the first fill: products whose rings and stages wrap, in
+integers that every order of summing gives exactly; norm gradients of many rows to a workgroup; values outside the numbers in
+the gradients; and what no pick has, which must not reach any result."""
+import pytest
+import torch
+
+import block_ref as ref
+import test_gpu_operators as ops
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import routed_expert_ffn_router_amd as m      # must load: no fallback path exists
+
+F32, BF16 = torch.float32, torch.bfloat16
+EPS = ops.EPS
+
+# N, K, T: one to sixteen row tiles to a workgroup, one to 65 steps of 128 columns, waves with unequal shares of them
+DEEP = [
+    (16390, 8192, 5), (16390, 7040, 9), (16390, 4736, 3), (16390, 8192, 16), (20011, 5888, 12), (65540, 2432, 5), (65540, 2432, 9),
+    (65540, 2432, 16), (65540, 2432, 20), (65540, 2432, 33), (65540, 2432, 49), (32900, 2432, 64), (16400, 4224, 40),
+    (16400, 8448, 16), (33001, 8320, 24), (9000, 4224, 40), (4099, 4224, 16), (4099, 4224, 33), (515, 8192, 64), (300, 16384, 2),
+    (300, 16384, 7), (16384, 8320, 5),
+]
+
+
+def matrix(N, K, wf, act):
+    return m.make_matrix(N, K, wf, m.MOE_DT_BF16 if act == BF16 else m.MOE_DT_F32)
+
+
+def linear_bound(q, s, wf, ts, x, bias):
+    """The float64 product with the bound of any order of summing: a product passes at most one addition for every column and
+    term (fp32 x has three terms), and sixteen more where waves share out the columns."""
+    W, x64 = ref.weights(q, s, wf), x.double()
+    depth = W.shape[1] * (3 if x.dtype == F32 else 1) + 16
+    y, mag = x64 @ W.t().contiguous(), x64.abs() @ W.abs().t().contiguous()
+    r = ref.Val(y, depth * ref.U * mag) * ref.alpha32(ts)
+    return r if bias is None else r + ref.Val(bias)
+
+
+@pytest.mark.parametrize("wf", [0, 1])
+@pytest.mark.parametrize("act", [BF16, F32])
+@pytest.mark.parametrize("N,K,T", DEEP)
+def test_linear_past_the_first_fill(N, K, T, act, wf):
+    """Random values within the bound, and integers to the bit: weights are multiples of 1/2 up to 12, so 16384 of them times
+    integers up to 7, or 64 of them times integers up to 4095 (two terms of an fp32 x; bf16 takes those up to 255), sum to
+    multiples of 1/2 below 2^23: exact in fp32 in any order."""
+    g = ops.gen(N + K + T)
+    q, s, ts = ops.quantised(g, N, K, wf)
+    x, bias, mat = ops.rand(g, T, K, dtype=act), ops.rand(g, N), matrix(N, K, wf, act)
+    y = torch.empty(T, N, dtype=act, device="cuda")
+    m.moe_linear(mat, q, s, ts, x, T, bias, y)
+    ref.check(y, linear_bound(q, s, wf, ts, x, bias), act, "y")
+    one, two = (127, 128) if wf == 0 else (0x38, 0x40)
+    s = torch.where(s % 2 == 0, one, two).to(torch.uint8)
+    W = ref.weights(q, s, wf)
+    dense = torch.randint(-7, 8, (T, K), generator=g, device="cuda")
+    most = 4095 if act == F32 else 255
+    big = torch.randint(-most, most + 1, (T, K), generator=g, device="cuda")
+    sparse = torch.where(torch.rand(T, K, generator=g, device="cuda").argsort(1) < 64, big, 0)
+    for xi in (dense, sparse):
+        m.moe_linear(mat, q, s, 1.0, xi.to(act), T, None, y)
+        want = xi.double() @ W.t().contiguous()
+        assert want.abs().max() < 2.0 ** 23
+        assert torch.equal(y, want.float().to(act))
+
+
+# ---------------------------------------------------------------------------------------------
+# norm gradients
+# ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,d,act,gate,post,y", [
+    (601, 6144, BF16, 2, 1, 1), (601, 6144, F32, 1, 1, 1), (300, 8192, F32, 1, 1, 1), (520, 8320, BF16, 2, 1, 1), (520, 8320, F32, 0, 1, 1),
+    (300, 16384, BF16, 1, 1, 1), (300, 16384, F32, 2, 1, 1), (2801, 6144, BF16, 2, 1, 1), (1401, 6144, F32, 2, 1, 1), (1400, 4224, BF16, 0, 0, 1),
+    (2049, 640, BF16, 1, 1, 1), (5000, 128, F32, 2, 1, 1), (700, 8192, BF16, 0, 0, 0),
+])
+def test_norm_gradients_of_many_rows(T, d, act, gate, post, y):
+    """Two to nineteen rows to a workgroup, so that its sums pass from row to row, with and without the next row requested ahead,
+    through the caches and past them."""
+    g, sh = ops.gen(32), ops.shape(d, act=act)
+    i, wide = ops.norm_inputs(g, T, d, act, gate, post, y)
+    dxo, dn = ops.rand(g, T, d, dtype=act), ops.rand(g, T, d, dtype=act)
+    ws = m.workspace(sh, T)
+    for a, b in ((dxo, dn), (dxo, None)) if y else ((dxo, dn),):
+        out = ops.norm_gradients(sh, i, T, d, act, gate, post, y, a, b, ws)
+        ops.check_gradients(out, ref.norm_backward(i["x"], i["y"], i["post"], i["pre"], wide, ops.ALPHA, EPS, a, b, gate == 1), act, gate)
+
+
+@pytest.mark.parametrize("T,d", [(5, 640), (600, 1152), (300, 8320)])
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_norm_gradients_keep_rows_apart(T, d, act):
+    """A row of zeros has finite gradients, and NaN or infinity in one row of any input reaches that row of the row gradients, the
+    gammas' gradients and nothing else."""
+    g, sh = ops.gen(33), ops.shape(d, act=act)
+    i, _ = ops.norm_inputs(g, T, d, act, 2, 1, 1)
+    up = {"a": ops.rand(g, T, d, dtype=act), "b": ops.rand(g, T, d, dtype=act)}
+    i["x"][1], i["y"][1] = 0.0, 0.0
+
+    def run(i, up):
+        return ops.norm_gradients(sh, i, T, d, act, 2, 1, 1, up["a"], up["b"])
+
+    clean = run(i, up)
+    assert all(torch.isfinite(v).all() for v in clean.values())
+    bad = 3
+    rest = torch.arange(T, device="cuda") != bad
+    for name in ("x", "y", "gate", "a", "b"):
+        for value in (float("nan"), float("inf")):
+            i2, up2 = dict(i), dict(up)
+            src = i2 if name in i2 else up2
+            src[name] = src[name].clone()
+            src[name][bad, 17] = value
+            out = run(i2, up2)
+            for k in ("dx", "dy", "d_gate"):
+                assert torch.equal(out[k][rest], clean[k][rest]), (name, value, k)
+            assert not torch.isfinite(out["dx"][bad, 17]), (name, value)
+
+
+# ---------------------------------------------------------------------------------------------
+# tokens by expert
+# ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,d,k,E,act,shared", [(5, 640, 3, 7, BF16, 1), (129, 384, 16, 64, F32, 0), (333, 1152, 8, 256, F32, 1),
+                                                (70, 4352, 8, 40, BF16, 0), (260, 256, 9, 33, BF16, 1)])
+def test_what_no_pick_has_reaches_no_result(T, d, k, E, act, shared):
+    """Rows past the last pick and the weights of dropped picks may hold anything: NaN there changes nothing, and NaN in a
+    row that a pick has stays with its token."""
+    g, sh = ops.gen(34), ops.shape(d, k, E, act, n_shared=shared, routed_scaling=2.5)
+    _, w, _, sp, pos = ops.routing(g, sh, T, True)
+    rows = T * (k + shared)
+    o, dxs, x = ops.rand(g, rows, d), ops.rand(g, rows, d, dtype=act), ops.rand(g, T, d, dtype=act)
+    pre = torch.ones(d, device="cuda")
+
+    def run(o, dxs, w):
+        out = {n: torch.zeros(s, dtype=t, device="cuda") for n, s, t in (("dx", (T, d), act), ("d_o", (rows, d), F32), ("d_w", (T, k), F32),
+                                                                           ("u", (T, d), act), ("n", (T, d), act), ("y", (T, d), act))}
+        m.moe_dispatch_backward(sh, dxs, T, pos, out["dx"])
+        m.moe_combine_backward(sh, x, o, w, pos, T, out["d_o"], out["d_w"])
+        m.moe_combine_norm(sh, o, w, pos, x, T, pre, pre, None, 0, 1.0, EPS, out["u"], out["n"])
+        m.moe_combine(sh, o, w, pos, T, None, out["y"])
+        return out
+
+    clean = run(o, dxs, w)
+    empty = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    empty[:T * k] = sp < 0
+    assert empty.any() and not (pos < 0).all()
+    o2, dxs2, w2 = o.clone(), dxs.clone(), w.clone()
+    o2[empty], dxs2[empty], w2[pos < 0] = float("nan"), float("nan"), float("nan")
+    out = run(o2, dxs2, w2)
+    for n, v in clean.items():
+        assert torch.equal(out[n], v), n
+    at = (pos >= 0).nonzero()[-1]                             # the last kept pick's row
+    t, row = int(at[0]), int(pos[at[0], at[1]])
+    rest = torch.arange(T, device="cuda") != t
+    o2[row, 5], dxs2[row, 5] = float("nan"), float("nan")
+    out = run(o2, dxs2, w2)
+    for n in ("dx", "d_w", "u", "n", "y"):
+        assert torch.equal(out[n][rest], clean[n][rest]), n
+    assert torch.equal(out["d_o"], clean["d_o"]) and torch.isnan(out["dx"][t, 5]) and torch.isnan(out["d_w"][t, at[1]])
+    assert torch.isnan(out["u"][t]).all() and torch.isnan(out["y"][t, 5])
