@@ -382,9 +382,11 @@ moe_status moe_block_norm_backward(const moe_shape *shape, const void *x, const 
  * experts, an output head), for up to 64 vectors:
  *   y[t,n] = tensor_scale * sum_k W[n,k] x[t,k] (+ bias[n]),
  * W dequantised on the fly from q ([rows][cols/2] codes) and s ([rows][cols/B] scales), as the
- * experts' sub-tensors are.  The weights and x enter the products exactly (fp32 x as three bf16
- * terms; a weight of 2^128 or more, under scale byte 253 or 254, is infinite), sums are fp32, and
- * y is rounded once.  1 <= rows <= 2^24, cols a multiple of 128,
+ * experts' sub-tensors are.  The weights and x enter the products exactly, but for two ends of the
+ * range: an fp32 x enters as three bf16 terms, which leave out its bits below 2^-133 (bf16's smallest
+ * number; none of an x of 2^-110 or more), and a weight of 2^128 or more, under scale byte 253 or
+ * 254, is infinite, its product with an fp32 x infinite or NaN.  Sums are fp32, and y is rounded
+ * once.  1 <= rows <= 2^24, cols a multiple of 128,
  * rows * cols <= 2^34, T <= 64 (MOE_ERR_UNSUPPORTED beyond).  tensor_scale is a host value, used
  * as given (1 for MXFP4).  x: [T][cols], y: [T][rows] act_dtype; bias: [rows] fp32 or NULL; q, s, x
  * and y 16-byte aligned; y may not alias x. */

@@ -4,8 +4,10 @@
 //
 // A code times its block scale is exact in bf16 (one bit of mantissa times a power of two, or times
 // the four bits of an E4M3 scale), so the weights enter the bf16 matrix cores exactly; a bf16 x does
-// too, and an fp32 x is the sum of three bf16 terms cut from it (8 + 8 + 8 bits, exact), each one more
-// MFMA column or MFMA into the same fp32 sums.
+// too, and an fp32 x is the sum of three bf16 terms cut from it (8 + 8 + 8 bits; exact but for bits below
+// 2^-133, bf16's smallest number), each one more MFMA column or MFMA into the same fp32 sums.  Subnormal terms
+// and weights count in full.  A weight that passes the type (E8M0 bytes 253 and 254) is infinite, and NaN times a
+// term that is zero.
 //
 // V_MFMA_F32_16X16X32_BF16: lane l supplies 8 consecutive K of weight row (A) or token (B) l % 16;
 // any assignment of K to the lane groups works when both operands share it.  A step covers 128 K of a

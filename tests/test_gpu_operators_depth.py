@@ -65,6 +65,34 @@ def test_linear_past_the_first_fill(N, K, T, act, wf):
         assert torch.equal(y, want.float().to(act))
 
 
+@pytest.mark.parametrize("N,K,T", [(40, 256, 1), (40, 256, 3), (4352, 256, 16), (16390, 256, 3), (16390, 2048, 5), (16390, 256, 16),
+                                   (16390, 256, 20), (65540, 256, 33), (9000, 256, 40)])
+def test_linear_smallest_inputs(N, K, T):
+    """fp32 x near the smallest normal numbers: its bf16 terms end at 2^-133, so each value is cut by less than that; and weights of
+    2^128 or more, which are infinite, leave no finite result."""
+    g = ops.gen(31)
+    q, s, _ = ops.quantised(g, N, K, 0)
+    s += 60                                                  # weights around 2^60
+    x = ops.rand(g, T, K) * 2.0 ** -120
+    mat, y = matrix(N, K, 0, F32), torch.empty(T, N, device="cuda")
+    m.moe_linear(mat, q, s, 1.0, x, T, None, y)
+    want = linear_bound(q, s, 0, 1.0, x, None)
+    want.e += 2.0 ** -133 * ref.weights(q, s, 0).abs().sum(1)[None]
+    ref.check(y, want, F32, "y")
+    q[3] = 0x77                                              # every code 6
+    s[3] = 254
+    for act in (F32, BF16):
+        xa = ops.rand(g, T, K, dtype=act)
+        xa[xa == 0] = 1.0
+        y, clean = torch.empty(T, N, dtype=act, device="cuda"), torch.empty(T, N, dtype=act, device="cuda")
+        m.moe_linear(matrix(N, K, 0, act), q, s - 60, 1.0, xa, T, None, clean)
+        s2 = s - 60
+        s2[3] = 254
+        m.moe_linear(matrix(N, K, 0, act), q, s2, 1.0, xa, T, None, y)
+        rest = torch.arange(N, device="cuda") != 3
+        assert not torch.isfinite(y[:, 3]).any() and torch.equal(y[:, rest], clean[:, rest])
+
+
 # ---------------------------------------------------------------------------------------------
 # norm gradients
 # ---------------------------------------------------------------------------------------------
