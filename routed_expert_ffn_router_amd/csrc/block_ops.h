@@ -93,15 +93,6 @@ __device__ __forceinline__ void store_act8(XT* p, size_t i, const f32x8& r) {
 // 8 picks, bf16).
 constexpr size_t kStreamBytes = (size_t)256 << 20;
 
-// Workgroups go to the eight XCDs in turn, so work that repeats every eight jobs (tokens that keep as many
-// picks as the eighth before them) would load one XCD more than another: the jobs of each group of
-// eight are rotated by their group.  (Tokens keeping 1, 8, 7, .. picks in turn: 1001 tokens' combine and norm
-// at d 6144, fp32: 43.0 us, in plain order 44.8.)
-__device__ __forceinline__ size_t xcd_rotate(size_t job, size_t jobs) {
-    const size_t group = job >> 3;
-    return (group + 1) * 8 <= jobs ? group * 8 + ((job + group) & 7) : job;
-}
-
 // A token's picks in rank order, in groups whose rows are loaded together: f(N, row, has, j0) with N = MAXN
 // (8 or 4), half or a quarter of it (at least 2) picks j0 .. j0 + N - 1 (a StepPos).  pos: the token's k
 // positions, the same in every lane of the wave; positions outside [0, P) have no row.  Dropped picks are

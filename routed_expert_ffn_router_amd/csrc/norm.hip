@@ -74,12 +74,13 @@ __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
 // COMBINE: 0, or the picks whose rows are loaded together.  LATE: the gate and the gammas are loaded when
 // they are used, which saves registers for more rows per CU (with eight picks and early loads one row of
 // d 6144 fits on a CU, so two); else with the row, before the first sum waits.
-// Combined, 8 picks: 64 tokens, d 4096 5.7 us; 1001 tokens, d 6144, fp32 43 us (185 MB at 4.3 TB/s: two rows
-// at a time on a CU do not cover each other's sums).
+// Combined, 8 picks: 64 tokens, d 4096 5.7 us; 1001 tokens, d 6144, fp32, one to eight picks kept at random 44 us
+// (185 MB at 4.2 TB/s: two rows at a time on a CU do not cover each other's sums); kept 1, 8, 7, .. 2 in turn
+// 46, since workgroups go to the eight XCDs in turn.
 template <typename XT, int VPT, int COMBINE, bool LATE, bool NT>
 __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
     __shared__ float s_post[16], s_pre[16];
-    const int t = COMBINE ? (int)xcd_rotate(blockIdx.x, a.T) : blockIdx.x;
+    const int t = blockIdx.x;
     const size_t base = (size_t)t * a.d;
     const bool has_y = COMBINE || a.y, element = a.gate_kind == MOE_GATE_ELEMENT;
     auto col = [&](int n) { return 8 * (int)(threadIdx.x + n * blockDim.x); };
