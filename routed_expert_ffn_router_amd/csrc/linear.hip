@@ -19,15 +19,16 @@
 // lanes of a quad hold four different rows, so a load of 16 bytes per lane costs as much as four that
 // are laid out along the rows, and a load of one scale byte per lane as much as one of 16 (taking the
 // scale or the x loads out of k_linear each saved 20 of 84 us at 65536 x 6144, 16 tokens).
-//   k_linear_ring    up to 16384 rows, and few tokens: codes, scales and x go straight to LDS
+//   k_linear_ring    few rows, and few tokens: codes, scales and x go straight to LDS
 //                    (global_load_lds) in row order, each wave into its own ring, so no wave waits for
 //                    another before the sums;
-//   k_linear_stream  many rows: each wave keeps its K slice of x in registers for all the row tiles that
+//   k_linear_stream  many long rows: each wave keeps its K slice of x in registers for all the row tiles that
 //                    its workgroup takes, so x is read once per CU;
-//   k_linear_tile    many rows and more tokens than the registers hold: the waves of a workgroup share x's
-//                    step in LDS;
-//   k_linear         many rows and up to 16 fp32 tokens, more than the stream's or of short rows, straight
-//                    from global memory to registers.
+//   k_linear_tile    many rows that are short, or too long for the registers, or with many tokens: the waves
+//                    of a workgroup share x's step in LDS;
+//   k_linear         6 to 16 fp32 tokens, or fewer with short rows, of many rows, straight from global memory
+//                    to registers.
+// Which one takes a call: lin_kernel_bf16 and lin_kernel_f32.
 #include "block_ops.h"
 
 namespace moe {
@@ -130,8 +131,8 @@ __device__ __forceinline__ void lin_store(const LinArgs& a, int t, int row, cons
 }
 
 // A workgroup of eight waves owns 64 rows and 16 fp32 tokens; its waves share out K, and their sums are added
-// through LDS in wave order.  65536 x 6144 MXFP4, 16 tokens: 111 us, 16384 x 4096 21 (k_linear_tile 101 and 45,
-// k_linear_ring 224 and 42); one or two rows' fragments per wave and deeper prefetch were slower.
+// through LDS in wave order.  65536 x 6144 MXFP4, 16 tokens: 111 us, 16384 x 4096 22 (k_linear_tile 97 and 45,
+// k_linear_ring 227 and 43); one or two rows' fragments per wave and deeper prefetch were slower.
 template <int WF>
 __global__ __launch_bounds__(512) void k_linear(LinArgs a) {
     constexpr int F = 4, W = 8;
@@ -715,10 +716,15 @@ static void stream_launch(const LinArgs& a, int passes, hipStream_t st) {
 template <typename XT, int WF, int C, int S>
 static void tile_launch_columns(const LinArgs& a, hipStream_t st) {
     const int passes = (a.T + 16 * C - 1) / (16 * C);
-    if ((long long)(a.N + 255) / 256 * passes >= 256)
-        MOE_LAUNCH((k_linear_tile<XT, WF, C, 2, S>), dim3((a.N + 255) / 256, passes), dim3(512), 0, st, a);
-    else
-        MOE_LAUNCH((k_linear_tile<XT, WF, C, 1, S>), dim3((a.N + 127) / 128, passes), dim3(512), 0, st, a);
+    // two fragments of 16 rows per wave once one would take more than a workgroup per CU, but for 32 bf16 tokens, whose
+    // step is short: 49152 x 4096, 64 bf16 tokens 45 us for 55, 32 fp32 tokens 67 for 95; 32 bf16 tokens 33 for 34, 98304 x 4096 64 for 53
+    if constexpr (sizeof(XT) == 4 || C == 4) {
+        if ((long long)(a.N + 127) / 128 * passes > 256) {
+            MOE_LAUNCH((k_linear_tile<XT, WF, C, 2, S>), dim3((a.N + 255) / 256, passes), dim3(512), 0, st, a);
+            return;
+        }
+    }
+    MOE_LAUNCH((k_linear_tile<XT, WF, C, 1, S>), dim3((a.N + 127) / 128, passes), dim3(512), 0, st, a);
 }
 template <typename XT, int WF>
 static void tile_launch(const LinArgs& a, hipStream_t st) {
@@ -727,42 +733,90 @@ static void tile_launch(const LinArgs& a, hipStream_t st) {
     else tile_launch_columns<XT, WF, 4, 4>(a, st);
 }
 
+enum class LinKernel { ring, stream, tile, straight };
+
+// The kernel for N rows, K columns and T tokens.  Each boundary stands where the times of two kernels cross, over 6300
+// timings (1024 to 131072 rows by 512 to 12288 columns, 1 to 64 tokens, both formats, the weights in memory and not in
+// the caches).  At 3300 other sizes at random between them the choice takes at most 10% longer than the best kernel in
+// 95% of the bf16 ones and 99% of the fp32 ones, and on average 1%.  Some of the timings, us, MXFP4:
+//   the stream against the ring: x in registers pays once a CU has several tiles of long rows.  bf16: 8192 x 4096,
+//   16 tokens 8.0, 10.8; 16384 x 4096, 2 tokens 10.7, 10.0, 8 tokens 10.8, 12.8; 65536 x 6144, 1 token 41.7, 45.8;
+//   16384 x 1024, 4 tokens 7.0, 4.5.  fp32, 5 tokens: 12288 x 4096 11.4, 14.3; 8192 x 2048 8.3, 6.5.
+//   the tile against the ring or the stream: x shared by 128 or 256 rows pays with short rows, rows past the
+//   registers and more than 16 tokens.  bf16: 65536 x 512, 16 tokens 8.2, 15.5; 32768 x 12288, 8 tokens 52, 63;
+//   12288 x 2048, 64 tokens 15.7, 22.5; 8192 x 4096, 32 tokens 18.6, 12.7.
+//   k_linear (straight) against the stream in two passes and the ring, fp32: 65536 x 2048, 8 tokens 32, 36;
+//   65536 x 6144 88, 77 (NVFP4 93, 96); 12288 x 4096, 16 tokens 21, 33; 4096 x 4096 18, 13.
+//   k_linear against the tile, fp32, 16 tokens: 65536 x 6144 111, 97, but 98304 x 4096 107, 125 and 49152 x 4096 56, 64,
+//   whose workgroups leave CUs idle at the end: k_linear throughout.
+static LinKernel lin_kernel_bf16(int N, int K, int T) {
+    const long long NK = (long long)N * K;
+    const bool fit = K <= kLinStreamMaxK, deep = fit && K > 2560;
+    bool tile, stream;
+    if (T <= 4) {
+        stream = T > 2 ? deep && NK >= 1 << 27 : K > 4096 && K <= 6144 && NK >= 1 << 28;
+        tile = N >= 49152 && K <= 512;
+    } else if (T <= 8) {
+        const int wgs = (N + 127) / 128, rounds = (wgs + 255) / 256;
+        stream = deep ? N >= 12288 : fit && K >= 1536 && N >= (K >= 2048 ? 16384 : 49152);
+        tile = K <= 512 ? N >= 24576 : N >= 32768 && (K <= 1024 || (!fit && 4 * wgs >= 3 * 256 * rounds));
+    } else if (T <= 16) {
+        stream = deep ? N >= 6144 : fit && K > 1024 && N > 8192;
+        tile = K <= 512 ? N >= 8192 : K <= 1024 ? N >= 12288 : !fit && N >= 24576;
+    } else if (T <= 32) {
+        stream = K >= 4096 && K <= 6144 && N >= 12288 && N < 16384;
+        tile = N >= 16384 || (N >= 9216 && K <= 1536) || (N >= 12288 && K < 4096);
+    } else {
+        stream = fit && K >= 4096 && T <= 48 && N >= 8192 && N < 16384;
+        tile = N >= 12288 || (N >= 8192 && K <= 2048) || (N >= 6144 && K <= 512);
+    }
+    return stream ? LinKernel::stream : tile ? LinKernel::tile : LinKernel::ring;
+}
+
+// mx: MXFP4 (NVFP4 takes longer to decode, and the stream decodes once a pass)
+static LinKernel lin_kernel_f32(int N, int K, int T, bool mx) {
+    const bool fit = K <= kLinStreamMaxK, deep = fit && K > 2560;
+    if (T <= 5) {
+        if (deep ? N >= 8192 : fit && K > 1024 && N >= 16384) return LinKernel::stream;
+        return K <= 1024 && N >= 16384 ? LinKernel::straight : LinKernel::ring;
+    }
+    if (T <= 10) {
+        if (mx && deep && N >= 24576) return LinKernel::stream;
+        return N > 8192 || (N == 8192 && K <= 2048) ? LinKernel::straight : LinKernel::ring;
+    }
+    if (T <= 16) return N >= 5632 ? LinKernel::straight : LinKernel::ring;
+    if (deep && T <= 24 && N >= 12288 && N < 16384) return LinKernel::stream;
+    // the ring's time grows with rows times passes, the tile's steps by rounds of the chip
+    const int passes = (T + 4) / 5, least = K <= 512 ? 24576 : K <= 1024 ? 43008 : 49152;
+    return (long long)N * passes >= least ? LinKernel::tile : LinKernel::ring;
+}
+
 template <typename XT, int WF>
 static void linear_launch(const LinArgs& a, hipStream_t st) {
-    // Many rows: x read once per CU (stream), once per workgroup of 128 or 256 rows (tile) or once per 16 rows
-    // (ring), us, MXFP4.
-    //   bf16, 16 tokens: 8192 x 4096 stream 9.6, ring 9.0; 16384 x 4096 10, 16.  Four tokens: 32768 x 4096 16.3,
-    //   18.6; 65536 x 6144 41, 52; one or two as fast either way.  Eight tokens of short rows: 49699 x 768 12.8,
-    //   10.2; 65536 x 2048 18, 22.
-    //   32 tokens: 16384 x 4096 stream 17, tile 18; 65536 x 6144 71, 50; 64 tokens: 16384 x 4096 31, 27.
-    //   Long rows, 32768 x 12288: 8 tokens ring 61, tile 52; 16 tokens 84, 51.
-    //   fp32, eight tokens: 49699 x 768 stream 27, k_linear 13; 65536 x 2048 35, 39; five: 15, 12; 19, 35.
-    //   fp32, 8192 x 4096: 32 tokens ring 41, tile 45; 64 tokens 79, 45.
-    // Two fragments of 16 rows per wave of a tile once that fills the CUs: 65536 x 6144, 64 tokens 68 for 81, fp32
-    // 199 for 258; 16384 x 4096 38 for 27, fp32 61 for 45.
-    // Few rows: 32 tokens in one pass, or 16 fp32 tokens (terms in turn) for five, once the passes no longer
-    // run side by side: 4096 x 4096, 32 tokens 6.9 for 7.8, 16 fp32 tokens 11.7 for 14.6; 512 x 2048 4.2 for 3.4
-    // and 6.7 for 4.2.
-    const int tiles = (a.N + 15) / 16;
-    const bool many = a.N >= 16384, most = a.N >= 32768, fit = a.K <= kLinStreamMaxK;
-    if constexpr (sizeof(XT) == 2) {
-        const int passes = (a.T + 15) / 16;
-        if (many && (a.T > 32 || (a.T > 16 && (most || !fit)) || (a.T > 8 && most && !fit))) tile_launch<XT, WF>(a, st);
-        else if (many && fit && (a.T > 8 || (a.T > 4 && a.K >= 2048) || (a.T > 2 && (long long)a.N * a.K >= 1 << 27)))
-            stream_launch<XT, WF>(a, passes, st);
-        else if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
+    constexpr bool F32 = sizeof(XT) == 4;
+    const int tiles = (a.N + 15) / 16, passes = (a.T + kLinPass<XT> - 1) / kLinPass<XT>;
+    const LinKernel kernel = F32 ? lin_kernel_f32(a.N, a.K, a.T, WF == MOE_WF_MXFP4) : lin_kernel_bf16(a.N, a.K, a.T);
+    if (kernel == LinKernel::tile) return tile_launch<XT, WF>(a, st);
+    if (kernel == LinKernel::stream) return stream_launch<XT, WF>(a, passes, st);
+    if constexpr (F32) {
+        if (kernel == LinKernel::straight) {
+            MOE_LAUNCH((k_linear<WF>), dim3((a.N + 63) / 64), dim3(512), 0, st, a);
+            return;
+        }
+        // 16 tokens in one pass (their terms in turn), a workgroup per CU, take as long as three rounds of 256 workgroups
+        // of five, of which two share a CU: 4096 x 4096, 16 tokens 12.7 us for 16.1, 20 tokens 23 for 16.2; 4220 x 4992, 15
+        // tokens 26.8 for 18.5; 1024 x 2048, 16 tokens 7.5 for 5.0
+        const int wgs5 = tiles * passes, passes16 = (a.T + 15) / 16, rounds16 = (tiles * passes16 + 255) / 256;
+        if (a.T <= 2) ring_launch<XT, WF, 1>(a, 1, st);
+        else if (a.T <= 4) ring_launch<XT, WF, 2>(a, 1, st);
+        else if (a.T <= 10 || wgs5 <= 512 || (rounds16 > 1 && wgs5 < 3 * 256 * rounds16)) ring_launch<XT, WF, 3>(a, passes, st);
+        else ring_launch<XT, WF, 8>(a, passes16, st);
+    } else {
+        // 32 tokens in one pass once two of 16 no longer run side by side: 4096 x 4096 7.2 us for 8.5; 2048 x 4096 6.8 for 5.4
+        if (a.T <= 4) ring_launch<XT, WF, 1>(a, 1, st);
         else if (a.T <= 8) ring_launch<XT, WF, 2>(a, 1, st);
         else if (a.T <= 16 || tiles * passes <= 256) ring_launch<XT, WF, 4>(a, passes, st);
         else ring_launch<XT, WF, 8>(a, (a.T + 31) / 32, st);
-    } else {
-        const int passes = (a.T + 4) / 5;
-        if ((many && a.T > 16) || (a.N >= 8192 && a.T > 32)) tile_launch<XT, WF>(a, st);
-        else if (many && fit && a.T <= 10 && a.K >= (a.T <= 5 ? 1024 : 2048)) stream_launch<XT, WF>(a, passes, st);
-        else if (many && (a.T > 5 || fit)) MOE_LAUNCH((k_linear<WF>), dim3((a.N + 63) / 64), dim3(512), 0, st, a);
-        else if (a.T <= 2) ring_launch<XT, WF, 1>(a, 1, st);
-        else if (a.T <= 4) ring_launch<XT, WF, 2>(a, 1, st);
-        else if (a.T <= 10 || tiles * passes <= 512) ring_launch<XT, WF, 3>(a, passes, st);
-        else ring_launch<XT, WF, 8>(a, (a.T + 15) / 16, st);
     }
 }
 

@@ -20,7 +20,10 @@ DEEP = [
     (16390, 8192, 5), (16390, 7040, 9), (16390, 4736, 3), (16390, 8192, 16), (20011, 5888, 12), (65540, 2432, 5), (65540, 2432, 9),
     (65540, 2432, 16), (65540, 2432, 20), (65540, 2432, 33), (65540, 2432, 49), (32900, 2432, 64), (16400, 4224, 40),
     (16400, 8448, 16), (33001, 8320, 24), (9000, 4224, 40), (4099, 4224, 16), (4099, 4224, 33), (515, 8192, 64), (300, 16384, 2),
-    (300, 16384, 7), (16384, 8320, 5),
+    (300, 16384, 7), (16384, 8320, 5), (24580, 4224, 7), (12290, 4224, 22), (12290, 4224, 30), (12300, 4096, 20), (49160, 5504, 2),
+    (49155, 512, 1), (49155, 512, 4), (4100, 512, 40), (6150, 640, 33), (4099, 4224, 17), (16390, 1152, 3), (12300, 1152, 9),
+    (6150, 4096, 13), (24600, 8320, 13), (8200, 1024, 48), (98310, 640, 7), (4090, 4224, 16), (2048, 8320, 64), (12300, 8192, 12),
+    (9000, 7168, 4),
 ]
 
 
@@ -91,6 +94,52 @@ def test_linear_smallest_inputs(N, K, T):
         m.moe_linear(matrix(N, K, 0, act), q, s2, 1.0, xa, T, None, y)
         rest = torch.arange(N, device="cuda") != 3
         assert not torch.isfinite(y[:, 3]).any() and torch.equal(y[:, rest], clean[:, rest])
+
+
+# sizes at which each kernel takes a call: N, K, T, activations
+KERNELS = [(256, 1152, 3, F32), (256, 1152, 8, F32), (4090, 1152, 16, F32), (16640, 1152, 3, F32), (16640, 4224, 5, F32),
+           (9000, 7168, 4, F32), (24580, 4224, 7, F32), (16640, 512, 2, F32), (8448, 1152, 8, F32), (12300, 2176, 16, F32),
+           (12300, 4224, 20, F32), (16640, 1152, 20, F32), (65540, 256, 33, F32), (256, 1152, 3, BF16), (256, 1152, 7, BF16),
+           (256, 1152, 16, BF16), (4352, 1152, 33, BF16), (12300, 1152, 9, BF16), (16640, 2176, 7, BF16), (12300, 5120, 16, BF16),
+           (16640, 7168, 12, BF16), (24580, 384, 7, BF16), (16640, 1152, 20, BF16), (16640, 1152, 40, BF16), (65540, 256, 40, BF16)]
+
+
+@pytest.mark.parametrize("N,K,T,act", KERNELS)
+def test_linear_scale_bytes_in_every_kernel(N, K, T, act):
+    ops.test_linear_scale_bytes(N, K, T, act)
+
+
+@pytest.mark.parametrize("N,K,T,act", KERNELS)
+def test_linear_outside_the_numbers_in_every_kernel(N, K, T, act):
+    """Infinity and NaN in x, a NaN whose payload lies in the lower half among them, reach that token alone, and the largest
+    finite value stays finite on the way."""
+    g = ops.gen(35)
+    q, s, _ = ops.quantised(g, N, K, 0)
+    x, mat = ops.rand(g, T, K, dtype=act), matrix(N, K, 0, act)
+    y, z = torch.empty(T, N, dtype=act, device="cuda"), torch.empty(T, N, dtype=act, device="cuda")
+    m.moe_linear(mat, q, s, 1.0, x, T, None, y)
+    w = ref.weights(q, s, 0)[:, 200]
+    for t, bits in ((0, None), (T - 1, float("nan")), (T // 2, 0x7f800001), (T // 2, -0x7ffff0)):
+        if isinstance(bits, int) and act != F32:
+            continue
+        x2 = x.clone()
+        if isinstance(bits, int):
+            x2.view(torch.int32)[t, 200] = bits
+        else:
+            x2[t, 200] = float("inf") if bits is None else bits
+        m.moe_linear(mat, q, s, 1.0, x2, T, None, z)
+        rest = torch.arange(T, device="cuda") != t
+        assert torch.equal(z[rest], y[rest])
+        if bits is None:
+            assert torch.equal(torch.isnan(z[t]), w == 0)    # 0 times infinity
+            assert torch.equal(z[t][w != 0], (torch.sign(w) * float("inf")).to(act)[w != 0])
+        else:
+            assert torch.isnan(z[t]).all()
+    x2 = torch.zeros_like(x)
+    x2[:, 7] = torch.finfo(act).max
+    low = torch.full_like(s, 100)
+    m.moe_linear(mat, q, low, 1.0, x2, T, None, z)
+    ref.check(z, linear_bound(q, low, 0, 1.0, x2, None), act, "y")
 
 
 # ---------------------------------------------------------------------------------------------
