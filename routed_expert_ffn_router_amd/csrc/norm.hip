@@ -40,7 +40,7 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
 }
 
 // the combine's sum for columns c .. c + 7 of token t, in k_combine's order
-template <int MAXN, bool NT>
+template <int MAXN>
 __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
     const int P = a.T * a.k;
     f32x8 acc = {};
@@ -50,7 +50,7 @@ __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
         float w[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i].template load<NT>(a.o, (size_t)row[i] * a.d + c);
+            v[i].load(a.o, (size_t)row[i] * a.d + c);
             w[i] = a.w[(size_t)t * a.k + (j0 + i < a.k ? j0 + i : j0)];
         }
 #pragma unroll
@@ -63,7 +63,7 @@ __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc.v[e] *= a.scaling;
     if (a.shared) {
-        const f32x8 v = load_act8<NT>(a.o, ((size_t)P + t) * a.d + c);
+        const f32x8 v = load_act8(a.o, ((size_t)P + t) * a.d + c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc.v[e] += v.v[e];
     }
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
             load_after(n);
             if (a.pre) pre[n] = load_act8(a.pre, (size_t)col(n));
         }
-        if constexpr (COMBINE > 0) z[n] = combine8<COMBINE, NT>(a, t, col(n));
+        if constexpr (COMBINE > 0) z[n] = combine8<COMBINE>(a, t, col(n));
         else if (has_y) z[n] = load_act8<NT>((const XT*)a.y, base + col(n));
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[0] = fmaf(z[n].v[e], z[n].v[e], sum[0]);
@@ -165,13 +165,12 @@ template <typename XT>
 static void norm_launch(const NormArgs& a, hipStream_t st) {
     int vpt;
     const dim3 grid(a.T), block(norm_threads(a.d, &vpt));
-    // the combine: with more rows than CUs, four picks at a time and late loads; past the caches once
-    // its rows are larger than they are
-    const bool many = a.T > 256 || vpt == 2, nt = 4 * (size_t)a.T * a.d * (a.k + a.shared) >= kStreamBytes;
     if (a.o) {
+        // the combine: with more rows than CUs, four picks at a time and late loads.  Never past the caches: 4096 tokens,
+        // d 4096, bf16 127 us, past them 135, 16384 502 for 556 (fp32 569 for 655); after a kernel that writes o 854 for
+        // 895 (914 for 983; 4096 tokens 233 for 222, the one size where it gained).
         if (vpt == 2) MOE_LAUNCH((k_block_norm<XT, 2, 4, true, false>), grid, block, 0, st, a);
-        else if (many && nt) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, true>), grid, block, 0, st, a);
-        else if (many) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, false>), grid, block, 0, st, a);
+        else if (a.T > 256) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, false>), grid, block, 0, st, a);
         else MOE_LAUNCH((k_block_norm<XT, 1, 8, false, false>), grid, block, 0, st, a);
     } else if (vpt == 2) {
         MOE_LAUNCH((k_block_norm<XT, 2, 0, true, false>), grid, block, 0, st, a);
