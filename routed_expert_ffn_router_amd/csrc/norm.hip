@@ -146,12 +146,20 @@ __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
         if constexpr (LATE) pre[n] = load_act8(a.pre, (size_t)col(n));
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[n].v[e] *= r * pre[n].v[e];
-        store_act8<NT>((XT*)a.normed, base + col(n), u[n]);
+        store_act8((XT*)a.normed, base + col(n), u[n]);        // the next kernel reads it
     }
 }
 
-// bytes of one row array from which its rows go past the caches (the eight L2s together)
+// Bytes of one row array from which bf16 rows go past the caches (the eight L2s together), but for normed, which the
+// router or dispatch reads next.  4096 rows, d 4096, gate per element: the norm alone 32.2 us, all of it through the
+// caches 33.4; then route and dispatch (4 picks) 134.5, 142.9, with normed past the caches too 138.5; 16384 rows 112 and
+// 484, 122 and 489, 116 and 507.  fp32 rows stay in the caches: 4096 rows 62 us, past them 68, with route and dispatch
+// 185, 196.
 constexpr size_t kStreamRows = (size_t)32 << 20;
+template <typename XT>
+static bool past_caches(int T, int d) {
+    return sizeof(XT) == 2 && (size_t)T * d * sizeof(XT) >= kStreamRows;
+}
 
 // threads of a workgroup for rows of d columns, eight per thread and vector
 static int norm_threads(int d, int* vpt) {
@@ -174,8 +182,8 @@ static void norm_launch(const NormArgs& a, hipStream_t st) {
         else MOE_LAUNCH((k_block_norm<XT, 1, 8, false, false>), grid, block, 0, st, a);
     } else if (vpt == 2) {
         MOE_LAUNCH((k_block_norm<XT, 2, 0, true, false>), grid, block, 0, st, a);
-    } else if ((size_t)a.T * a.d * sizeof(XT) >= kStreamRows) {
-        MOE_LAUNCH((k_block_norm<XT, 1, 0, false, true>), grid, block, 0, st, a);
+    } else if (past_caches<XT>(a.T, a.d)) {
+        MOE_LAUNCH((k_block_norm<XT, 1, 0, false, sizeof(XT) == 2>), grid, block, 0, st, a);
     } else {
         MOE_LAUNCH((k_block_norm<XT, 1, 0, false, false>), grid, block, 0, st, a);
     }
