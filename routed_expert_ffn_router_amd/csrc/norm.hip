@@ -463,11 +463,15 @@ static void norm_backward_launch(const NormArgs& a, const NormGradArgs& g, int g
     int vpt;
     const int threads = norm_threads(a.d, &vpt);
     const dim3 grid(groups);
-    const bool nt = (size_t)a.T * a.d * sizeof(XT) >= kStreamRows;
+    // as the forward pass; dy, which the combine's gradient reads next, past the caches too (d 4096, gate per element, 2
+    // picks: 8192 bf16 rows 98 us, with the combine's gradient 238, through the caches 104 and 239; 4096 fp32 rows 122 and
+    // 197, 113 and 187)
+    const bool nt = past_caches<XT>(a.T, a.d);
+    constexpr bool NT = sizeof(XT) == 2;
     if (vpt == 2) MOE_LAUNCH((k_block_norm_backward<XT, 2, 1024, false>), grid, dim3(threads), 0, st, a, g);
-    else if (threads > 512 && nt) MOE_LAUNCH((k_block_norm_backward<XT, 1, 1024, true>), grid, dim3(threads), 0, st, a, g);
+    else if (threads > 512 && nt) MOE_LAUNCH((k_block_norm_backward<XT, 1, 1024, NT>), grid, dim3(threads), 0, st, a, g);
     else if (threads > 512) MOE_LAUNCH((k_block_norm_backward<XT, 1, 1024, false>), grid, dim3(threads), 0, st, a, g);
-    else if (nt) MOE_LAUNCH((k_block_norm_backward<XT, 1, 512, true>), grid, dim3(threads), 0, st, a, g);
+    else if (nt) MOE_LAUNCH((k_block_norm_backward<XT, 1, 512, NT>), grid, dim3(threads), 0, st, a, g);
     else MOE_LAUNCH((k_block_norm_backward<XT, 1, 512, false>), grid, dim3(threads), 0, st, a, g);
 }
 
