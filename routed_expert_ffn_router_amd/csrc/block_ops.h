@@ -87,17 +87,20 @@ __device__ __forceinline__ void store_act8(XT* p, size_t i, const f32x8& r) {
     }
     store16<NT>(p + i, w[0]);
 }
-// Bytes of an expert-side array from which its rows go past the caches: the last-level cache's size.  Below
-// it the next kernel finds them there (82 MB of rows read past the caches: 19.8 us instead of 14.6); above
-// it 4096 tokens' dispatch took 53.5 us instead of 61.8 and its gradient 50.4 instead of 59.6 (d 4096,
-// 8 picks, bf16).
+// Bytes of an expert-side array from which the dispatch's and the gradients' rows go past the caches: the last-level
+// cache's size.  Below it the next kernel finds them there: 128 MB (2048 tokens, d 4096, 8 picks, bf16) dispatched
+// and read again 53 us, past the caches 63.  Above it, d 4096, us, past the caches and through them: dispatch of 256 MB 55,
+// 58, with a matrix product behind it 164, 181 (512 MB 108, 119 and 325, 341); its gradient 50, 59, behind a kernel
+// that writes the rows 124, 130 (512 MB 100, 117 and 258, 297; fp32 256 MB 59, 60 and 148, 135, 512 MB 117, 116 and 281, 296);
+// the combine's gradient 116, 129, with a reader of d_o 167, 174 (2 GB 867, 894 and 1220, 1242).
 constexpr size_t kStreamBytes = (size_t)256 << 20;
 
 // A token's picks in rank order, in groups whose rows are loaded together: f(N, row, has, j0) with N = MAXN
 // (8 or 4), half or a quarter of it (at least 2) picks j0 .. j0 + N - 1 (a StepPos).  pos: the token's k
 // positions, the same in every lane of the wave; positions outside [0, P) have no row.  Dropped picks are
 // the last ranks, so the groups end with the last pick that has one; a pick without a row inside a group
-// (has false) stands on another pick's row, which it reads from the cache and must not use.
+// (has false) stands on another pick's row, which it reads from the cache and must not use.  The positions
+// themselves are waited for one after the other, before the first row is requested.
 template <int MAXN, typename F>
 __device__ __forceinline__ void for_picks(const int32_t* __restrict__ pos, int k, int P, F&& f) {
     for (int j0 = 0; j0 < k; j0 += MAXN) {

@@ -307,8 +307,8 @@ __device__ __forceinline__ lin_f32x4 lin_sum_waves(const lin_f32x4* part, int la
 // fp32 tokens each), swizzled by token.  Two steps of codes and x in flight, scales with the first step that
 // they serve.  bf16: 16 columns of tokens, or twice 16 (NX = 8).  fp32: up to five tokens of three columns, or
 // (NX = 8) 16 columns of tokens, multiplied by each term in turn.
-// 4096 x 4096 MXFP4, one token: 4.2 us (8.9 MB; a kernel of one round trip to memory takes 2.0), 16 tokens 5.1, 32
-// 6.9; 4096 x 16384 8.6, 14.7 and 20.  Eight waves and two steps were as fast or faster than 4 or 16 waves and one
+// 4096 x 4096 MXFP4, one token: 4.0 us (8.9 MB; a kernel of one round trip to memory takes 2.0), 16 tokens 5.4, 32
+// 7.2; 4096 x 16384 8.6, 14.7 and 20.  Eight waves and two steps were as fast or faster than 4 or 16 waves and one
 // to four steps up to 4096 rows.  With many rows x is what costs (65536 x 6144, 16 tokens: 92 us).
 template <typename XT, int WF, int NX, int W>
 __global__ __launch_bounds__(64 * W) void k_linear_ring(LinArgs a) {
@@ -575,8 +575,8 @@ __device__ __forceinline__ void lin_read(uint32_t at, lin_u32x4 (&v)[N]) {
 // Many rows and many tokens: 16 F rows per wave, eight waves over rows, and 16 C tokens, whose step of x the
 // waves share in LDS; each wave has its own ring of codes and scales.  S steps alive, one barrier a step.
 // fp32 x is cut into its terms once per workgroup and step, each wave the part that it loaded.
-// 65536 x 6144 MXFP4, bf16: 32 tokens 50 us, 64 68; fp32: 102 and 199 (at the matrix cores' 1.23 PFLOP/s 63 and
-// 126).  With the workgroups' rows on few CUs a step's chain of LDS reads, decode, products and barrier (0.5 us)
+// 65536 x 6144 MXFP4, bf16: 32 tokens 54 us, 64 70; fp32: 102 and 190 (at the matrix cores' 1.23 PFLOP/s 63 and
+// 126).  16384 rows are 128 workgroups on 256 CUs: 19 and 28 us with 4096 columns.  With the workgroups' rows on few CUs a step's chain of LDS reads, decode, products and barrier (0.5 us)
 // bounds it: steps of 256 K, all of a step's reads at once or four stages for three took as long; sixteen waves
 // that share out a step's K took 22 us for 27 at 16384 x 4096 and 64 tokens, but 82 for 68 at 65536 x 6144.
 template <typename XT, int WF, int C, int F, int S>
@@ -717,7 +717,8 @@ template <typename XT, int WF, int C, int S>
 static void tile_launch_columns(const LinArgs& a, hipStream_t st) {
     const int passes = (a.T + 16 * C - 1) / (16 * C);
     // two fragments of 16 rows per wave once one would take more than a workgroup per CU, but for 32 bf16 tokens, whose
-    // step is short: 49152 x 4096, 64 bf16 tokens 45 us for 55, 32 fp32 tokens 67 for 95; 32 bf16 tokens 33 for 34, 98304 x 4096 64 for 53
+    // step is short: 49152 x 4096, 64 bf16 tokens 45 us for 55, 32 fp32 tokens 67 for 95; 32 bf16 tokens 33 for 34, with 98304
+    // rows 64 for 53
     if constexpr (sizeof(XT) == 4 || C == 4) {
         if ((long long)(a.N + 127) / 128 * passes > 256) {
             MOE_LAUNCH((k_linear_tile<XT, WF, C, 2, S>), dim3((a.N + 255) / 256, passes), dim3(512), 0, st, a);

@@ -6,7 +6,7 @@
 //
 // A workgroup holds one row in registers, eight columns per thread and vector, so each row is read
 // once and written once; the row sums go through DPP and LDS in a fixed order.  Bound by HBM where there
-// are many rows (d 4096, bf16, with a gate: 4096 rows 32 us, 168 MB at 5.3 TB/s), by the chain load, sum,
+// are many rows (d 4096, bf16, with a gate: 4096 rows 31 us, 168 MB at 5.5 TB/s), by the chain load, sum,
 // sum, store where there are few (one row 2.6 us).  Two vectors per thread and half the threads, tried for
 // d 4096 to 8192, were slower (35 -> 39 us; the combine 45 -> 50).
 #include "block_ops.h"
@@ -205,9 +205,10 @@ hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t 
 //   dy = r(y) (dz post - yn mean(dz post yn)),  or dz without a post-norm.
 // A workgroup takes rows b, b + G, ... (G workgroups) and keeps its columns' sums of d_post and d_pre
 // itself; k_norm_grad_sums adds the workgroups' sums in order.  Bound by HBM: 4096 rows, d 4096, bf16, with a
-// gate per element: 52 us, 277 MB at 5.3 TB/s, and 4.6 us for the sums.  Requesting the next row before the
-// sums of this one needs its registers: the gammas wait in LDS (72 -> 54 us with both, fewer groups, and
-// rows past the caches).
+// gate per element: 51 us, 277 MB at 5.4 TB/s, and 4.7 us for the sums; fp32 112 us at 5.0 TB/s, with 20 bytes of a lane
+// spilled.  Requesting the next row before the sums of this one needs its registers: the gammas wait in LDS (72 -> 54 us
+// with both, fewer groups, and rows past the caches).  Past 8192 columns a CU holds one row and none ahead: 2048 bf16
+// rows of 12288 113 us at 3.6 TB/s (28 bytes spilled, fp32 72).
 // ---------------------------------------------------------------------------------------------
 // Groups: a row's chain of three sums takes about 2 us, so a CU needs some 64 KB of rows at once to keep its
 // share of HBM busy: one workgroup per CU for long rows, up to eight for short ones.  More only add partial sums
