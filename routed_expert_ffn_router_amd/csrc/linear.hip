@@ -747,7 +747,7 @@ enum class LinKernel { ring, stream, tile, straight };
 //   registers and more than 16 tokens.  bf16: 65536 x 512, 16 tokens 8.2, 15.5; 32768 x 12288, 8 tokens 52, 63;
 //   12288 x 2048, 64 tokens 15.7, 22.5; 8192 x 4096, 32 tokens 18.6, 12.7.
 //   k_linear (straight) against the stream in two passes and the ring, fp32: 65536 x 2048, 8 tokens 32, 36;
-//   65536 x 6144 88, 77 (NVFP4 93, 96); 12288 x 4096, 16 tokens 21, 33; 4096 x 4096 18, 13.
+//   65536 x 6144 88, 77 (NVFP4 93, 96); 20239 x 3200, 9 tokens 25, 23; 12288 x 4096, 16 tokens 21, 33; 4096 x 4096 18, 13.
 //   k_linear against the tile, fp32, 16 tokens: 65536 x 6144 111, 97, but 98304 x 4096 107, 125 and 49152 x 4096 56, 64,
 //   whose workgroups leave CUs idle at the end: k_linear throughout.
 static LinKernel lin_kernel_bf16(int N, int K, int T) {
@@ -782,7 +782,7 @@ static LinKernel lin_kernel_f32(int N, int K, int T, bool mx) {
         return K <= 1024 && N >= 16384 ? LinKernel::straight : LinKernel::ring;
     }
     if (T <= 10) {
-        if (mx && deep && N >= 24576) return LinKernel::stream;
+        if (mx && deep && N > 16384) return LinKernel::stream;
         return N > 8192 || (N == 8192 && K <= 2048) ? LinKernel::straight : LinKernel::ring;
     }
     if (T <= 16) return N >= 5632 ? LinKernel::straight : LinKernel::ring;

@@ -23,7 +23,7 @@ DEEP = [
     (300, 16384, 7), (16384, 8320, 5), (24580, 4224, 7), (12290, 4224, 22), (12290, 4224, 30), (12300, 4096, 20), (49160, 5504, 2),
     (49155, 512, 1), (49155, 512, 4), (4100, 512, 40), (6150, 640, 33), (4099, 4224, 17), (16390, 1152, 3), (12300, 1152, 9),
     (6150, 4096, 13), (24600, 8320, 13), (8200, 1024, 48), (98310, 640, 7), (4090, 4224, 16), (2048, 8320, 64), (12300, 8192, 12),
-    (9000, 7168, 4),
+    (9000, 7168, 4), (16400, 2688, 8),
 ]
 
 
