@@ -176,7 +176,7 @@ static void norm_launch(const NormArgs& a, hipStream_t st) {
     if (a.o) {
         // the combine: with more rows than CUs, four picks at a time and late loads.  Never past the caches: 4096 tokens,
         // d 4096, bf16 127 us, past them 135, 16384 502 for 556 (fp32 569 for 655); after a kernel that writes o 854 for
-        // 895 (914 for 983; only there, and with 3072 to 6144 bf16 tokens, past them gained: 4096 222 for 233).
+        // 895 (914 for 983; only there, with 384 to 768 MB of o and bf16 rows, past them gained: 4096 tokens 222 for 233).
         if (vpt == 2) MOE_LAUNCH((k_block_norm<XT, 2, 4, true, false>), grid, block, 0, st, a);
         else if (a.T > 256) MOE_LAUNCH((k_block_norm<XT, 1, 4, true, false>), grid, block, 0, st, a);
         else MOE_LAUNCH((k_block_norm<XT, 1, 8, false, false>), grid, block, 0, st, a);
