@@ -192,6 +192,49 @@ def test_norm_gradients_keep_rows_apart(T, d, act):
             assert not torch.isfinite(out["dx"][bad, 17]), (name, value)
 
 
+@pytest.mark.parametrize("T,d,act", [(4099, 4096, BF16), (2100, 8192, BF16), (2051, 4096, F32)])
+def test_rows_larger_than_the_caches_in_place(T, d, act):
+    """Each value is read before its place is written, past the caches too: outputs over the inputs, and over the upstream
+    gradients, have the bits of outputs of their own, eagerly and replayed."""
+    g, sh = ops.gen(36), ops.shape(d, act=act)
+    i, _ = ops.norm_inputs(g, T, d, act, 2, 1, 1)
+    up = [ops.rand(g, T, d, dtype=act) for _ in range(2)]
+    tail = (i["post"], i["pre"], i["gate"], 2, ops.ALPHA, EPS)
+    want = [torch.empty_like(i["x"]) for _ in range(2)]
+    m.moe_block_norm(sh, i["x"], i["y"], T, *tail, *want)
+    grads = ops.norm_gradients(sh, i, T, d, act, 2, 1, 1, *up)
+    x, y, gate, a, b = (torch.empty_like(i["x"]) for _ in range(5))
+    ws, sums = m.workspace(sh, T), [torch.empty(d, device="cuda") for _ in range(2)]
+
+    def fill():
+        for dst, src in ((x, i["x"]), (y, i["y"]), (gate, i["gate"]), (a, up[0]), (b, up[1])):
+            dst.copy_(src)
+
+    def forward():
+        m.moe_block_norm(sh, x, y, T, i["post"], i["pre"], gate, 2, ops.ALPHA, EPS, x, y)
+
+    def backward():
+        m.moe_block_norm_backward(sh, x, y, T, i["post"], i["pre"], gate, 2, ops.ALPHA, EPS, a, b, a, b, gate, *sums, ws)
+
+    for run, out in ((forward, ((x, want[0]), (y, want[1]))),
+                     (backward, ((a, grads["dx"]), (b, grads["dy"]), (gate, grads["d_gate"]), (sums[0], grads["d_post"]),
+                                 (sums[1], grads["d_pre"])))):
+        fill()
+        run()
+        torch.cuda.synchronize()
+        for got, ref_bits in out:
+            assert torch.equal(got, ref_bits)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(3):
+            fill()
+            graph.replay()
+            torch.cuda.synchronize()
+            for got, ref_bits in out:
+                assert torch.equal(got, ref_bits)
+
+
 # ---------------------------------------------------------------------------------------------
 # tokens by expert
 # ---------------------------------------------------------------------------------------------
