@@ -350,6 +350,17 @@ moe_status moe_block_norm(const moe_shape *shape, const void *x, const void *y, 
                           int32_t gate_kind, float residual_scale, float eps, void *x_out,
                           void *normed, hipStream_t stream);
 
+/* moe_block_norm with the normed row in MXFP8, for 8-bit products behind it (moe_matmul, moe_gated): instead of
+ * normed, codes ([T][d_model] E4M3FN bytes) and scales ([T][d_model/32] bytes b: 2^(b-127)) as MOE_AQ_MXFP8 defines
+ * them, quantised from the fp32 values; a block of 32 with an infinity or a NaN gets scale byte 255 (NaN) and codes
+ * of zero.  With pre_gamma NULL the row u itself is quantised; with y NULL too, u is x (rows of x, or of a weight
+ * with d_model columns, in MXFP8).  codes and scales are both given; x_out may be NULL.  codes 16-byte aligned; codes
+ * and scales alias nothing. */
+moe_status moe_block_norm_mx8(const moe_shape *shape, const void *x, const void *y, int32_t T,
+                              const float *post_gamma, const float *pre_gamma, const void *gate,
+                              int32_t gate_kind, float residual_scale, float eps, void *x_out,
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
+
 /* moe_combine and moe_block_norm in one pass: the same with
  *   y[t] = routed_scaling * sum_j topk_w[t,j] * o[pick_pos[t,j]] (+ o[T*top_k + t])
  * summed as in moe_combine (without its residual) and never rounded or written.  For callers that run
@@ -401,6 +412,79 @@ typedef struct {
 
 moe_status moe_linear(const moe_matrix *matrix, const uint8_t *q, const uint8_t *s, float tensor_scale,
                       const void *x, int32_t T, const float *bias, void *y, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Dense products beside the experts, for any number of tokens: projections, heads and the dense
+ * feed-forward blocks of the layers without experts, for serving and, with their gradients, for
+ * training.
+ *
+ * moe_dense describes one: rows outputs (of the gated block: columns of h) and cols inputs.
+ *   operands MOE_OPERANDS_ACT: x and the weight in act_dtype.  bf16 values enter the products as they are.  fp32
+ *     values enter as three bf16 terms each, of which the six largest products are summed (what is left out is
+ *     below 2^-24 of |x| |W|); bits below 2^-133 are left out, and a sum that an infinity enters is infinite or NaN.
+ *   operands MOE_OPERANDS_MXFP8: x and the weight as E4M3FN codes with a scale byte for each 32 consecutive columns
+ *     (moe_block_norm_mx8 writes both), x_scales [T][cols/32] and w_scales [weight rows][cols/32]; forward only.
+ *     With bf16 outputs the sums are the scaled FP8 matrix cores', which cut the products of eight neighbouring codes to
+ *     2^-13 of the largest before they add them (1.5e-5 of a result); with fp32 outputs the values enter bf16 products,
+ *     whose sums are right to fp32.
+ *   Sums are fp32; y, h, pre, dx and dw are rounded once to act_dtype.
+ * Limits: rows a multiple of 8, cols of 8 (MXFP8: of 128), each at most 2^20, rows * cols at most 2^33,
+ * T <= 65536 (MOE_ERR_UNSUPPORTED beyond).  Pointers are 16-byte aligned (scales of operands: 4 bytes; of h: any).
+ * Arrays are contiguous, and outputs alias neither inputs nor one another unless a call says so.
+ *
+ * ws: a workspace of moe_dense_workspace_bytes(dense, T) bytes, 256-byte aligned, for the calls below with that
+ * description (any activation) and at most T tokens.  It needs no preparation, and nothing in it outlives a call;
+ * calls that overlap in time need distinct ones.
+ * --------------------------------------------------------------------------------------- */
+typedef enum { MOE_OPERANDS_ACT = 0, MOE_OPERANDS_MXFP8 = 1 } moe_operands;
+
+/* SILU v sigmoid(v); GELU v Phi(v), Phi the normal distribution's function (erf); SIGMOID 1 / (1 + exp(-v)). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_SIGMOID = 3 } moe_activation;
+
+typedef struct {
+    int32_t rows;
+    int32_t cols;
+    int32_t act_dtype;    /* moe_dtype      */
+    int32_t operands;     /* moe_operands   */
+    int32_t activation;   /* moe_activation */
+} moe_dense;
+
+/* Workspace of the calls below; 0 for a bad description or T.  It does not fall as T grows. */
+size_t moe_dense_workspace_bytes(const moe_dense *dense, int32_t T);
+
+/* y[t,n] = f(v[t,n]) (+ residual[t,n]),  v[t,n] = sum_k W[n,k] x[t,k] (+ bias[n]),  f the activation.
+ * x: [T][cols]; w: [rows][cols]; bias: [rows] fp32 or NULL; residual: [T][rows] act_dtype or NULL, which may be y;
+ * pre: NULL, or [T][rows] act_dtype for v, which the gradient needs if there is an activation; y: [T][rows]
+ * act_dtype.  x_scales and w_scales are given with MOE_OPERANDS_MXFP8 and NULL without. */
+moe_status moe_matmul(const moe_dense *dense, const void *x, const uint8_t *x_scales, int32_t T, const void *w,
+                      const uint8_t *w_scales, const float *bias, const void *residual, void *pre, void *y,
+                      void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradient of moe_matmul for an upstream dy ([T][rows] act_dtype; the residual's gradient is dy itself): with
+ * d[t,n] = dy[t,n] f'(pre[t,n]),
+ *   dx = d W ([T][cols]),  dw = d^T x ([rows][cols]),  both act_dtype,  d_bias[n] = sum_t d[t,n] (fp32).
+ * For the two products d is rounded to bf16 with bf16 activations; d_bias is summed before that, in a fixed order
+ * (no atomics).  pre is given exactly if there is an activation.  Outputs that are not wanted are NULL (one is
+ * given); x is needed for dw, w for dx.  T = 0 writes zeros to dw and d_bias. */
+moe_status moe_matmul_backward(const moe_dense *dense, const void *x, int32_t T, const void *w, const void *pre,
+                               const void *dy, void *dx, void *dw, float *d_bias, void *ws, size_t ws_bytes,
+                               hipStream_t stream);
+
+/* The gated block's first half, both projections in one product:
+ *   h[t,n] = f(g[t,n]) u[t,n],  g[t,n] = sum_k W[n,k] x[t,k],  u[t,n] = sum_k W[rows+n,k] x[t,k].
+ * w: [2 rows][cols], the gate's rows and then the up projection's.  pre: NULL, or [T][2 rows] act_dtype for g and
+ * then u of each token, which the gradient needs.  h: [T][rows] act_dtype; or, with h_scales ([T][rows/32], rows a
+ * multiple of 32), E4M3FN codes of h in MXFP8, for an 8-bit product behind it (as moe_block_norm_mx8 writes them). */
+moe_status moe_gated(const moe_dense *dense, const void *x, const uint8_t *x_scales, int32_t T, const void *w,
+                     const uint8_t *w_scales, void *pre, void *h, uint8_t *h_scales, void *ws, size_t ws_bytes,
+                     hipStream_t stream);
+
+/* Gradient of moe_gated from pre and an upstream dh ([T][rows] act_dtype): with d[t,n] = dh u f'(g) and
+ * d[t,rows+n] = dh f(g),  dx = d W ([T][cols]) and dw = d^T x ([2 rows][cols]), both act_dtype; either may be NULL.
+ * d is rounded to bf16 for the two products with bf16 activations.  x is needed for dw, w for dx.  T = 0 writes
+ * zeros to dw. */
+moe_status moe_gated_backward(const moe_dense *dense, const void *x, int32_t T, const void *w, const void *pre,
+                              const void *dh, void *dx, void *dw, void *ws, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,8 @@ MOE_DT_F32, MOE_DT_BF16 = 0, 1
 MOE_WF_MXFP4, MOE_WF_NVFP4 = 0, 1
 MOE_AQ_EXACT, MOE_AQ_MXFP8 = 0, 1
 MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2
+MOE_OPERANDS_ACT, MOE_OPERANDS_MXFP8 = 0, 1
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SIGMOID = 0, 1, 2, 3
 MOE_WS_STATUS_OFFSET = 0
 MOE_WS_ROUTE_TIMEOUT, MOE_WS_BAD_EXPERT_ID = 0x1, 0x2
 
@@ -53,6 +55,11 @@ class moe_matrix(ctypes.Structure):
                 ("act_dtype", ctypes.c_int32)]
 
 
+class moe_dense(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("operands", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
 EXPERT_BYTES = ctypes.sizeof(moe_expert)
 
 if not os.path.exists(LIB_PATH):
@@ -65,6 +72,7 @@ _SP = ctypes.POINTER(moe_shape)
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
 _f32 = ctypes.c_float
+_DP = ctypes.POINTER(moe_dense)
 TRACE_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int, ctypes.c_void_p)
 EVENT_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_char_p, ctypes.POINTER(ctypes.c_void_p),
                               ctypes.POINTER(ctypes.c_void_p))
@@ -99,6 +107,12 @@ _SIGS = {
     "moe_block_norm_backward": (ctypes.c_int, [_SP, _P, _P, _i32, _P, _P, _P, _i32, _f32, _f32, _P, _P, _P, _P, _P, _P,
                                                _P, _P, _sz, _P]),
     "moe_linear": (ctypes.c_int, [ctypes.POINTER(moe_matrix), _P, _P, _f32, _P, _i32, _P, _P, _P]),
+    "moe_block_norm_mx8": (ctypes.c_int, [_SP, _P, _P, _i32, _P, _P, _P, _i32, _f32, _f32, _P, _P, _P, _P]),
+    "moe_dense_workspace_bytes": (_sz, [_DP, _i32]),
+    "moe_matmul": (ctypes.c_int, [_DP, _P, _P, _i32, _P, _P, _P, _P, _P, _P, _P, _sz, _P]),
+    "moe_matmul_backward": (ctypes.c_int, [_DP, _P, _i32, _P, _P, _P, _P, _P, _P, _P, _sz, _P]),
+    "moe_gated": (ctypes.c_int, [_DP, _P, _P, _i32, _P, _P, _P, _P, _P, _P, _sz, _P]),
+    "moe_gated_backward": (ctypes.c_int, [_DP, _P, _i32, _P, _P, _P, _P, _P, _P, _sz, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -355,6 +369,28 @@ def moe_block_norm(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: 
                                                  residual_scale, eps, pxo, pn, _stream(stream)))
 
 
+def _eight_bits(t, kind: str):
+    """dtype of a tensor of MXFP8 codes or scales: torch's float8 type of that name, or its bytes as uint8."""
+    import torch
+    if t is not None and not isinstance(t, int) and t.dtype is getattr(torch, kind):
+        return t.dtype
+    return torch.uint8
+
+
+def moe_block_norm_mx8(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
+                       eps: float, x_out, codes, scales, stream=None):
+    """codes: float8_e4m3fn or uint8; scales: float8_e8m0fnu or uint8."""
+    act, f32, _, _ = _dtypes(shape.act_dtype)
+    d = shape.d_model
+    n = T * d
+    px, py, ppost, ppre, pg, pxo, pc, ps = _pointers(
+        "moe_block_norm_mx8", (x, act, n), (y, act, n), (post_gamma, f32, d), (pre_gamma, f32, d),
+        (gate, f32, T) if gate_kind == MOE_GATE_TOKEN else (gate, act, n), (x_out, act, n),
+        (codes, _eight_bits(codes, "float8_e4m3fn"), n), (scales, _eight_bits(scales, "float8_e8m0fnu"), n // 32))
+    _check("moe_block_norm_mx8", _lib.moe_block_norm_mx8(ctypes.byref(shape), px, py, T, ppost, ppre, pg, gate_kind,
+                                                         residual_scale, eps, pxo, pc, ps, _stream(stream)))
+
+
 def moe_combine_norm(shape, o, topk_w, pick_pos, x, T: int, post_gamma, pre_gamma, gate, gate_kind: int,
                      residual_scale: float, eps: float, x_out, normed, stream=None):
     act, f32, i32, _ = _dtypes(shape.act_dtype)
@@ -398,3 +434,84 @@ def moe_linear(matrix, q, s, tensor_scale: float, x, T: int, bias, y, stream=Non
                                    (s, u8, N * K // (32 if matrix.wformat == MOE_WF_MXFP4 else 16)), (x, act, T * K),
                                    (bias, f32, N), (y, act, T * N))
     _check("moe_linear", _lib.moe_linear(ctypes.byref(matrix), pq, ps, tensor_scale, px, T, pb, py, _stream(stream)))
+
+
+# dense products: the codes of MXFP8 operands (and of h) are float8_e4m3fn or uint8 tensors, their scales
+# float8_e8m0fnu or uint8
+
+def make_dense(rows: int, cols: int, act_dtype: int = MOE_DT_BF16, operands: int = MOE_OPERANDS_ACT,
+               activation: int = MOE_ACT_NONE) -> moe_dense:
+    return moe_dense(rows, cols, act_dtype, operands, activation)
+
+
+def moe_dense_workspace_bytes(dense: moe_dense, T: int) -> int:
+    return _lib.moe_dense_workspace_bytes(ctypes.byref(dense), T)
+
+
+def dense_workspace(dense: moe_dense, T: int, device="cuda"):
+    """A uint8 device tensor of moe_dense_workspace_bytes(dense, T) bytes (its contents do not matter)."""
+    import torch
+    return torch.empty(max(moe_dense_workspace_bytes(dense, T), 256), dtype=torch.uint8, device=device)
+
+
+def _scratch(ws, ws_bytes):
+    """(the _pointers triple of a workspace, its size in bytes)"""
+    if ws is None or isinstance(ws, int):
+        return (ws, None, 0), ws_bytes or 0
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    return (ws, ws.dtype, -(-ws_bytes // ws.element_size())), ws_bytes
+
+
+def _operands(dense, x, x_scales, T: int, w, w_scales, R: int) -> list:
+    """_pointers triples of a forward call's operands, R weight rows."""
+    act, K = _dtypes(dense.act_dtype)[0], dense.cols
+    if dense.operands == MOE_OPERANDS_ACT:
+        return [(x, act, T * K), (x_scales, None, 0), (w, act, R * K), (w_scales, None, 0)]
+    return [(x, _eight_bits(x, "float8_e4m3fn"), T * K), (x_scales, _eight_bits(x_scales, "float8_e8m0fnu"), T * K // 32),
+            (w, _eight_bits(w, "float8_e4m3fn"), R * K), (w_scales, _eight_bits(w_scales, "float8_e8m0fnu"), R * K // 32)]
+
+
+def moe_matmul(dense, x, x_scales, T: int, w, w_scales, bias, residual, pre, y, ws, ws_bytes=None, stream=None):
+    act, f32, _, _ = _dtypes(dense.act_dtype)
+    N = dense.rows
+    scratch, ws_bytes = _scratch(ws, ws_bytes)
+    px, pxs, pw, pws, pb, pr, pp, py, ps = _pointers(
+        "moe_matmul", *_operands(dense, x, x_scales, T, w, w_scales, N), (bias, f32, N), (residual, act, T * N),
+        (pre, act, T * N), (y, act, T * N), scratch)
+    _check("moe_matmul", _lib.moe_matmul(ctypes.byref(dense), px, pxs, T, pw, pws, pb, pr, pp, py, ps, ws_bytes,
+                                         _stream(stream)))
+
+
+def moe_matmul_backward(dense, x, T: int, w, pre, dy, dx, dw, d_bias, ws, ws_bytes=None, stream=None):
+    act, f32, _, _ = _dtypes(dense.act_dtype)
+    N, K = dense.rows, dense.cols
+    scratch, ws_bytes = _scratch(ws, ws_bytes)
+    px, pw, pp, pdy, pdx, pdw, pdb, ps = _pointers(
+        "moe_matmul_backward", (x, act, T * K), (w, act, N * K), (pre, act, T * N), (dy, act, T * N), (dx, act, T * K),
+        (dw, act, N * K), (d_bias, f32, N), scratch)
+    _check("moe_matmul_backward", _lib.moe_matmul_backward(ctypes.byref(dense), px, T, pw, pp, pdy, pdx, pdw, pdb, ps,
+                                                           ws_bytes, _stream(stream)))
+
+
+def moe_gated(dense, x, x_scales, T: int, w, w_scales, pre, h, h_scales, ws, ws_bytes=None, stream=None):
+    act = _dtypes(dense.act_dtype)[0]
+    N = dense.rows
+    scratch, ws_bytes = _scratch(ws, ws_bytes)
+    px, pxs, pw, pws, pp, ph, phs, ps = _pointers(
+        "moe_gated", *_operands(dense, x, x_scales, T, w, w_scales, 2 * N), (pre, act, 2 * T * N),
+        (h, act if h_scales is None else _eight_bits(h, "float8_e4m3fn"), T * N),
+        (h_scales, _eight_bits(h_scales, "float8_e8m0fnu"), T * N // 32), scratch)
+    _check("moe_gated", _lib.moe_gated(ctypes.byref(dense), px, pxs, T, pw, pws, pp, ph, phs, ps, ws_bytes,
+                                       _stream(stream)))
+
+
+def moe_gated_backward(dense, x, T: int, w, pre, dh, dx, dw, ws, ws_bytes=None, stream=None):
+    act = _dtypes(dense.act_dtype)[0]
+    N, K = dense.rows, dense.cols
+    scratch, ws_bytes = _scratch(ws, ws_bytes)
+    px, pw, pp, pdh, pdx, pdw, ps = _pointers(
+        "moe_gated_backward", (x, act, T * K), (w, act, 2 * N * K), (pre, act, 2 * T * N), (dh, act, T * N), (dx, act, T * K),
+        (dw, act, 2 * N * K), scratch)
+    _check("moe_gated_backward", _lib.moe_gated_backward(ctypes.byref(dense), px, T, pw, pp, pdh, pdx, pdw, ps, ws_bytes,
+                                                         _stream(stream)))

@@ -3,9 +3,10 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
-#include "block_ops.h"
+#include "dense.h"
 
 namespace moe {
 
@@ -344,6 +345,144 @@ static moe_status check_norm_rows(const NormArgs& a, bool has_y) {
     return MOE_OK;
 }
 
+// ---------------------------------------------------------------------------------------------
+// dense products: R weight rows (the gated block's gate and up projection: 2 rows), workspace
+// ---------------------------------------------------------------------------------------------
+static moe_status check_dense(const moe_dense* m, int32_t T) {
+    if (!m || m->rows <= 0 || m->cols <= 0 || T < 0) return MOE_ERR_INVALID;
+    if (m->act_dtype != MOE_DT_F32 && m->act_dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (m->operands != MOE_OPERANDS_ACT && m->operands != MOE_OPERANDS_MXFP8) return MOE_ERR_INVALID;
+    if (m->activation < MOE_ACT_NONE || m->activation > MOE_ACT_SIGMOID) return MOE_ERR_INVALID;
+    if (T > 65536 || m->rows > (1 << 20) || m->cols > (1 << 20) || (long long)m->rows * m->cols > (1LL << 33))
+        return MOE_ERR_UNSUPPORTED;
+    if (m->rows % 8 != 0 || m->cols % (m->operands == MOE_OPERANDS_MXFP8 ? 128 : 8) != 0) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// regions of a call's workspace
+struct DenseLayout {
+    size_t d, xp, wp, bias, part, total;
+};
+static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool backward) {
+    // bytes per value of the operands' bf16 copies, where there are any: three planes of fp32 values; MXFP8 values for
+    // fp32 outputs
+    const size_t copies = m->act_dtype != MOE_DT_F32 ? 0 : m->operands == MOE_OPERANDS_ACT ? 6 : 2;
+    const size_t K = m->cols, t = T;
+    DenseLayout L;
+    size_t o = 0;
+    auto take = [&](size_t bytes) { size_t at = o; o += align256(bytes); return at; };
+    L.d = take(backward ? t * R * (copies ? copies : 2) : 0);
+    L.xp = take(t * K * copies);
+    L.wp = take(R * K * copies);
+    L.bias = take(backward ? (size_t)kBiasChunks * m->rows * 4 : 0);
+    size_t part = product_part_bytes(backward ? R : t, backward ? K : R);
+    if (backward && product_part_bytes(t, K) > part) part = product_part_bytes(t, K);
+    L.part = take(part);
+    L.total = o;
+    return L;
+}
+
+static ProductArgs product_args(const moe_dense* m, int I, int J, int K, void* out) {
+    ProductArgs a;
+    memset(&a, 0, sizeof a);
+    a.I = I;
+    a.J = J;
+    a.K = K;
+    a.pairs = 1;
+    a.activation = MOE_ACT_NONE;
+    a.out_f32 = m->act_dtype == MOE_DT_F32;
+    a.out = out;
+    return a;
+}
+
+// the forward product of R weight rows: operands, planes of fp32 ones, and the launch
+static moe_status run_forward(const moe_dense* m, const void* x, const uint8_t* x_scales, int32_t T, const void* w,
+                              const uint8_t* w_scales, size_t R, ProductArgs a, uint8_t* ws, const DenseLayout& L,
+                              hipStream_t st) {
+    const bool mx8 = m->operands == MOE_OPERANDS_MXFP8, f32 = m->act_dtype == MOE_DT_F32;
+    const size_t K = m->cols;
+    uint16_t *xp = (uint16_t*)(ws + L.xp), *wp = (uint16_t*)(ws + L.wp);
+    a.p = f32 ? (const uint8_t*)xp : (const uint8_t*)x;
+    a.q = f32 ? (const uint8_t*)wp : (const uint8_t*)w;
+    a.p_ld = a.q_ld = (int)(mx8 && !f32 ? K : 2 * K);
+    a.p_scales = x_scales;
+    a.q_scales = w_scales;
+    a.activation = m->activation;
+    a.part = (float*)(ws + L.part);
+    if (f32 && mx8) {
+        // the scaled matrix cores' sums are right to about 1.5e-5 of a result, bf16 ones to fp32
+        MOE_HIP(launch_unpack((const uint8_t*)x, x_scales, T * K, xp, st));
+        MOE_HIP(launch_unpack((const uint8_t*)w, w_scales, R * K, wp, st));
+    } else if (f32) {
+        MOE_HIP(launch_planes((const float*)x, T * K, xp, st));
+        MOE_HIP(launch_planes((const float*)w, R * K, wp, st));
+        a.p_plane = T * K * 2;
+        a.q_plane = R * K * 2;
+        a.pairs = 6;
+    }
+    return hip_status(launch_product(a, mx8 && !f32, false, false, a.J != m->rows, st));
+}
+
+// dx = d W and dw = d^T x, d ([T][R]) being the pre-activations' gradient
+static moe_status run_backward(const moe_dense* m, const void* x, int32_t T, const void* w, size_t R, const void* d,
+                               void* dx, void* dw, uint8_t* ws, const DenseLayout& L, hipStream_t st) {
+    const bool f32 = m->act_dtype == MOE_DT_F32;
+    const size_t K = m->cols;
+    ProductArgs a = product_args(m, T, (int)K, (int)R, dx);
+    a.part = (float*)(ws + L.part);
+    a.pairs = f32 ? 6 : 1;
+    a.p = (const uint8_t*)d;
+    a.p_plane = T * R * 2;
+    a.p_ld = (int)(2 * R);
+    a.q_ld = (int)(2 * K);
+    if (dx) {
+        a.q = (const uint8_t*)w;
+        if (f32) {
+            MOE_HIP(launch_planes((const float*)w, R * K, (uint16_t*)(ws + L.wp), st));
+            a.q = ws + L.wp;
+            a.q_plane = R * K * 2;
+        }
+        MOE_HIP(launch_product(a, false, false, true, false, st));
+    }
+    if (dw) {
+        a.I = (int)R;
+        a.K = T;
+        a.out = dw;
+        a.q = (const uint8_t*)x;
+        if (f32) {
+            MOE_HIP(launch_planes((const float*)x, T * K, (uint16_t*)(ws + L.xp), st));
+            a.q = ws + L.xp;
+            a.q_plane = T * K * 2;
+        }
+        MOE_HIP(launch_product(a, false, true, true, false, st));
+    }
+    return MOE_OK;
+}
+
+static bool all_aligned(std::initializer_list<const void*> ps, size_t to) {
+    for (const void* p : ps)
+        if (p && !aligned(p, to)) return false;
+    return true;
+}
+// no output in the place of an input or of another output
+static bool apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (auto q = outs.begin(); q != o; ++q)
+            if (*q == *o) return false;
+        for (const void* i : ins)
+            if (i == *o) return false;
+    }
+    return true;
+}
+// the operands of a forward call
+static moe_status check_operands(const moe_dense* m, const void* x, const uint8_t* x_scales, const void* w,
+                                 const uint8_t* w_scales) {
+    const bool mx8 = m->operands == MOE_OPERANDS_MXFP8;
+    if (!x || !w || mx8 != (x_scales != nullptr) || mx8 != (w_scales != nullptr)) return MOE_ERR_INVALID;
+    return all_aligned({x, w}, 16) && all_aligned({x_scales, w_scales}, 4) ? MOE_OK : MOE_ERR_INVALID;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -526,6 +665,25 @@ moe_status moe_block_norm(const moe_shape* s, const void* x, const void* y, int3
     return hip_status(launch_block_norm(s, a, stream));
 }
 
+moe_status moe_block_norm_mx8(const moe_shape* s, const void* x, const void* y, int32_t T, const float* post_gamma,
+                              const float* pre_gamma, const void* gate, int32_t gate_kind, float residual_scale, float eps,
+                              void* x_out, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+    MOE_TRY(check_shape(s));
+    MOE_TRY(check_T(s, T));
+    NormArgs a = norm_args(s, x, T, post_gamma, pre_gamma, gate, gate_kind, residual_scale, eps);
+    a.y = y;
+    a.x_out = x_out;
+    a.codes = codes;
+    a.scales = scales;
+    MOE_TRY(check_norm(a));
+    if (T == 0) return MOE_OK;
+    if (!x || !codes || !scales || (!y && (post_gamma || gate))) return MOE_ERR_INVALID;
+    const void* element = gate_kind == MOE_GATE_ELEMENT ? gate : nullptr;
+    if (!all_aligned({x, y, x_out, codes, post_gamma, pre_gamma, element}, 16)) return MOE_ERR_INVALID;
+    if (!apart({codes, scales}, {x, y, x_out, gate, post_gamma, pre_gamma})) return MOE_ERR_INVALID;
+    return hip_status(launch_block_norm(s, a, stream));
+}
+
 moe_status moe_combine_norm(const moe_shape* s, const float* o, const float* topk_w, const int32_t* pick_pos,
                             const void* x, int32_t T, const float* post_gamma, const float* pre_gamma, const void* gate,
                             int32_t gate_kind, float residual_scale, float eps, void* x_out, void* normed,
@@ -607,6 +765,96 @@ moe_status moe_linear(const moe_matrix* m, const uint8_t* q, const uint8_t* s, f
     if (!aligned(q, 16) || !aligned(s, 16) || !aligned(x, 16) || !aligned(y, 16) || (bias && !aligned(bias, 4)))
         return MOE_ERR_INVALID;
     return hip_status(launch_linear(m, q, s, tensor_scale, x, T, bias, y, stream));
+}
+
+size_t moe_dense_workspace_bytes(const moe_dense* m, int32_t T) {
+    if (check_dense(m, T) != MOE_OK) return 0;
+    if (T == 0) return 256;
+    const size_t forward = dense_layout(m, T, 2 * (size_t)m->rows, false).total;
+    if (m->operands == MOE_OPERANDS_MXFP8) return forward;
+    const size_t backward = dense_layout(m, T, 2 * (size_t)m->rows, true).total;
+    return forward > backward ? forward : backward;
+}
+
+moe_status moe_matmul(const moe_dense* m, const void* x, const uint8_t* x_scales, int32_t T, const void* w,
+                      const uint8_t* w_scales, const float* bias, const void* residual, void* pre, void* y, void* ws,
+                      size_t ws_bytes, hipStream_t stream) {
+    MOE_TRY(check_dense(m, T));
+    if (T == 0) return MOE_OK;
+    MOE_TRY(check_operands(m, x, x_scales, w, w_scales));
+    if (!y || !ws || !all_aligned({bias, residual, pre, y}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
+    if (!apart({y, pre}, {x, x_scales, w, w_scales, bias}) || (pre && pre == residual)) return MOE_ERR_INVALID;
+    const DenseLayout L = dense_layout(m, T, m->rows, false);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    ProductArgs a = product_args(m, T, m->rows, m->cols, y);
+    a.bias = bias;
+    a.residual = residual;
+    a.pre = pre;
+    return run_forward(m, x, x_scales, T, w, w_scales, m->rows, a, (uint8_t*)ws, L, stream);
+}
+
+moe_status moe_gated(const moe_dense* m, const void* x, const uint8_t* x_scales, int32_t T, const void* w,
+                     const uint8_t* w_scales, void* pre, void* h, uint8_t* h_scales, void* ws, size_t ws_bytes,
+                     hipStream_t stream) {
+    MOE_TRY(check_dense(m, T));
+    if (h_scales && m->rows % 32 != 0) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    MOE_TRY(check_operands(m, x, x_scales, w, w_scales));
+    if (!h || !ws || !all_aligned({pre, h}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
+    if (!apart({h, h_scales, pre}, {x, x_scales, w, w_scales})) return MOE_ERR_INVALID;
+    const size_t R = 2 * (size_t)m->rows;
+    const DenseLayout L = dense_layout(m, T, R, false);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    ProductArgs a = product_args(m, T, (int)R, m->cols, h);
+    a.pre = pre;
+    a.out_scales = h_scales;
+    return run_forward(m, x, x_scales, T, w, w_scales, R, a, (uint8_t*)ws, L, stream);
+}
+
+// both backward calls; R: the weight's rows
+static moe_status dense_backward(const moe_dense* m, const void* x, int32_t T, const void* w, const void* pre,
+                                 const void* dy, void* dx, void* dw, float* d_bias, void* ws, size_t ws_bytes, bool gated,
+                                 hipStream_t stream) {
+    MOE_TRY(check_dense(m, T));
+    if (m->operands != MOE_OPERANDS_ACT) return MOE_ERR_UNSUPPORTED;
+    const bool f32 = m->act_dtype == MOE_DT_F32, wants_pre = gated || m->activation != MOE_ACT_NONE;
+    const size_t R = (size_t)m->rows * (gated ? 2 : 1);
+    // written whatever T is
+    if (!all_aligned({dw, d_bias}, 16) || !apart({dx, dw, d_bias}, {x, w, pre, dy})) return MOE_ERR_INVALID;
+    if (T == 0) {
+        if (dw) MOE_HIP(launch_ws_init((uint32_t*)dw, R * m->cols * (f32 ? 4 : 2) / 4, 0, stream));
+        if (d_bias) MOE_HIP(launch_ws_init((uint32_t*)d_bias, m->rows, 0, stream));
+        return MOE_OK;
+    }
+    if (!dy || !ws || (!dx && !dw && !d_bias) || (dx && !w) || (dw && !x) || wants_pre != (pre != nullptr)) return MOE_ERR_INVALID;
+    if (!all_aligned({x, w, pre, dy, dx}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
+    const DenseLayout L = dense_layout(m, T, R, true);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    uint8_t* w8 = (uint8_t*)ws;
+    const bool as_is = !wants_pre && !f32;       // dy itself is the pre-activations' gradient
+    PreGradArgs g;
+    memset(&g, 0, sizeof g);
+    g.T = T;
+    g.N = m->rows;
+    g.activation = m->activation;
+    g.gated = gated;
+    g.dy = dy;
+    g.pre = pre;
+    g.d = as_is || (!dx && !dw) ? nullptr : (uint16_t*)(w8 + L.d);
+    g.bias_part = d_bias ? (float*)(w8 + L.bias) : nullptr;
+    g.d_bias = d_bias;
+    if (g.d || d_bias) MOE_HIP(launch_pre_grad(g, f32, stream));
+    return run_backward(m, x, T, w, R, as_is ? dy : w8 + L.d, dx, dw, w8, L, stream);
+}
+
+moe_status moe_matmul_backward(const moe_dense* m, const void* x, int32_t T, const void* w, const void* pre, const void* dy,
+                               void* dx, void* dw, float* d_bias, void* ws, size_t ws_bytes, hipStream_t stream) {
+    return dense_backward(m, x, T, w, pre, dy, dx, dw, d_bias, ws, ws_bytes, false, stream);
+}
+
+moe_status moe_gated_backward(const moe_dense* m, const void* x, int32_t T, const void* w, const void* pre, const void* dh,
+                              void* dx, void* dw, void* ws, size_t ws_bytes, hipStream_t stream) {
+    return dense_backward(m, x, T, w, pre, dh, dx, dw, nullptr, ws, ws_bytes, true, stream);
 }
 
 moe_status moe_layer(const moe_shape* s, const void* x, int32_t T, const float* w_router,

@@ -87,6 +87,37 @@ __device__ __forceinline__ void store_act8(XT* p, size_t i, const f32x8& r) {
     }
     store16<NT>(p + i, w[0]);
 }
+// ---------------------------------------------------------------------------------------------
+// MXFP8: a block of 32 values shares the scale 2^S of split_exponent (max / 2^S < 256).  A block with an infinity
+// or a NaN gets the NaN scale byte 255, and codes of zero.
+// ---------------------------------------------------------------------------------------------
+// this lane's largest magnitude, infinite where one of its values is not finite
+__device__ __forceinline__ float mx8_amax(const f32x8& v) {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_isfinite(v.v[e]) ? fabsf(v.v[e]) : __builtin_inff());
+    return m;
+}
+// the largest of four neighbouring lanes, in each
+__device__ __forceinline__ float quad_max(float m) {
+    m = fmaxf(m, __uint_as_float(dpp_u32<kDppXor1, 0xF>(__float_as_uint(m), __float_as_uint(m))));
+    return fmaxf(m, __uint_as_float(dpp_u32<kDppXor2, 0xF>(__float_as_uint(m), __float_as_uint(m))));
+}
+// eight codes and the scale byte of a block whose largest magnitude is amax
+__device__ __forceinline__ uint2 mx8_codes(const f32x8& v, float amax, uint8_t* scale) {
+    if (!__builtin_isfinite(amax)) {
+        *scale = 0xFF;
+        return make_uint2(0, 0);
+    }
+    const int S = split_exponent(amax);
+    const float sc = pow2f(S);
+    *scale = (uint8_t)(S + 127);
+    uint2 c;
+    c.x = fp8x2_encode<true>(fp8x2_encode<false>(0u, v.v[0], v.v[1], sc), v.v[2], v.v[3], sc);
+    c.y = fp8x2_encode<true>(fp8x2_encode<false>(0u, v.v[4], v.v[5], sc), v.v[6], v.v[7], sc);
+    return c;
+}
+
 // Bytes of an expert-side array from which the dispatch's and the gradients' rows go past the caches: the last-level
 // cache's size.  Below it the next kernel finds them there: 128 MB (2048 tokens, d 4096, 8 picks, bf16) dispatched
 // and read again 53 us, past the caches 63.  Above it, d 4096, us, past the caches and through them: dispatch of 256 MB 55,
@@ -150,6 +181,8 @@ struct NormArgs {
     float alpha, eps;         // residual scale, eps
     void* x_out;              // or null
     void* normed;             // or null
+    uint8_t* codes;           // or null: what would be normed, in MXFP8 (without a pre-norm: x_out, unrounded)
+    uint8_t* scales;
 };
 hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t st);   // a.o: fused with the combine
 

@@ -1,0 +1,137 @@
+// Declarations of the dense products (dense.hip, dense_rows.hip): operand planes, the products' arguments, the
+// epilogue shared by the kernels, and the launchers.
+#pragma once
+
+#include "block_ops.h"
+
+namespace moe {
+
+// One product out[i][j] = sum_k P[i][k] Q[j][k], i < I, j < J, with its epilogue.  P and Q are bf16, MXFP8
+// codes, or the three bf16 planes of an fp32 operand; each is stored with k along its rows ([i][k]) or,
+// "k-major", across them ([k][i]).
+struct ProductArgs {
+    int I, J, K;
+    const uint8_t *p, *q;
+    size_t p_plane, q_plane;      // bytes from one plane of an fp32 operand to the next
+    int p_ld, q_ld;               // bytes of a stored row
+    const uint8_t *p_scales, *q_scales;   // MXFP8: [i][K/32], [j][K/32]
+    int pairs;                    // products of planes: 1, or 6 for fp32 operands
+    int splits;                   // parts of the sum over k; more than one: fp32 sums to part, [splits][I][J]
+    float* part;
+    // epilogue; the outputs' rows are J long (gated: N = J / 2)
+    int activation;
+    int out_f32;                  // type of residual, pre and out: fp32 or bf16
+    const float* bias;            // or null
+    const void* residual;         // or null
+    void* pre;                    // or null: the activation's argument (gated: both halves, [I][J])
+    void* out;
+    uint8_t* out_scales;          // or null; gated only: out in MXFP8
+};
+
+// ---------------------------------------------------------------------------------------------
+// activations, in fp32
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
+__device__ __forceinline__ float normal_cdf(float v) { return 0.5f * (1.0f + erff(v * 0.70710678118654752f)); }
+
+__device__ __forceinline__ float activate(int f, float v) {
+    switch (f) {
+        case MOE_ACT_SILU: return v * logistic(v);
+        case MOE_ACT_GELU: return v * normal_cdf(v);
+        case MOE_ACT_SIGMOID: return logistic(v);
+        default: return v;
+    }
+}
+// the activation's derivative
+__device__ __forceinline__ float slope(int f, float v) {
+    switch (f) {
+        case MOE_ACT_SILU: {
+            const float p = logistic(v);
+            return p * (1.0f + v * (1.0f - p));
+        }
+        case MOE_ACT_GELU: return normal_cdf(v) + v * 0.39894228040143268f * expf(-0.5f * v * v);
+        case MOE_ACT_SIGMOID: {
+            const float p = logistic(v);
+            return p * (1.0f - p);
+        }
+        default: return 1.0f;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// epilogues of eight consecutive columns of one row
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void store_out8(const ProductArgs& a, void* p, size_t i, const f32x8& v) {
+    if (a.out_f32) store_act8((float*)p, i, v);
+    else store_act8((uint16_t*)p, i, v);
+}
+__device__ __forceinline__ void product_out8(const ProductArgs& a, int i, int j, f32x8 v) {
+    const size_t at = (size_t)i * a.J + j;
+    if (a.bias) {
+        const f32x8 b = load_act8(a.bias, (size_t)j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] += b.v[e];
+    }
+    if (a.pre) store_out8(a, a.pre, at, v);
+    if (a.activation != MOE_ACT_NONE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = activate(a.activation, v.v[e]);
+    }
+    if (a.residual) {
+        const f32x8 r = a.out_f32 ? load_act8((const float*)a.residual, at) : load_act8((const uint16_t*)a.residual, at);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] += r.v[e];
+    }
+    store_out8(a, a.out, at, v);
+}
+// gate g and up projection u of columns n .. n + 7 of h's row i.  block_max(m): the largest m of the four lanes that
+// hold a block of 32 columns; every lane of the wave calls this, valid or not.
+template <typename BlockMax>
+__device__ __forceinline__ void gated_out8(const ProductArgs& a, int i, int n, bool valid, const f32x8& g, const f32x8& u,
+                                           BlockMax block_max) {
+    const int N = a.J / 2;
+    if (valid && a.pre) {
+        store_out8(a, a.pre, (size_t)i * a.J + n, g);
+        store_out8(a, a.pre, (size_t)i * a.J + N + n, u);
+    }
+    f32x8 h;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h.v[e] = activate(a.activation, g.v[e]) * u.v[e];
+    if (a.out_scales) {
+        uint8_t scale;
+        const uint2 c = mx8_codes(h, block_max(mx8_amax(h)), &scale);
+        if (!valid) return;
+        *(uint2*)((uint8_t*)a.out + (size_t)i * N + n) = c;
+        if (n % 32 == 0) a.out_scales[(size_t)i * (N / 32) + n / 32] = scale;
+    } else if (valid) {
+        store_out8(a, a.out, (size_t)i * N + n, h);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// launchers; all return hipGetLastError() of their launches
+// ---------------------------------------------------------------------------------------------
+// bytes for the partial sums of any product of up to I rows and J columns
+size_t product_part_bytes(size_t I, size_t J);
+// mx8: MXFP8 operands; p_kmajor, q_kmajor: stored [k][i], [k][j] (bf16 only); gated: Q holds the gate's rows, then
+// the up projection's.  Chooses a.splits, given a.part with product_part_bytes(I, J) bytes.
+hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st);
+
+// fp32 [n] as three bf16 planes of n values, n a multiple of 8
+hipError_t launch_planes(const float* x, size_t n, uint16_t* planes, hipStream_t st);
+
+// MXFP8 [n] as bf16, which holds every code times its scale
+hipError_t launch_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, uint16_t* values, hipStream_t st);
+
+constexpr int kBiasChunks = 64;   // row chunks of the bias gradient's sums, at most
+struct PreGradArgs {
+    int T, N;                     // gated: pre and d are [T][2 N]
+    int activation, gated;
+    const void *dy, *pre;
+    uint16_t* d;                  // the pre-activations' gradient in bf16, or three planes for fp32; or null
+    float* bias_part;             // or null: [chunks][N]
+    float* d_bias;
+};
+hipError_t launch_pre_grad(const PreGradArgs& a, bool f32, hipStream_t st);
+
+}  // namespace moe

@@ -77,7 +77,8 @@ __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
 // Combined, 8 picks: 64 tokens, d 4096 5.7 us; 1001 tokens, d 6144, fp32, one to eight picks kept at random 44 us
 // (185 MB at 4.2 TB/s: two rows at a time on a CU do not cover each other's sums); kept 1, 8, 7, .. 2 in turn
 // 46, since workgroups go to the eight XCDs in turn.
-template <typename XT, int VPT, int COMBINE, bool LATE, bool NT>
+// MX8: the normed row goes out as MXFP8, a block of 32 columns in four neighbouring lanes.
+template <typename XT, int VPT, int COMBINE, bool LATE, bool NT, bool MX8 = false>
 __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
     __shared__ float s_post[16], s_pre[16];
     const int t = blockIdx.x;
@@ -137,16 +138,28 @@ __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[0] = fmaf(u[n].v[e], u[n].v[e], sum[0]);
     }
-    if (!a.normed) return;
-    block_sums(sum, s_pre);
-    const float r = inv_rms(sum[0], a.d, a.eps);
+    if (!MX8 && !a.normed) return;
+    float r = 1.0f;
+    if (!MX8 || a.pre) {
+        block_sums(sum, s_pre);
+        r = inv_rms(sum[0], a.d, a.eps);
+    }
 #pragma unroll
     for (int n = 0; n < VPT; ++n) {
         if (col(n) >= a.d) continue;
-        if constexpr (LATE) pre[n] = load_act8(a.pre, (size_t)col(n));
+        if (LATE && (!MX8 || a.pre)) pre[n] = load_act8(a.pre, (size_t)col(n));
+        if (!MX8 || a.pre) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[n].v[e] *= r * pre[n].v[e];
-        store_act8((XT*)a.normed, base + col(n), u[n]);        // the next kernel reads it
+            for (int e = 0; e < 8; ++e) u[n].v[e] *= r * pre[n].v[e];
+        }
+        if constexpr (MX8) {
+            uint8_t scale;
+            const uint2 c = mx8_codes(u[n], quad_max(mx8_amax(u[n])), &scale);
+            *(uint2*)(a.codes + base + col(n)) = c;
+            if (threadIdx.x % 4 == 0) a.scales[(base + col(n)) / 32] = scale;
+        } else {
+            store_act8((XT*)a.normed, base + col(n), u[n]);    // the next kernel reads it
+        }
     }
 }
 
@@ -189,10 +202,20 @@ static void norm_launch(const NormArgs& a, hipStream_t st) {
     }
 }
 
+template <typename XT>
+static void norm_mx8_launch(const NormArgs& a, hipStream_t st) {
+    int vpt;
+    const dim3 grid(a.T), block(norm_threads(a.d, &vpt));
+    if (vpt == 2) MOE_LAUNCH((k_block_norm<XT, 2, 0, true, false, true>), grid, block, 0, st, a);
+    else MOE_LAUNCH((k_block_norm<XT, 1, 0, false, false, true>), grid, block, 0, st, a);
+}
+
 hipError_t launch_block_norm(const moe_shape* s, const NormArgs& a, hipStream_t st) {
-    const char* name = a.o ? "combine_norm" : "block_norm";
+    const char* name = a.o ? "combine_norm" : a.codes ? "block_norm_mx8" : "block_norm";
     trace(name, 0, st);
-    if (s->act_dtype == MOE_DT_BF16) norm_launch<uint16_t>(a, st);
+    if (a.codes && s->act_dtype == MOE_DT_BF16) norm_mx8_launch<uint16_t>(a, st);
+    else if (a.codes) norm_mx8_launch<float>(a, st);
+    else if (s->act_dtype == MOE_DT_BF16) norm_launch<uint16_t>(a, st);
     else norm_launch<float>(a, st);
     trace(name, 1, st);
     return hipGetLastError();
