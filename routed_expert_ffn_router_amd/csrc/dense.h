@@ -34,12 +34,29 @@ struct ProductArgs {
 __device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
 __device__ __forceinline__ float normal_cdf(float v) { return 0.5f * (1.0f + erff(v * 0.70710678118654752f)); }
 
+template <int F>
+__device__ __forceinline__ float activate(float v) {
+    if constexpr (F == MOE_ACT_SILU) return v * logistic(v);
+    if constexpr (F == MOE_ACT_GELU) return v * normal_cdf(v);
+    if constexpr (F == MOE_ACT_SIGMOID) return logistic(v);
+    return v;
+}
 __device__ __forceinline__ float activate(int f, float v) {
     switch (f) {
-        case MOE_ACT_SILU: return v * logistic(v);
-        case MOE_ACT_GELU: return v * normal_cdf(v);
-        case MOE_ACT_SIGMOID: return logistic(v);
+        case MOE_ACT_SILU: return activate<MOE_ACT_SILU>(v);
+        case MOE_ACT_GELU: return activate<MOE_ACT_GELU>(v);
+        case MOE_ACT_SIGMOID: return activate<MOE_ACT_SIGMOID>(v);
         default: return v;
+    }
+}
+// f(StepPos<F>{}) for the activation F: one branch, outside the loops over rows, so that the code that runs is short
+template <typename Fn>
+__device__ __forceinline__ void with_activation(int activation, Fn&& f) {
+    switch (activation) {
+        case MOE_ACT_SILU: f(StepPos<MOE_ACT_SILU>{}); break;
+        case MOE_ACT_GELU: f(StepPos<MOE_ACT_GELU>{}); break;
+        case MOE_ACT_SIGMOID: f(StepPos<MOE_ACT_SIGMOID>{}); break;
+        default: f(StepPos<MOE_ACT_NONE>{});
     }
 }
 // the activation's derivative
@@ -65,6 +82,7 @@ __device__ __forceinline__ void store_out8(const ProductArgs& a, void* p, size_t
     if (a.out_f32) store_act8((float*)p, i, v);
     else store_act8((uint16_t*)p, i, v);
 }
+template <int F>
 __device__ __forceinline__ void product_out8(const ProductArgs& a, int i, int j, f32x8 v) {
     const size_t at = (size_t)i * a.J + j;
     if (a.bias) {
@@ -73,10 +91,8 @@ __device__ __forceinline__ void product_out8(const ProductArgs& a, int i, int j,
         for (int e = 0; e < 8; ++e) v.v[e] += b.v[e];
     }
     if (a.pre) store_out8(a, a.pre, at, v);
-    if (a.activation != MOE_ACT_NONE) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] = activate(a.activation, v.v[e]);
-    }
+    for (int e = 0; e < 8; ++e) v.v[e] = activate<F>(v.v[e]);
     if (a.residual) {
         const f32x8 r = a.out_f32 ? load_act8((const float*)a.residual, at) : load_act8((const uint16_t*)a.residual, at);
 #pragma unroll
@@ -84,11 +100,10 @@ __device__ __forceinline__ void product_out8(const ProductArgs& a, int i, int j,
     }
     store_out8(a, a.out, at, v);
 }
-// gate g and up projection u of columns n .. n + 7 of h's row i.  block_max(m): the largest m of the four lanes that
-// hold a block of 32 columns; every lane of the wave calls this, valid or not.
-template <typename BlockMax>
-__device__ __forceinline__ void gated_out8(const ProductArgs& a, int i, int n, bool valid, const f32x8& g, const f32x8& u,
-                                           BlockMax block_max) {
+// gate g and up projection u of columns n .. n + 7 of h's row i; a block of 32 columns is in four neighbouring lanes, and
+// every lane of them calls this, valid or not
+template <int F>
+__device__ __forceinline__ void gated_out8(const ProductArgs& a, int i, int n, bool valid, const f32x8& g, const f32x8& u) {
     const int N = a.J / 2;
     if (valid && a.pre) {
         store_out8(a, a.pre, (size_t)i * a.J + n, g);
@@ -96,10 +111,10 @@ __device__ __forceinline__ void gated_out8(const ProductArgs& a, int i, int n, b
     }
     f32x8 h;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h.v[e] = activate(a.activation, g.v[e]) * u.v[e];
+    for (int e = 0; e < 8; ++e) h.v[e] = activate<F>(g.v[e]) * u.v[e];
     if (a.out_scales) {
         uint8_t scale;
-        const uint2 c = mx8_codes(h, block_max(mx8_amax(h)), &scale);
+        const uint2 c = mx8_codes(h, quad_max(mx8_amax(h)), &scale);
         if (!valid) return;
         *(uint2*)((uint8_t*)a.out + (size_t)i * N + n) = c;
         if (n % 32 == 0) a.out_scales[(size_t)i * (N / 32) + n / 32] = scale;

@@ -8,15 +8,18 @@
 // are summed in fp32; the three left out are below 2^-24 of the whole.
 //
 // A tile of P and Q advances by 128 bytes of k a step through a ring in LDS, filled by direct loads.  The matrix
-// instruction's rows are Q's, so that a lane ends with 16 consecutive columns of one output row: row i of
-// fragment f is column 16 (i / 4) + 4 f + i % 4 of the wave's 64.
+// instruction's rows are Q's, so that a lane ends with four consecutive columns of one output row.
+#include <type_traits>
+
 #include "dense.h"
 
 namespace moe {
 
 typedef __bf16 pr_bf16x8 __attribute__((ext_vector_type(8)));
 typedef float pr_f32x4 __attribute__((ext_vector_type(4)));
+typedef float pr_f32x16 __attribute__((ext_vector_type(16)));
 typedef int pr_i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t pr_u32x4 __attribute__((ext_vector_type(4)));
 typedef short pr_i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t* pr_lds_t;
 
@@ -26,165 +29,294 @@ constexpr uint32_t kNowhere = 0x80000000u;   // past every descriptor's end: a l
 // planes of the six products of fp32 operands
 constexpr uint32_t kPlaneP = 0x021100u, kPlaneQ = 0x200110u;   // (0,0) (0,1) (1,1) (1,0) (2,0) (0,2), four bits each
 
-// one wave's 16 bytes per lane, lane l's to lds + 16 l
+// Direct loads to LDS: 16 (4) bytes per lane from base + off, lane l's to lds + 16 l (4 l); an offset past the descriptor's
+// end brings zeros.  In assembly, because the compiler has every transposing read of LDS wait for all direct loads that
+// it knows of; they have no result in registers, and are waited for by count (wait_vm).  (Nothing else here uses m0.)
+__device__ __forceinline__ pr_u32x4 load_rsrc(const uint8_t* base) {
+    const uint64_t p = (uint64_t)base;                       // the same in every lane
+    return pr_u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                    (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
+}
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint8_t* lds) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (dma_dst_t)lds, 16, off, 0, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
+                 "v"(off), "s"(load_rsrc(base)) : "memory");
 }
 __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t off, uint8_t* lds) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (dma_dst_t)lds, 4, off, 0, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
+                 "v"(off), "s"(load_rsrc(base)) : "memory");
 }
 
-// Place of a row's 16-byte chunk in LDS: chunk ^ key(row).  The sixteen rows that a fragment reads at once are
-// 0 .. 15 of P and 16 a + b (a, b < 4) of Q; two rows fill the 64 banks, so eight keys are needed.
-template <bool Q>
-__device__ __forceinline__ int row_key(int r) {
-    return Q ? ((r >> 1) & 1) | ((r >> 3) & 6) : (r >> 1) & 7;
-}
-// the same of a k-major tile: a read takes four rows k of 32 bytes (P), or of four 8-byte pieces 32 bytes apart (Q)
-template <bool Q>
-__device__ __forceinline__ int kmajor_key(int k) {
-    return Q ? (k & 1) | ((k << 2) & 8) : ((k & 3) << 1) | (k & 8);
-}
+// Place of a row's 16-byte chunk in LDS: chunk ^ key(row).  Eight lanes, on eight rows, are served at once, from 32 banks.
+__device__ __forceinline__ int row_key(int r) { return r & 7; }
+// the same of a k-major tile, where sixteen lanes read 32 bytes of each of four rows k
+__device__ __forceinline__ int kmajor_key(int k) { return ((k & 3) << 1) | (k & 8); }
 
-// One operand's tile of B rows: the lane's share of a step's loads.
-template <bool Q, bool KMAJOR, int B, int N, bool GATED>
-struct TileLoads {
-    uint32_t off[N];         // from the step's first byte; kNowhere outside the matrix
-    const uint8_t* base;
-    size_t step, upper;      // bytes from one step to the next; from the gate's rows to the up projection's
-    int left;                // bytes of a row (k-major: rows) from the step on
+// gated: of each 64 rows of Q's tile, the first 32 are the gate's of 32 columns of h, the others the up projection's
+__device__ __forceinline__ int gated_row(int r) { return (r & ~63) / 2 + (r & 31); }
 
-    // first: the tile's first row (gated: h column); rows: rows of the matrix; ld: its rows' bytes; K: length of the sum
-    __device__ __forceinline__ void init(const uint8_t* p, int first, int rows, int ld, int K, int esize, int wave, int lane) {
-        if constexpr (KMAJOR) {
-            constexpr int C = B / 8;                        // chunks of a k
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int unit = (wave * N + n) * 64 + lane, k = unit / C;
-                const int c = (unit % C) ^ kmajor_key<Q>(k);
-                off[n] = first + c * 8 < rows ? (uint32_t)(k * ld + c * 16) : kNowhere;
-            }
-            base = p + (size_t)first * 2;
-            step = (size_t)ld * 64;
-            left = K;
-        } else {
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int r = (wave * N + n) * 8 + (lane >> 3), c = (lane & 7) ^ row_key<Q>(r);
-                // gated: rows 16 q + 4 f + e of each 64 are columns 8 q + 4 (f % 2) + e of 32, f / 2 the half
-                const int row = GATED ? (r & ~63) / 2 + ((r >> 4) & 3) * 8 + (r & 7) : r;
-                off[n] = first + row < rows ? (uint32_t)(row * ld + c * 16) : kNowhere;
-            }
-            base = p + (size_t)first * ld;
-            step = kStepBytes;
-            left = K * esize;
-            upper = (size_t)rows * ld;
+// Where an operand's next step is: step s of a part of the sum is step s / pairs of k, in one plane.  Scalar state that is
+// moved on by a step at a time, since the products wait for what computes their loads' addresses.
+struct Walk {
+    const uint8_t *k, *at;   // the step of k in the first plane, and the plane's
+    size_t step, plane;
+    uint32_t planes;         // plane of each product, four bits each
+    int pairs, pair, unit, left, steps;
+
+    // rows: KMAJOR: rows left of the sum, else bytes left of a row; unit: of them a step; the steps [s, end) are walked
+    __device__ __forceinline__ void init(const uint8_t* p, size_t step_, int left_, int unit_, size_t plane_, uint32_t planes_,
+                                         int pairs_, int s, int end) {
+        step = step_;
+        plane = plane_;
+        planes = planes_;
+        pairs = pairs_;
+        unit = unit_;
+        int first = s;
+        pair = 0;
+        if (pairs > 1) {
+            first = s / 6;
+            pair = s - 6 * first;
         }
+        k = p + (size_t)first * step;
+        left = left_ - first * unit;
+        steps = end - s;
+        place();
     }
-    // step s of plane `plane` bytes on
-    __device__ __forceinline__ void load(int s, size_t plane, uint8_t* lds, int wave, int lane) const {
-        const uint8_t* b = base + (size_t)s * step + plane;
-        const int here = left - s * (KMAJOR ? 64 : kStepBytes);
-        const bool whole = here >= (KMAJOR ? 64 : kStepBytes);
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            uint32_t o = off[n];
-            if (!whole) {
-                int at;
-                if constexpr (KMAJOR) at = ((wave * N + n) * 64 + lane) / (B / 8);
-                else at = ((lane & 7) ^ row_key<Q>((wave * N + n) * 8 + (lane >> 3))) * 16;
-                if (at >= here) o = kNowhere;
-            }
-            // gated: eight rows are all the gate's (even n) or all the up projection's
-            load_lds16(GATED && (n & 1) ? b + upper : b, o, lds + (wave * N + n) * 1024);
+    __device__ __forceinline__ void place() { at = k + ((planes >> (4 * pair)) & 15) * plane; }
+    // units of the step that there are; none past the last step
+    __device__ __forceinline__ int here() const { return steps > 0 ? left : 0; }
+    __device__ __forceinline__ void next() {
+        --steps;
+        if (++pair >= pairs) {
+            pair = 0;
+            k += step;
+            left -= unit;
         }
+        place();
     }
 };
 
-// fragment f (P: rows 16 f .. of the wave's; Q: see above) of 32 k from 32 h on
-template <bool Q, bool KMAJOR, int B>
+// One operand's tile of B rows: the lane's share of a step's loads.
+template <bool KMAJOR, int B, int N, bool GATED>
+struct TileLoads {
+    uint32_t off[N];         // from the step's first byte; kNowhere outside the matrix
+    size_t upper;            // bytes from the gate's rows to the up projection's
+    Walk walk;
+
+    // first: the tile's first row (gated: h column); rows: rows of the matrix; ld: its rows' bytes; K: length of the sum;
+    // [s, end): the steps
+    __device__ __forceinline__ void init(const uint8_t* p, int first, int rows, int ld, int K, int esize, size_t plane,
+                                         uint32_t planes, int pairs, int s, int end, int wave, int lane) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if constexpr (KMAJOR) {
+                constexpr int C = B / 8;                    // chunks of a k
+                const int unit = (wave * N + n) * 64 + lane, k = unit / C;
+                const int c = (unit % C) ^ kmajor_key(k);
+                off[n] = first + c * 8 < rows ? (uint32_t)(k * ld + c * 16) : kNowhere;
+            } else {
+                const int r = (wave * N + n) * 8 + (lane >> 3), c = (lane & 7) ^ row_key(r);
+                const int row = GATED ? gated_row(r) : r;
+                off[n] = first + row < rows ? (uint32_t)(row * ld + c * 16) : kNowhere;
+            }
+        }
+        upper = (size_t)rows * ld;
+        if constexpr (KMAJOR) walk.init(p + (size_t)first * 2, (size_t)ld * 64, K, 64, plane, planes, pairs, s, end);
+        else walk.init(p + (size_t)first * ld, kStepBytes, K * esize, kStepBytes, plane, planes, pairs, s, end);
+    }
+    // load n of the walk's step; zeros past the end of the sum
+    __device__ __forceinline__ void load(int n, uint8_t* lds, int wave, int lane) const {
+        int at;
+        if constexpr (KMAJOR) at = ((wave * N + n) * 64 + lane) / (B / 8);
+        else at = ((lane & 7) ^ row_key((wave * N + n) * 8 + (lane >> 3))) * 16;
+        load_lds16(GATED && ((wave * N + n) & 4) ? walk.at + upper : walk.at, at < walk.here() ? off[n] : kNowhere,
+                   lds + (wave * N + n) * 1024);
+    }
+};
+
+// rows first + 16 f .. of 32 k from 32 h on
+template <bool KMAJOR, int B>
 __device__ __forceinline__ pr_bf16x8 fragment(const uint8_t* tile, int first, int f, int h, int lane) {
     const int i = lane & 15, g = lane >> 4;
     pr_bf16x8 r;
     if constexpr (KMAJOR) {
         const int k = 32 * h + 8 * g + (i >> 2);
-        const int m = first + (Q ? (i & 3) * 16 + f * 4 : f * 16 + (i & 3) * 4);
+        const int m = first + f * 16 + (i & 3) * 4;
         pr_i16x4 v[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int kk = k + 4 * e;
-            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<Q>(kk)) << 4) + (m & 4) * 2;
+            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key(kk)) << 4) + (m & 4) * 2;
             v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) pr_i16x4*)p);
         }
         __builtin_memcpy(&r, v, 16);
     } else {
-        const int row = first + (Q ? (i >> 2) * 16 + f * 4 + (i & 3) : f * 16 + i);
-        r = *(const pr_bf16x8*)(tile + row * kStepBytes + (((4 * h + g) ^ row_key<Q>(row)) << 4));
+        const int row = first + f * 16 + i;
+        r = *(const pr_bf16x8*)(tile + row * kStepBytes + (((4 * h + g) ^ row_key(row)) << 4));
     }
     return r;
 }
 // of 128 codes: lane group g holds k 16 g .. and 64 + 16 g ..
-template <bool Q>
 __device__ __forceinline__ pr_i32x8 fragment8(const uint8_t* tile, int first, int f, int lane) {
     const int i = lane & 15, g = lane >> 4;
-    const int row = first + (Q ? (i >> 2) * 16 + f * 4 + (i & 3) : f * 16 + i);
-    const uint4 a = *(const uint4*)(tile + row * kStepBytes + ((g ^ row_key<Q>(row)) << 4));
-    const uint4 b = *(const uint4*)(tile + row * kStepBytes + (((4 + g) ^ row_key<Q>(row)) << 4));
+    const int row = first + f * 16 + i;
+    const uint4 a = *(const uint4*)(tile + row * kStepBytes + ((g ^ row_key(row)) << 4));
+    const uint4 b = *(const uint4*)(tile + row * kStepBytes + (((4 + g) ^ row_key(row)) << 4));
     return pr_i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// The steps [first, end) of a workgroup's part of the sum
+struct Steps {
+    int first, end;
+    template <bool MX8>
+    __device__ __forceinline__ void init(const ProductArgs& a) {
+        const int total = (a.K + (MX8 ? 127 : 63)) / (MX8 ? 128 : 64) * a.pairs;
+        first = 0;
+        end = total;
+        if (a.splits > 1) {                                  // (K up to 2^20: 32 bits hold the products)
+            first = (int)((uint32_t)(blockIdx.y * total) / (uint32_t)a.splits);
+            end = (int)((uint32_t)((blockIdx.y + 1) * total) / (uint32_t)a.splits);
+        }
+    }
+};
+
+// One load of 64 rows' scale bytes of a step, the lane's row four of them
+struct ScaleLoads {
+    uint32_t off;
+    const uint8_t* at;
+    int steps;
+    // rows first + from + lane of a tile from `first` on (gated: rows from + lane of Q's tile)
+    template <bool GATED>
+    __device__ __forceinline__ void init(const uint8_t* scales, int first, int from, int rows, int K, const Steps& s, int lane) {
+        const int ld = K / 32, r = from + lane, row = GATED ? gated_row(r) : r;
+        off = first + row < rows ? (uint32_t)((row + (GATED && (r & 32) ? rows : 0)) * ld) : kNowhere;
+        at = scales + (size_t)first * ld + 4 * (size_t)s.first;
+        steps = s.end - s.first;
+    }
+    __device__ __forceinline__ void load(uint8_t* lds) const { load_lds4(at, steps > 0 ? off : kNowhere, lds); }
+    __device__ __forceinline__ void next() {
+        at += 4;
+        --steps;
+    }
+};
+
+// The lane's share of every load of a tile's step.
+template <bool MX8, bool PK, bool QK, int BI, int BJ, int W, bool GATED>
+struct StepLoads {
+    static constexpr int NP = BI / 8 / W, NQ = BJ / 8 / W, NS = MX8 ? (BI + BJ) / 64 / W : 0, PER = NP + NQ + NS;
+    static constexpr int PB = BI * kStepBytes, QB = BJ * kStepBytes, BYTES = PB + QB + (MX8 ? 4 * (BI + BJ) : 0);
+    static_assert(!MX8 || (BI % 64 == 0 && NS >= 1 && NS * 64 * W == BI + BJ), "whole loads of scales");
+    TileLoads<PK, BI, NP, false> p;
+    TileLoads<QK, BJ, NQ, GATED> q;
+    ScaleLoads sc[NS > 0 ? NS : 1];
+
+    __device__ __forceinline__ void init(const ProductArgs& a, const Steps& s, int i0, int j0, int wave, int lane) {
+        const int JH = GATED ? a.J / 2 : a.J;
+        p.init(a.p, i0, a.I, a.p_ld, a.K, MX8 ? 1 : 2, a.p_plane, kPlaneP, a.pairs, s.first, s.end, wave, lane);
+        q.init(a.q, j0, JH, a.q_ld, a.K, MX8 ? 1 : 2, a.q_plane, kPlaneQ, a.pairs, s.first, s.end, wave, lane);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            const int at = (wave * NS + n) * 64;
+            if (at < BI) sc[n].template init<false>(a.p_scales, i0, at, a.I, a.K, s, lane);
+            else sc[n].template init<GATED>(a.q_scales, j0, at - BI, JH, a.K, s, lane);
+        }
+    }
+    // the next step
+    __device__ __forceinline__ void load(uint8_t* st, int wave, int lane) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) p.load(n, st, wave, lane);
+        p.walk.next();
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) q.load(n, st + PB, wave, lane);
+        q.walk.next();
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            sc[n].load(st + PB + QB + (wave * NS + n) * 256);
+            sc[n].next();
+        }
+    }
+};
+
+// A wave's sums go through its own LDS, 256 bytes for each row of 64 columns, from where a lane takes eight columns of a
+// row, and a store 128 bytes of it.  The 16-byte chunks of a row are exchanged by the row's number, which keeps the writes,
+// many rows at once, on different banks.
+__device__ __forceinline__ pr_f32x4* sums_chunk(uint8_t* mine, int r, int c) {
+    return (pr_f32x4*)(mine + r * 256 + ((c ^ (r & 15)) << 4));
+}
+// ROWS rows from `row` on and 64 columns from `column` on (gated: 32 columns of h, the gate's and the up projection's)
+template <int ROWS, bool GATED>
+__device__ __forceinline__ void write_rows(const ProductArgs& a, uint8_t* mine, int row, int column, int lane) {
+    constexpr int PER_ROW = GATED ? 4 : 8;                   // lanes of a row
+    const int N = GATED ? a.J / 2 : a.J, c = lane % PER_ROW, n = column + 8 * c;
+    auto read8 = [&](int r, int c) {
+        const pr_f32x4 x = *sums_chunk(mine, r, c), y = *sums_chunk(mine, r, c + 1);
+        return f32x8{{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
+    };
+    asm volatile("" ::: "memory");                           // one wave's own writes and reads, in order
+    if (a.splits > 1) {
+#pragma unroll 2
+        for (int r = lane / PER_ROW; r < ROWS; r += 64 / PER_ROW) {
+            const int i = row + r;
+            if (i >= a.I || n >= N) continue;
+            float* sums = a.part + ((size_t)blockIdx.y * a.I + i) * a.J + n;
+            store_act8(sums, 0, read8(r, 2 * c));
+            if (GATED) store_act8(sums, (size_t)N, read8(r, 8 + 2 * c));
+        }
+    } else {
+        with_activation(a.activation, [&](auto f) {
+            constexpr int F = decltype(f)::value;
+#pragma unroll 2
+            for (int r = lane / PER_ROW; r < ROWS; r += 64 / PER_ROW) {
+                const int i = row + r;
+                const f32x8 v = read8(r, 2 * c);
+                if constexpr (GATED) gated_out8<F>(a, i, n, i < a.I && n < N, v, read8(r, 8 + 2 * c));
+                else if (i < a.I && n < N) product_out8<F>(a, i, n, v);
+            }
+        });
+    }
+    asm volatile("" ::: "memory");
+}
+
+// Workgroups go to the eight XCDs in turn: an XCD takes a run of tiles, in panels of eight tile rows, so that the tiles
+// it works on at once share their operands in its L2.
+__device__ __forceinline__ void tile_place(int b, int tiles, int ti, int tj, int* i, int* j) {
+    const int x = b & 7, per = tiles >> 3, more = tiles & 7;
+    const uint32_t t = x * per + (x < more ? x : more) + (b >> 3);
+    const int panel = t / (uint32_t)(8 * tj), r = t - panel * 8 * tj, rows = ti - panel * 8 < 8 ? ti - panel * 8 : 8;
+    *j = rows == 8 ? r >> 3 : (int)((uint32_t)r / (uint32_t)rows);
+    *i = panel * 8 + r - *j * rows;
+}
+
+// scale bytes of four fragments, rows first + 16 f .., for this lane's block
+__device__ __forceinline__ int four_scales(const uint8_t* scales, int first, int lane) {
+    const uint8_t* p = scales + 4 * (first + (lane & 15)) + (lane >> 4);
+    return p[0] | p[64] << 8 | p[128] << 16 | p[192] << 24;
+}
+// acc[f] += P's fragment FI times Q's fragment f, their scales in byte FI % 4 of ps and f of qs
+template <int FI>
+__device__ __forceinline__ void multiply_mx8(pr_f32x4 (&acc)[4], const pr_i32x8& p, const pr_i32x8 (&q)[4], int ps, int qs) {
+    acc[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[0], p, acc[0], 0, 0, 0, qs, FI % 4, ps);
+    acc[1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[1], p, acc[1], 0, 0, 1, qs, FI % 4, ps);
+    acc[2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[2], p, acc[2], 0, 0, 2, qs, FI % 4, ps);
+    acc[3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[3], p, acc[3], 0, 0, 3, qs, FI % 4, ps);
 }
 
 // Tile of BI rows and 64 WJ columns; WI x WJ waves, each BI / WI rows by 64 columns.  ST stages.
 template <bool MX8, bool PK, bool QK, int BI, int WI, int WJ, int ST, bool GATED>
 __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
-    constexpr int W = WI * WJ, BJ = 64 * WJ, FI = BI / WI / 16;
-    constexpr int NP = BI / 8 / W, NQ = BJ / 8 / W;
-    constexpr int PB = BI * kStepBytes, QB = BJ * kStepBytes, SB = MX8 ? W * 256 : 0, STG = PB + QB + SB;
-    static_assert(!GATED || NQ % 2 == 0, "even loads are the gate's");
-    static_assert(!MX8 || W * 64 >= BI + BJ, "one load brings a step's scales");
+    constexpr int W = WI * WJ, BJ = 64 * WJ, FI = BI / WI / 16, BH = GATED ? BJ / 2 : BJ;
+    typedef StepLoads<MX8, PK, QK, BI, BJ, W, GATED> Loads;
+    constexpr int STG = Loads::BYTES, PB = Loads::PB, PER = Loads::PER;
     __shared__ __align__(1024) uint8_t ring[ST * STG];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? BJ / 2 : BJ;
-    const int tj = (JH + BH - 1) / BH;
-    const int tile = blockIdx.x;
-    const int i0 = tile / tj * BI, j0 = tile % tj * BH;
-    TileLoads<false, PK, BI, NP, false> lp;
-    TileLoads<true, QK, BJ, NQ, GATED> lq;
-    lp.init(a.p, i0, a.I, a.p_ld, a.K, MX8 ? 1 : 2, wave, lane);
-    lq.init(a.q, j0, JH, a.q_ld, a.K, MX8 ? 1 : 2, wave, lane);
-    uint32_t soff = kNowhere;
-    const uint8_t* sbase = a.p_scales;
-    if constexpr (MX8) {
-        const int ld = a.K / 32, r = wave * 64 + lane;
-        if (wave * 64 < BI) {
-            if (i0 + r < a.I) soff = (uint32_t)(r * ld);
-            sbase = a.p_scales + (size_t)i0 * ld;
-        } else {
-            const int w = r - BI;
-            const int row = GATED ? (w & ~63) / 2 + ((w >> 4) & 3) * 8 + (w & 7) : w;
-            if (w < BJ && j0 + row < JH) soff = (uint32_t)((row + (GATED && (w & 8) ? JH : 0)) * ld);
-            sbase = a.q_scales + (size_t)j0 * ld;
-        }
-    }
-    const int ksteps = (a.K + (MX8 ? 127 : 63)) / (MX8 ? 128 : 64);
-    const int total = ksteps * a.pairs;
-    const int s0 = (int)((long long)blockIdx.y * total / a.splits), s1 = (int)((long long)(blockIdx.y + 1) * total / a.splits);
-    auto load = [&](int s) {
-        uint8_t* st = ring + (s - s0) % ST * STG;
-        int k = s;
-        size_t pp = 0, qp = 0;
-        if (a.pairs > 1) {
-            const int pair = s % 6;
-            k = s / 6;
-            pp = ((kPlaneP >> (4 * pair)) & 15) * a.p_plane;
-            qp = ((kPlaneQ >> (4 * pair)) & 15) * a.q_plane;
-        }
-        lp.load(k, pp, st, wave, lane);
-        lq.load(k, qp, st + PB, wave, lane);
-        if constexpr (MX8) load_lds4(sbase + 4 * (size_t)k, soff, st + PB + QB + wave * 256);
-    };
-    constexpr int PER = NP + NQ + (MX8 ? 1 : 0);
+    const int ti = (a.I + BI - 1) / BI, tj = ((GATED ? a.J / 2 : a.J) + BH - 1) / BH;
+    int i0, j0;
+    tile_place(blockIdx.x, gridDim.x, ti, tj, &i0, &j0);
+    i0 *= BI;
+    j0 *= BH;
+    Steps steps;
+    steps.init<MX8>(a);
+    Loads loads;
+    loads.init(a, steps, i0, j0, wave, lane);
     const int wi = wave / WJ * (BI / WI), wj = wave % WJ * 64;
     pr_f32x4 acc[FI][4];
 #pragma unroll
@@ -192,38 +324,36 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) acc[f][g] = pr_f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s)
-        if (s0 + s < s1) load(s0 + s);
-    for (int s = s0; s < s1; ++s) {
-        if (s + ST - 2 < s1) wait_vm<(ST - 2) * PER>();
-        else wait_vm<0>();
+    for (int s = 0; s < ST - 1; ++s) loads.load(ring + s * STG, wave, lane);
+    int at = 0;
+    for (int s = steps.first; s < steps.end; ++s) {
+        wait_vm<(ST - 2) * PER>();
         ring_barrier();
-        if (s + ST - 1 < s1) load(s + ST - 1);
-        const uint8_t* st = ring + (s - s0) % ST * STG;
+        loads.load(ring + (at == 0 ? ST - 1 : at - 1) * STG, wave, lane);
+        const uint8_t* st = ring + at * STG;
+        at = at + 1 == ST ? 0 : at + 1;
         if constexpr (MX8) {
-            pr_i32x8 q[4];
-            int qs[4];
+            pr_i32x8 p[FI], q[4];
+            int ps[FI / 4];
+            const int qs = four_scales(st + PB + Loads::QB + 4 * BI, wj, lane);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                q[f] = fragment8<true>(st + PB, wj, f, lane);
-                qs[f] = st[PB + QB + 4 * (BI + wj + ((lane & 15) >> 2) * 16 + f * 4 + (lane & 3)) + (lane >> 4)];
-            }
+            for (int f = 0; f < FI / 4; ++f) ps[f] = four_scales(st + PB + Loads::QB, wi + 64 * f, lane);
 #pragma unroll
-            for (int fi = 0; fi < FI; ++fi) {
-                const pr_i32x8 p = fragment8<false>(st, wi, fi, lane);
-                const int ps = st[PB + QB + 4 * (wi + fi * 16 + (lane & 15)) + (lane >> 4)];
+            for (int f = 0; f < 4; ++f) q[f] = fragment8(st + PB, wj, f, lane);
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    acc[fi][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(q[f], p, acc[fi][f], 0, 0, 0, qs[f], 0, ps);
-            }
+            for (int f = 0; f < FI; ++f) p[f] = fragment8(st, wi, f, lane);
+            for_steps<0>([&](auto n) {
+                constexpr int fi = decltype(n)::value;
+                multiply_mx8<fi>(acc[fi], p[fi], q, ps[fi / 4], qs);
+            }, std::make_integer_sequence<int, FI>{});
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 pr_bf16x8 q[4], p[FI];
 #pragma unroll
-                for (int f = 0; f < 4; ++f) q[f] = fragment<true, QK, BJ>(st + PB, wj, f, h, lane);
+                for (int f = 0; f < 4; ++f) q[f] = fragment<QK, BJ>(st + PB, wj, f, h, lane);
 #pragma unroll
-                for (int fi = 0; fi < FI; ++fi) p[fi] = fragment<false, PK, BI>(st, wi, fi, h, lane);
+                for (int fi = 0; fi < FI; ++fi) p[fi] = fragment<PK, BI>(st, wi, fi, h, lane);
 #pragma unroll
                 for (int fi = 0; fi < FI; ++fi)
 #pragma unroll
@@ -232,36 +362,234 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
             }
         }
     }
-    const int g = lane >> 4;
+    wait_vm<0>();                                            // no direct load is under way
+    ring_barrier();
+    static_assert(ST * STG >= W * FI * 4096, "the waves' sums fit into the ring");
+    uint8_t* mine = ring + wave * FI * 4096;
 #pragma unroll
-    for (int fi = 0; fi < FI; ++fi) {
+    for (int fi = 0; fi < FI; ++fi)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) mfma_results_here(acc[fi][f]);
-        const int i = i0 + wi + fi * 16 + (lane & 15);
-        f32x8 v[2];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e / 8].v[e % 8] = acc[fi][e / 4][e % 4];
-        if constexpr (GATED) {
-            const int n = j0 + wj / 2 + g * 8;
-            const bool valid = i < a.I && n < JH;
-            if (a.splits > 1) {
-                if (valid) {
-                    float* part = a.part + ((size_t)blockIdx.y * a.I + i) * a.J + n;
-                    store_act8(part, 0, v[0]);
-                    store_act8(part, (size_t)JH, v[1]);
-                }
-            } else {
-                gated_out8(a, i, n, valid, v[0], v[1], [](float m) { return max_xor32(max_xor16(m)); });
-            }
-        } else {
-            const int j = j0 + wj + g * 16;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (i >= a.I || j + 8 * c >= a.J) continue;
-                if (a.splits > 1) store_act8(a.part, ((size_t)blockIdx.y * a.I + i) * a.J + j + 8 * c, v[c]);
-                else product_out8(a, i, j + 8 * c, v[c]);
-            }
+        for (int f = 0; f < 4; ++f) {
+            mfma_results_here(acc[fi][f]);
+            *sums_chunk(mine, fi * 16 + (lane & 15), f * 4 + (lane >> 4)) = acc[fi][f];
         }
+    write_rows<FI * 16, GATED>(a, mine, i0 + wi, GATED ? j0 + wj / 2 : j0 + wj, lane);
+}
+
+// of 32 rows, first + 32 f ..: 16 k from 16 j on
+template <bool KMAJOR, int B>
+__device__ __forceinline__ pr_bf16x8 fragment32(const uint8_t* tile, int first, int f, int j, int lane) {
+    const int g = lane >> 5;
+    pr_bf16x8 r;
+    if constexpr (KMAJOR) {
+        const int i = lane & 15, k = 16 * j + 8 * g + (i >> 2), m = first + f * 32 + (lane & 16) + (i & 3) * 4;
+        pr_i16x4 v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int kk = k + 4 * e;
+            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key(kk)) << 4) + (m & 4) * 2;
+            v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) pr_i16x4*)p);
+        }
+        __builtin_memcpy(&r, v, 16);
+    } else {
+        const int row = first + f * 32 + (lane & 31);
+        r = *(const pr_bf16x8*)(tile + row * kStepBytes + (((2 * j + g) ^ row_key(row)) << 4));
+    }
+    return r;
+}
+
+// of 128 codes, 64 from 64 j on: lane group g holds k 16 g .. and 32 + 16 g ..
+__device__ __forceinline__ pr_i32x8 fragment8_32(const uint8_t* tile, int first, int f, int j, int lane) {
+    const int row = first + f * 32 + (lane & 31), g = lane >> 5;
+    const uint4 a = *(const uint4*)(tile + row * kStepBytes + (((4 * j + g) ^ row_key(row)) << 4));
+    const uint4 b = *(const uint4*)(tile + row * kStepBytes + (((4 * j + 2 + g) ^ row_key(row)) << 4));
+    return pr_i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+// the row's four scale bytes, moved so that bytes 0 and 2 are those of the lane group's blocks
+__device__ __forceinline__ int scales32(const uint8_t* scales, int first, int f, int lane) {
+    return (int)(*(const uint32_t*)(scales + 4 * (first + f * 32 + (lane & 31))) >> (8 * (lane >> 5)));
+}
+
+// Tile of 256 x 256 for large products: four waves of 128 x 128, each alone on its SIMD.  A step is four parts of 16 k (two
+// of 64 codes); while the matrix cores work on one, the next one's fragments come from LDS, and the direct loads are
+// handed out between the products (a burst of them would hold the products up).  One barrier a step, before its last
+// part: every wave has the whole step in registers then, and the next one has landed.  P has two places in LDS, whose
+// loads follow that barrier; Q three, and its loads a step more to land.  (With MXFP8 the scales leave room for two.)
+template <bool MX8, bool PK, bool QK, bool GATED>
+__global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
+    constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kStepBytes, QS = MX8 ? 2 : 3, PARTS = MX8 ? 2 : 4;
+    constexpr int QAT = 2 * TB, SAT = QAT + QS * TB, SB = MX8 ? 8 * B : 0;
+    __shared__ __align__(1024) uint8_t lds[SAT + 2 * SB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int JH = GATED ? a.J / 2 : a.J;
+    int i0, j0;
+    tile_place(blockIdx.x, gridDim.x, (a.I + B - 1) / B, (JH + BH - 1) / BH, &i0, &j0);
+    i0 *= B;
+    j0 *= BH;
+    Steps steps;
+    steps.init<MX8>(a);
+    TileLoads<PK, B, 8, false> lp;
+    TileLoads<QK, B, 8, GATED> lq;
+    ScaleLoads ls[2];
+    lp.init(a.p, i0, a.I, a.p_ld, a.K, MX8 ? 1 : 2, a.p_plane, kPlaneP, a.pairs, steps.first, steps.end, wave, lane);
+    lq.init(a.q, j0, JH, a.q_ld, a.K, MX8 ? 1 : 2, a.q_plane, kPlaneQ, a.pairs, steps.first, steps.end, wave, lane);
+    if constexpr (MX8) {
+        ls[0].init<false>(a.p_scales, i0, wave * 64, a.I, a.K, steps, lane);
+        ls[1].init<GATED>(a.q_scales, j0, wave * 64, JH, a.K, steps, lane);
+    }
+    const int wi = wave / 2 * 128, wj = wave % 2 * 128;
+    pr_f32x16 acc[4][4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[f][g][e] = 0.0f;
+    // the places where the next loads go, and of the step that is read
+    int p_to = 0, q_to = QAT, s_to = SAT, p_at = 0, q_at = QAT, s_at = SAT;
+    auto q_after = [](int q) { return q == QAT + (QS - 1) * TB ? QAT : q + TB; };
+    auto load_p = [&](int n) { lp.load(n, lds + p_to, wave, lane); };
+    auto load_q = [&](int n) { lq.load(n, lds + q_to, wave, lane); };
+    auto load_s = [&](int n) { ls[n].load(lds + s_to + n * 4 * B + wave * 256); };
+    auto p_next = [&] {
+        p_to ^= TB;
+        lp.walk.next();
+    };
+    auto q_next = [&] {
+        q_to = q_after(q_to);
+        lq.walk.next();
+    };
+    auto s_next = [&] {
+        s_to = s_to == SAT ? SAT + SB : SAT;
+        ls[0].next();
+        ls[1].next();
+    };
+    typename std::conditional<MX8, pr_i32x8, pr_bf16x8>::type p[2][4], q[2][4];
+    int ps[4], qs[4], ps_next[4], qs_next[4];
+    // fragment n of part j: Q's, then P's
+    auto read = [&](int j, int n) {
+        if constexpr (MX8) {
+            if (n < 4) q[j & 1][n] = fragment8_32(lds + q_at, wj, n, j, lane);
+            else p[j & 1][n - 4] = fragment8_32(lds + p_at, wi, n - 4, j, lane);
+        } else {
+            if (n < 4) q[j & 1][n] = fragment32<QK, B>(lds + q_at, wj, n, j, lane);
+            else p[j & 1][n - 4] = fragment32<PK, B>(lds + p_at, wi, n - 4, j, lane);
+        }
+    };
+    auto read_scales = [&](int f) {
+        ps_next[f] = scales32(lds + s_at, wi, f, lane);
+        qs_next[f] = scales32(lds + s_at + 4 * B, wj, f, lane);
+    };
+    auto multiply = [&](auto part, int n) {                  // products 2 n and 2 n + 1 of a part
+        constexpr int j = decltype(part)::value;
+#pragma unroll
+        for (int f = n % 2 * 2; f < n % 2 * 2 + 2; ++f) {
+            pr_f32x16& c = acc[n / 2][f];
+            if constexpr (MX8)
+                c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j & 1][f], p[j & 1][n / 2], c, 0, 0, 2 * j, qs[f], 2 * j, ps[n / 2]);
+            else c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j & 1][f], p[j & 1][n / 2], c, 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto take_scales = [&] {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            ps[f] = ps_next[f];
+            qs[f] = qs_next[f];
+        }
+    };
+    auto load_all = [&](bool with_p, bool with_q) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            if (with_p) load_p(n);
+            if (with_q) load_q(n);
+        }
+        if (with_p) p_next();
+        if (with_q) q_next();
+    };
+    load_all(true, true);
+    if constexpr (MX8) {
+        load_s(0);
+        load_s(1);
+        s_next();
+        load_all(true, true);
+        load_s(0);
+        load_s(1);
+        s_next();
+        wait_vm<18>();
+    } else {
+        load_all(false, true);
+        load_all(true, false);
+        wait_vm<16>();
+    }
+    ring_barrier();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) read(0, n);
+    if constexpr (MX8) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) read_scales(f);
+        take_scales();
+    }
+    for (int s = steps.first; s < steps.end; ++s) {
+        for_steps<0>([&](auto part) {
+            constexpr int j = decltype(part)::value;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                if (n < 4) {
+                    read(j + 1, 2 * n);
+                    read(j + 1, 2 * n + 1);
+                }
+                if (!MX8 && j == 0) load_q(n);
+                multiply(part, n);
+            }
+            if (!MX8 && j == 0) q_next();
+        }, std::make_integer_sequence<int, PARTS - 1>{});
+        wait_vm<MX8 ? 0 : 8>();
+        __builtin_amdgcn_sched_barrier(0);
+        ring_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        p_at ^= TB;
+        q_at = q_after(q_at);
+        s_at = s_at == SAT ? SAT + SB : SAT;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            if (n < 4) {
+                read(0, 2 * n);
+                read(0, 2 * n + 1);
+            }
+            load_p(n);
+            if constexpr (MX8) {
+                load_q(n);
+                if (n >= 4) read_scales(n - 4);
+                if (n >= 6) load_s(n - 6);
+            }
+            multiply(StepPos<PARTS - 1>{}, n);
+        }
+        p_next();
+        if constexpr (MX8) {
+            q_next();
+            s_next();
+            take_scales();
+        }
+    }
+    wait_vm<0>();                                            // no direct load is under way
+    ring_barrier();
+    uint8_t* mine = lds + wave * 32768;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int fi = 0; fi < 4; ++fi)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const pr_f32x16& v = acc[fi][2 * c + f];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const pr_f32x4 w = {v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+                    mfma_results_here(w);
+                    *sums_chunk(mine, fi * 32 + (lane & 31), f * 8 + 2 * e + (lane >> 5)) = w;
+                }
+            }
+        write_rows<128, GATED>(a, mine, i0 + wi, GATED ? j0 + wj / 2 + 32 * c : j0 + wj + 64 * c, lane);
     }
 }
 
@@ -282,12 +610,12 @@ __global__ __launch_bounds__(256) void k_product_finish(ProductArgs a) {
         }
         return v;
     };
-    if constexpr (GATED) {
+    with_activation(a.activation, [&](auto f) {
+        constexpr int F = decltype(f)::value;
         // (with 8-bit outputs N is a multiple of 32, so a block's four lanes are a quad)
-        gated_out8(a, i, n, valid, sum(n), sum(N + n), [](float m) { return quad_max(m); });
-    } else {
-        if (valid) product_out8(a, i, n, sum(n));
-    }
+        if constexpr (GATED) gated_out8<F>(a, i, n, valid, sum(n), sum(N + n));
+        else if (valid) product_out8<F>(a, i, n, sum(n));
+    });
 }
 
 constexpr size_t kPartBytes = (size_t)64 << 20;
@@ -297,9 +625,8 @@ size_t product_part_bytes(size_t I, size_t J) {
     return all < kPartBytes ? all : kPartBytes;
 }
 
-template <bool MX8, bool PK, bool QK, bool GATED>
-static void product_launch(ProductArgs& a, hipStream_t st) {
-    constexpr int BI = 128, WI = 2, WJ = 2;
+template <bool MX8, bool PK, bool QK, bool GATED, int BI, int WI, int WJ>
+static void product_launch_as(ProductArgs& a, hipStream_t st) {
     const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 32 * WJ : 64 * WJ;
     const int tiles = (a.I + BI - 1) / BI * ((JH + BH - 1) / BH);
     const int steps = (a.K + (MX8 ? 127 : 63)) / (MX8 ? 128 : 64) * a.pairs;
@@ -309,6 +636,17 @@ static void product_launch(ProductArgs& a, hipStream_t st) {
     while (splits > 1 && (size_t)splits * a.I * a.J * 4 > product_part_bytes(a.I, a.J)) --splits;
     a.splits = splits < 1 ? 1 : splits;
     MOE_LAUNCH((k_product<MX8, PK, QK, BI, WI, WJ, 2, GATED>), dim3(tiles, a.splits), dim3(64 * WI * WJ), 0, st, a);
+}
+
+template <bool MX8, bool PK, bool QK, bool GATED>
+static void product_launch(ProductArgs& a, hipStream_t st) {
+    const size_t tiles = ((size_t)a.I + 255) / 256 * (((size_t)a.J + 255) / 256);
+    if (tiles >= 192) {
+        a.splits = 1;
+        MOE_LAUNCH((k_product_large<MX8, PK, QK, GATED>), dim3((uint32_t)tiles), dim3(256), 0, st, a);
+        return;
+    }
+    product_launch_as<MX8, PK, QK, GATED, 128, 2, 2>(a, st);
 }
 
 hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st) {

@@ -174,6 +174,86 @@ def test_gated_backward(n, act):
         assert torch.equal(one[0], dx) and torch.equal(one[1], dw)
 
 
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_large_products(act):
+    """Many tiles each way, the last ones cut, and steps past the places that the operands have in LDS: the product and
+    both gradients."""
+    T, N, K = 3593, 3600, 3592
+    g = gen(500)
+    x, w, dy = rand(g, T, K, dtype=act), rand(g, N, K, dtype=act, std=0.02), rand(g, T, N, dtype=act)
+    d = dense(N, K, act, "silu")
+    bias, residual, pre, y = rand(g, N), rand(g, T, N, dtype=act), nan(T, N, dtype=act), nan(T, N, dtype=act)
+    m.moe_matmul(d, x, None, T, w, None, bias, residual, pre, y, scratch(d, T))
+    v, want = ref.matmul(x.double(), w.double(), kind(act), "silu", bias, residual)
+    check(pre, v, act, "pre")
+    check(y, want, act, "y")
+    dx, dw, db = nan(T, K, dtype=act), nan(N, K, dtype=act), nan(N)
+    m.moe_matmul_backward(d, x, T, w, pre, dy, dx, dw, db, scratch(d, T))
+    grad = ref.matmul_grad(dy, pre, "silu")
+    wx, ww = ref.backward(grad, x.double(), w.double(), kind(act))
+    check(dx, wx, act, "dx")
+    check(dw, ww, act, "dw")
+    check(db, ref.bias_grad(grad), F32, "d_bias")
+
+
+@pytest.mark.parametrize("K", [64, 72, 128, 200, 264])
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_large_products_of_few_steps(act, K):
+    """Sums of one to five steps, some cut, for each layout of the operands."""
+    g = gen(510)
+    T, N = 3600, 3664
+    x, w = rand(g, T, K, dtype=act), rand(g, N, K, dtype=act, std=0.1)
+    y = nan(T, N, dtype=act)
+    d = dense(N, K, act)
+    m.moe_matmul(d, x, None, T, w, None, None, None, None, y, scratch(d, T))
+    check(y, ref.matmul(x.double(), w.double(), kind(act), "none")[1], act, "y")
+    d = dense(K, N, act)                                     # dx sums over K rows, dw over K tokens
+    dy, w, dx = rand(g, T, K, dtype=act), rand(g, K, N, dtype=act, std=0.1), nan(T, N, dtype=act)
+    m.moe_matmul_backward(d, None, T, w, None, dy, dx, None, None, scratch(d, T))
+    check(dx, product_of(dy, w.t(), act), act, "dx")
+    d = dense(T, N, act)
+    dy, x, dw = rand(g, K, T, dtype=act), rand(g, K, N, dtype=act), nan(T, N, dtype=act)
+    m.moe_matmul_backward(d, x, K, None, None, dy, None, dw, None, scratch(d, K))
+    check(dw, product_of(dy.t(), x.t(), act), act, "dw")
+
+
+def product_of(a, b, act):
+    return ref.product(a.double(), b.double(), kind(act))
+
+
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_large_gated(act):
+    T, N, K = 3593, 1824, 456
+    g = gen(501)
+    x, w = rand(g, T, K, dtype=act), rand(g, 2 * N, K, dtype=act, std=0.1)
+    d = dense(N, K, act, "gelu")
+    pre, h = nan(T, 2 * N, dtype=act), nan(T, N, dtype=act)
+    m.moe_gated(d, x, None, T, w, None, pre, h, None, scratch(d, T))
+    v, want = ref.gated(x.double(), w.double(), kind(act), "gelu")
+    check(pre, v, act, "pre")
+    check(h, want, act, "h")
+    codes, scales = torch.full((T, N), 170, dtype=torch.uint8, device="cuda"), torch.zeros(T, N // 32, dtype=torch.uint8, device="cuda")
+    m.moe_gated(d, x, None, T, w, None, None, codes, scales, scratch(d, T))
+    ref.check_mx8(codes, scales, want, "h8")
+
+
+@pytest.mark.parametrize("K", [128, 256, 384, 1152])
+def test_large_mxfp8(K):
+    T, N = 3593, 3616
+    g = gen(502)
+    (x, xs), (w, ws) = mx8(g, T, K), mx8(g, N, K, std=0.1)
+    X, W = ref.values(x, xs), ref.values(w, ws)
+    d, y = dense(N, K, BF16, "sigmoid", True), nan(T, N, dtype=BF16)
+    m.moe_matmul(d, x, xs, T, w, ws, None, None, None, y, scratch(d, T))
+    check(y, ref.matmul(X, W, "mx8", "sigmoid")[1], BF16, "y")
+    half = N // 2
+    d, h, pre = dense(half, K, BF16, "silu", True), nan(T, half, dtype=BF16), nan(T, N, dtype=BF16)
+    m.moe_gated(d, x, xs, T, w, ws, pre, h, None, scratch(d, T))
+    v, want = ref.gated(X, W, "mx8", "silu")
+    check(pre, v, BF16, "pre")
+    check(h, want, BF16, "h")
+
+
 def test_gradients_against_differences():
     """The gradients of a sum of outputs, in fp32, along random directions: central differences of the calls themselves
     with step h are off by the curvature (h^2, with values of order one) and by the outputs' rounding over h."""
