@@ -402,12 +402,21 @@ static moe_status run_forward(const moe_dense* m, const void* x, const uint8_t* 
     const bool mx8 = m->operands == MOE_OPERANDS_MXFP8, f32 = m->act_dtype == MOE_DT_F32;
     const size_t K = m->cols;
     uint16_t *xp = (uint16_t*)(ws + L.xp), *wp = (uint16_t*)(ws + L.wp);
+    a.activation = m->activation;
+    const int bytes = mx8 ? 1 : f32 ? 4 : 2;
+    if (product_few_ok(a, bytes)) {
+        a.p = (const uint8_t*)x;
+        a.q = (const uint8_t*)w;
+        a.p_scales = x_scales;
+        a.q_scales = w_scales;
+        a.splits = 1;
+        return hip_status(launch_product_few(a, bytes, a.J != m->rows, st));
+    }
     a.p = f32 ? (const uint8_t*)xp : (const uint8_t*)x;
     a.q = f32 ? (const uint8_t*)wp : (const uint8_t*)w;
     a.p_ld = a.q_ld = (int)(mx8 && !f32 ? K : 2 * K);
     a.p_scales = x_scales;
     a.q_scales = w_scales;
-    a.activation = m->activation;
     a.part = (float*)(ws + L.part);
     if (f32 && mx8) {
         // the scaled matrix cores' sums are right to about 1.5e-5 of a result, bf16 ones to fp32

@@ -98,6 +98,8 @@ __device__ __forceinline__ float mx8_amax(const f32x8& v) {
     for (int e = 0; e < 8; ++e) m = fmaxf(m, __builtin_isfinite(v.v[e]) ? fabsf(v.v[e]) : __builtin_inff());
     return m;
 }
+// what a scale byte stands for
+__device__ __forceinline__ float mx8_scale(uint32_t b) { return b == 255 ? __builtin_nanf("") : ldexpf(1.0f, (int)b - 127); }
 // the largest of four neighbouring lanes, in each
 __device__ __forceinline__ float quad_max(float m) {
     m = fmaxf(m, __uint_as_float(dpp_u32<kDppXor1, 0xF>(__float_as_uint(m), __float_as_uint(m))));

@@ -132,6 +132,10 @@ size_t product_part_bytes(size_t I, size_t J);
 // the up projection's.  Chooses a.splits, given a.part with product_part_bytes(I, J) bytes.
 hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st);
 
+// Few rows of P, both operands as they are ([i][k], [j][k], `bytes` a value: 2 bf16, 4 fp32, 1 MXFP8)
+bool product_few_ok(const ProductArgs& a, int bytes);
+hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st);
+
 // fp32 [n] as three bf16 planes of n values, n a multiple of 8
 hipError_t launch_planes(const float* x, size_t n, uint16_t* planes, hipStream_t st);
 

@@ -11,44 +11,11 @@
 // instruction's rows are Q's, so that a lane ends with four consecutive columns of one output row.
 #include <type_traits>
 
-#include "dense.h"
+#include "dense_tile.h"
 
 namespace moe {
 
-typedef __bf16 pr_bf16x8 __attribute__((ext_vector_type(8)));
-typedef float pr_f32x4 __attribute__((ext_vector_type(4)));
-typedef float pr_f32x16 __attribute__((ext_vector_type(16)));
-typedef int pr_i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t pr_u32x4 __attribute__((ext_vector_type(4)));
-typedef short pr_i16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) uint8_t* pr_lds_t;
-
-constexpr int kStepBytes = 128;              // of a row and step: 64 bf16, 128 codes
-constexpr uint32_t kNowhere = 0x80000000u;   // past every descriptor's end: a load from there brings zeros
-
-// planes of the six products of fp32 operands
-constexpr uint32_t kPlaneP = 0x021100u, kPlaneQ = 0x200110u;   // (0,0) (0,1) (1,1) (1,0) (2,0) (0,2), four bits each
-
-// Direct loads to LDS: 16 (4) bytes per lane from base + off, lane l's to lds + 16 l (4 l); an offset past the descriptor's
-// end brings zeros.  In assembly, because the compiler has every transposing read of LDS wait for all direct loads that
-// it knows of; they have no result in registers, and are waited for by count (wait_vm).  (Nothing else here uses m0.)
-__device__ __forceinline__ pr_u32x4 load_rsrc(const uint8_t* base) {
-    const uint64_t p = (uint64_t)base;                       // the same in every lane
-    return pr_u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
-                    (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
-}
-__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint8_t* lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
-                 "v"(off), "s"(load_rsrc(base)) : "memory");
-}
-__device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t off, uint8_t* lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
-                 "v"(off), "s"(load_rsrc(base)) : "memory");
-}
-
-// Place of a row's 16-byte chunk in LDS: chunk ^ key(row).  Eight lanes, on eight rows, are served at once, from 32 banks.
-__device__ __forceinline__ int row_key(int r) { return r & 7; }
-// the same of a k-major tile, where sixteen lanes read 32 bytes of each of four rows k
+// Place of a k-major tile's 16-byte chunk, as row_key: sixteen lanes read 32 bytes of each of four rows k
 __device__ __forceinline__ int kmajor_key(int k) { return ((k & 3) << 1) | (k & 8); }
 
 // gated: of each 64 rows of Q's tile, the first 32 are the gate's of 32 columns of h, the others the up projection's
@@ -155,15 +122,6 @@ __device__ __forceinline__ pr_bf16x8 fragment(const uint8_t* tile, int first, in
     }
     return r;
 }
-// of 128 codes: lane group g holds k 16 g .. and 64 + 16 g ..
-__device__ __forceinline__ pr_i32x8 fragment8(const uint8_t* tile, int first, int f, int lane) {
-    const int i = lane & 15, g = lane >> 4;
-    const int row = first + f * 16 + i;
-    const uint4 a = *(const uint4*)(tile + row * kStepBytes + ((g ^ row_key(row)) << 4));
-    const uint4 b = *(const uint4*)(tile + row * kStepBytes + (((4 + g) ^ row_key(row)) << 4));
-    return pr_i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
-
 // The steps [first, end) of a workgroup's part of the sum
 struct Steps {
     int first, end;
@@ -202,9 +160,9 @@ struct ScaleLoads {
 // The lane's share of every load of a tile's step.
 template <bool MX8, bool PK, bool QK, int BI, int BJ, int W, bool GATED>
 struct StepLoads {
-    static constexpr int NP = BI / 8 / W, NQ = BJ / 8 / W, NS = MX8 ? (BI + BJ) / 64 / W : 0, PER = NP + NQ + NS;
-    static constexpr int PB = BI * kStepBytes, QB = BJ * kStepBytes, BYTES = PB + QB + (MX8 ? 4 * (BI + BJ) : 0);
-    static_assert(!MX8 || (BI % 64 == 0 && NS >= 1 && NS * 64 * W == BI + BJ), "whole loads of scales");
+    static constexpr int NP = BI / 8 / W, NQ = BJ / 8 / W, NS = MX8 ? ((BI + BJ) / 64 + W - 1) / W : 0, PER = NP + NQ + NS;
+    static constexpr int PB = BI * kStepBytes, QB = BJ * kStepBytes, BYTES = PB + QB + NS * W * 256;
+    static_assert(BI % 64 == 0, "whole loads of scales");
     TileLoads<PK, BI, NP, false> p;
     TileLoads<QK, BJ, NQ, GATED> q;
     ScaleLoads sc[NS > 0 ? NS : 1];
@@ -217,7 +175,7 @@ struct StepLoads {
         for (int n = 0; n < NS; ++n) {
             const int at = (wave * NS + n) * 64;
             if (at < BI) sc[n].template init<false>(a.p_scales, i0, at, a.I, a.K, s, lane);
-            else sc[n].template init<GATED>(a.q_scales, j0, at - BI, JH, a.K, s, lane);
+            else sc[n].template init<GATED>(a.q_scales, j0, at - BI, at < BI + BJ ? JH : 0, a.K, s, lane);
         }
     }
     // the next step
@@ -334,10 +292,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
         at = at + 1 == ST ? 0 : at + 1;
         if constexpr (MX8) {
             pr_i32x8 p[FI], q[4];
-            int ps[FI / 4];
+            int ps[(FI + 3) / 4];                            // (fewer fragments: the other bytes are not used)
             const int qs = four_scales(st + PB + Loads::QB + 4 * BI, wj, lane);
 #pragma unroll
-            for (int f = 0; f < FI / 4; ++f) ps[f] = four_scales(st + PB + Loads::QB, wi + 64 * f, lane);
+            for (int f = 0; f < (FI + 3) / 4; ++f) ps[f] = four_scales(st + PB + Loads::QB, wi + 64 * f, lane);
 #pragma unroll
             for (int f = 0; f < 4; ++f) q[f] = fragment8(st + PB, wj, f, lane);
 #pragma unroll
@@ -625,7 +583,7 @@ size_t product_part_bytes(size_t I, size_t J) {
     return all < kPartBytes ? all : kPartBytes;
 }
 
-template <bool MX8, bool PK, bool QK, bool GATED, int BI, int WI, int WJ>
+template <bool MX8, bool PK, bool QK, bool GATED, int BI, int WI, int WJ, int ST>
 static void product_launch_as(ProductArgs& a, hipStream_t st) {
     const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 32 * WJ : 64 * WJ;
     const int tiles = (a.I + BI - 1) / BI * ((JH + BH - 1) / BH);
@@ -635,7 +593,7 @@ static void product_launch_as(ProductArgs& a, hipStream_t st) {
     if (splits > kMostSplits) splits = kMostSplits;
     while (splits > 1 && (size_t)splits * a.I * a.J * 4 > product_part_bytes(a.I, a.J)) --splits;
     a.splits = splits < 1 ? 1 : splits;
-    MOE_LAUNCH((k_product<MX8, PK, QK, BI, WI, WJ, 2, GATED>), dim3(tiles, a.splits), dim3(64 * WI * WJ), 0, st, a);
+    MOE_LAUNCH((k_product<MX8, PK, QK, BI, WI, WJ, ST, GATED>), dim3(tiles, a.splits), dim3(64 * WI * WJ), 0, st, a);
 }
 
 template <bool MX8, bool PK, bool QK, bool GATED>
@@ -646,7 +604,13 @@ static void product_launch(ProductArgs& a, hipStream_t st) {
         MOE_LAUNCH((k_product_large<MX8, PK, QK, GATED>), dim3((uint32_t)tiles), dim3(256), 0, st, a);
         return;
     }
-    product_launch_as<MX8, PK, QK, GATED, 128, 2, 2>(a, st);
+    if constexpr (!PK && !QK) {
+        if (a.I <= 64) {
+            product_launch_as<MX8, PK, QK, GATED, 64, 4, 1, 4>(a, st);
+            return;
+        }
+    }
+    product_launch_as<MX8, PK, QK, GATED, 128, 2, 2, 2>(a, st);
 }
 
 hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st) {
@@ -721,8 +685,7 @@ __global__ __launch_bounds__(256) void k_unpack(const uint8_t* __restrict__ code
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= n) return;
     const uint2 c = *(const uint2*)(codes + i);
-    const int b = scales[i / 32];
-    const float sc = b == 255 ? __builtin_nanf("") : ldexpf(1.0f, b - 127);
+    const float sc = mx8_scale(scales[i / 32]);
     f32x8 v;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {

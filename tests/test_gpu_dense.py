@@ -53,10 +53,13 @@ def mx8(g, rows, cols, std=1.0):
     return codes, torch.randint(top - 3, top + 3, (rows, cols // 32), generator=g, device="cuda", dtype=torch.uint8)
 
 
+# few tokens: more tiles than workgroups, sums shorter than a wave's share and longer than its ring
+FEW = [(1, 4424, 328), (16, 4424, 72), (32, 8264, 136), (33, 4424, 264), (64, 4104, 1096), (7, 8288, 8), (20, 8288, 456), (48, 6144, 2056), (2, 72, 8200)]
+FEW8 = [(1, 8288, 128), (16, 4424, 640), (31, 8288, 1152), (33, 4424, 256), (64, 4104, 384), (48, 96, 8192)]
 # T, rows, cols: single values, sizes that end inside tiles and steps, several tiles each way, sums in parts
 SIZES = [(1, 8, 8), (2, 24, 40), (1, 4096, 1024), (3, 136, 64), (5, 40, 2056), (16, 64, 256), (17, 72, 200), (33, 264, 136), (64, 512, 1024),
          (100, 1000, 520), (128, 128, 128), (129, 384, 648), (257, 520, 1160), (300, 2048, 512), (1030, 328, 72),
-         (513, 96, 4104), (2049, 264, 264), (600, 2056, 328)]
+         (513, 96, 4104), (2049, 264, 264), (600, 2056, 328), *FEW]
 EPILOGUES = [("none", 0, 0, 0), ("silu", 1, 0, 1), ("gelu", 0, 1, 1), ("sigmoid", 1, 1, 0), ("none", 1, 1, 1)]
 
 
@@ -103,7 +106,7 @@ def test_gated(n, act):
             ref.check_mx8(codes, scales, want, f"h8 {fn}")
 
 
-SIZES8 = [(1, 8, 128), (3, 40, 256), (1, 4096, 1024), (16, 64, 4096), (17, 96, 384), (65, 1032, 128), (130, 256, 1152), (300, 512, 640), (1025, 520, 256), (512, 1056, 2048)]
+SIZES8 = [(1, 8, 128), (3, 40, 256), (1, 4096, 1024), (16, 64, 4096), (17, 96, 384), (65, 1032, 128), (130, 256, 1152), (300, 512, 640), (1025, 520, 256), (512, 1056, 2048), *FEW8]
 
 
 @pytest.mark.parametrize("act", [BF16, F32])
