@@ -16,7 +16,8 @@
 namespace moe {
 
 // Place of a k-major tile's 16-byte chunk, as row_key: sixteen lanes read 32 bytes of each of four rows k
-__device__ __forceinline__ int kmajor_key(int k) { return ((k & 3) << 1) | (k & 8); }
+template <int B>
+__device__ __forceinline__ int kmajor_key(int k) { return (((k & 3) << 1) | (k & 8)) & (B / 8 - 1); }
 
 // gated: of each 64 rows of Q's tile, the first 32 are the gate's of 32 columns of h, the others the up projection's
 __device__ __forceinline__ int gated_row(int r) { return (r & ~63) / 2 + (r & 31); }
@@ -78,7 +79,7 @@ struct TileLoads {
             if constexpr (KMAJOR) {
                 constexpr int C = B / 8;                    // chunks of a k
                 const int unit = (wave * N + n) * 64 + lane, k = unit / C;
-                const int c = (unit % C) ^ kmajor_key(k);
+                const int c = (unit % C) ^ kmajor_key<B>(k);
                 off[n] = first + c * 8 < rows ? (uint32_t)(k * ld + c * 16) : kNowhere;
             } else {
                 const int r = (wave * N + n) * 8 + (lane >> 3), c = (lane & 7) ^ row_key(r);
@@ -112,7 +113,7 @@ __device__ __forceinline__ pr_bf16x8 fragment(const uint8_t* tile, int first, in
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int kk = k + 4 * e;
-            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key(kk)) << 4) + (m & 4) * 2;
+            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<B>(kk)) << 4) + (m & 4) * 2;
             v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) pr_i16x4*)p);
         }
         __builtin_memcpy(&r, v, 16);
@@ -345,7 +346,7 @@ __device__ __forceinline__ pr_bf16x8 fragment32(const uint8_t* tile, int first, 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int kk = k + 4 * e;
-            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key(kk)) << 4) + (m & 4) * 2;
+            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<B>(kk)) << 4) + (m & 4) * 2;
             v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) pr_i16x4*)p);
         }
         __builtin_memcpy(&r, v, 16);
@@ -583,34 +584,60 @@ size_t product_part_bytes(size_t I, size_t J) {
     return all < kPartBytes ? all : kPartBytes;
 }
 
+// Which tile, and how many parts of the sum: the least time by a model of each tile's own measurements.  A workgroup takes
+// `start` and `step` for each 128 bytes of k, `step2` where two share a CU; parts cost a second kernel, that adds them.
+// us, model and measured (bf16): 256 tokens, 4096 x 4096 64 x 128 in two parts 21, 21.6 (128 x 256 26); 1024 tokens 64 x 128
+// 42, 42.0 (128 x 256 48); 2048 tokens 128 x 256 64, 64.1 (64 x 128 80); 4096 tokens 256 x 256 106, 110 (128 x 256 125);
+// 512 tokens, 1024 x 1024 64 x 64 9.4, 9.3 (64 x 128 9.8).
+struct TileChoice {
+    int bi, bj, per_cu;
+    float start, step, step2;
+};
+static const TileChoice kTiles[] = {
+    {64, 64, 2, 5.4f, 0.25f, 0.42f}, {64, 128, 2, 5.7f, 0.32f, 0.57f}, {128, 256, 1, 5.2f, 0.92f, 0.92f}, {256, 256, 1, 6.2f, 1.55f, 1.55f}};
+
+static int choose_tile(ProductArgs& a, bool mx8) {
+    const int steps = (a.K + (mx8 ? 127 : 63)) / (mx8 ? 128 : 64) * a.pairs;
+    float least = 0.0f;
+    int best = -1;
+    for (int t = 0; t < 4; ++t) {
+        const TileChoice& c = kTiles[t];
+        const long long tiles = (long long)((a.I + c.bi - 1) / c.bi) * ((a.J + c.bj - 1) / c.bj);
+        for (int splits = 1; splits <= kMostSplits; ++splits) {
+            const size_t part = (size_t)splits * a.I * a.J * 4;
+            if (splits > 1 && (splits * 4 > steps || part > product_part_bytes(a.I, a.J) || tiles * splits > 256 * c.per_cu)) break;
+            const long long groups = tiles * splits, rounds = (groups + 256 * c.per_cu - 1) / (256 * c.per_cu);
+            // (a step of 128 codes takes a third longer than one of 64 bf16)
+            const float step = (groups <= 256 ? c.step : c.step2) * (mx8 ? 1.35f : 1.0f);
+            float us = rounds * (steps / (float)splits) * step + c.start * (rounds < 2 ? 1.0f : 0.5f + 0.5f * rounds);
+            if (splits > 1) us += 4.0f + part * 1.5e-7f;
+            if (best < 0 || us < least) {
+                least = us;
+                best = t;
+                a.splits = splits;
+            }
+        }
+    }
+    return best;
+}
+
 template <bool MX8, bool PK, bool QK, bool GATED, int BI, int WI, int WJ, int ST>
-static void product_launch_as(ProductArgs& a, hipStream_t st) {
-    const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 32 * WJ : 64 * WJ;
-    const int tiles = (a.I + BI - 1) / BI * ((JH + BH - 1) / BH);
-    const int steps = (a.K + (MX8 ? 127 : 63)) / (MX8 ? 128 : 64) * a.pairs;
-    int splits = 512 / tiles;
-    if (splits > steps / 4) splits = steps / 4;
-    if (splits > kMostSplits) splits = kMostSplits;
-    while (splits > 1 && (size_t)splits * a.I * a.J * 4 > product_part_bytes(a.I, a.J)) --splits;
-    a.splits = splits < 1 ? 1 : splits;
+static void product_launch_as(const ProductArgs& a, hipStream_t st) {
+    const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 32 * WJ : 64 * WJ, tiles = (a.I + BI - 1) / BI * ((JH + BH - 1) / BH);
     MOE_LAUNCH((k_product<MX8, PK, QK, BI, WI, WJ, ST, GATED>), dim3(tiles, a.splits), dim3(64 * WI * WJ), 0, st, a);
 }
 
 template <bool MX8, bool PK, bool QK, bool GATED>
 static void product_launch(ProductArgs& a, hipStream_t st) {
-    const size_t tiles = ((size_t)a.I + 255) / 256 * (((size_t)a.J + 255) / 256);
-    if (tiles >= 192) {
-        a.splits = 1;
-        MOE_LAUNCH((k_product_large<MX8, PK, QK, GATED>), dim3((uint32_t)tiles), dim3(256), 0, st, a);
-        return;
-    }
-    if constexpr (!PK && !QK) {
-        if (a.I <= 64) {
-            product_launch_as<MX8, PK, QK, GATED, 64, 4, 1, 4>(a, st);
-            return;
+    switch (choose_tile(a, MX8)) {
+        case 0: product_launch_as<MX8, PK, QK, GATED, 64, 4, 1, 4>(a, st); break;
+        case 1: product_launch_as<MX8, PK, QK, GATED, 64, 2, 2, 3>(a, st); break;
+        case 2: product_launch_as<MX8, PK, QK, GATED, 128, 2, 4, 3>(a, st); break;
+        default: {
+            const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 128 : 256, tiles = (a.I + 255) / 256 * ((JH + BH - 1) / BH);
+            MOE_LAUNCH((k_product_large<MX8, PK, QK, GATED>), dim3(tiles, a.splits), dim3(256), 0, st, a);
         }
     }
-    product_launch_as<MX8, PK, QK, GATED, 128, 2, 2, 2>(a, st);
 }
 
 hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st) {
