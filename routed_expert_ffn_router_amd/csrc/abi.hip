@@ -364,14 +364,13 @@ struct DenseLayout {
     size_t d, xp, wp, bias, part, total;
 };
 static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool backward) {
-    // bytes per value of the operands' bf16 copies, where there are any: three planes of fp32 values; MXFP8 values for
-    // fp32 outputs
-    const size_t copies = m->act_dtype != MOE_DT_F32 ? 0 : m->operands == MOE_OPERANDS_ACT ? 6 : 2;
+    // MXFP8 operands of fp32 outputs are copied to bf16
+    const size_t copies = m->act_dtype == MOE_DT_F32 && m->operands == MOE_OPERANDS_MXFP8 ? 2 : 0;
     const size_t K = m->cols, t = T;
     DenseLayout L;
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o += align256(bytes); return at; };
-    L.d = take(backward ? t * R * (copies ? copies : 2) : 0);
+    L.d = take(backward ? t * R * (m->act_dtype == MOE_DT_F32 ? 4 : 2) : 0);
     L.xp = take(t * K * copies);
     L.wp = take(R * K * copies);
     L.bias = take(backward ? (size_t)kBiasChunks * m->rows * 4 : 0);
@@ -388,82 +387,61 @@ static ProductArgs product_args(const moe_dense* m, int I, int J, int K, void* o
     a.I = I;
     a.J = J;
     a.K = K;
-    a.pairs = 1;
     a.activation = MOE_ACT_NONE;
     a.out_f32 = m->act_dtype == MOE_DT_F32;
     a.out = out;
     return a;
 }
 
-// the forward product of R weight rows: operands, planes of fp32 ones, and the launch
+// the forward product of R weight rows
 static moe_status run_forward(const moe_dense* m, const void* x, const uint8_t* x_scales, int32_t T, const void* w,
                               const uint8_t* w_scales, size_t R, ProductArgs a, uint8_t* ws, const DenseLayout& L,
                               hipStream_t st) {
     const bool mx8 = m->operands == MOE_OPERANDS_MXFP8, f32 = m->act_dtype == MOE_DT_F32;
     const size_t K = m->cols;
-    uint16_t *xp = (uint16_t*)(ws + L.xp), *wp = (uint16_t*)(ws + L.wp);
+    const bool gated = a.J != m->rows;
+    int bytes = mx8 ? 1 : f32 ? 4 : 2;
     a.activation = m->activation;
-    const int bytes = mx8 ? 1 : f32 ? 4 : 2;
-    if (product_few_ok(a, bytes)) {
-        a.p = (const uint8_t*)x;
-        a.q = (const uint8_t*)w;
-        a.p_scales = x_scales;
-        a.q_scales = w_scales;
-        a.splits = 1;
-        return hip_status(launch_product_few(a, bytes, a.J != m->rows, st));
-    }
-    a.p = f32 ? (const uint8_t*)xp : (const uint8_t*)x;
-    a.q = f32 ? (const uint8_t*)wp : (const uint8_t*)w;
-    a.p_ld = a.q_ld = (int)(mx8 && !f32 ? K : 2 * K);
+    a.p = (const uint8_t*)x;
+    a.q = (const uint8_t*)w;
     a.p_scales = x_scales;
     a.q_scales = w_scales;
     a.part = (float*)(ws + L.part);
+    a.splits = 1;
+    if (product_few_ok(a, bytes)) return hip_status(launch_product_few(a, bytes, gated, st));
     if (f32 && mx8) {
         // the scaled matrix cores' sums are right to about 1.5e-5 of a result, bf16 ones to fp32
+        uint16_t *xp = (uint16_t*)(ws + L.xp), *wp = (uint16_t*)(ws + L.wp);
         MOE_HIP(launch_unpack((const uint8_t*)x, x_scales, T * K, xp, st));
         MOE_HIP(launch_unpack((const uint8_t*)w, w_scales, R * K, wp, st));
-    } else if (f32) {
-        MOE_HIP(launch_planes((const float*)x, T * K, xp, st));
-        MOE_HIP(launch_planes((const float*)w, R * K, wp, st));
-        a.p_plane = T * K * 2;
-        a.q_plane = R * K * 2;
-        a.pairs = 6;
+        a.p = (const uint8_t*)xp;
+        a.q = (const uint8_t*)wp;
+        bytes = 2;
     }
-    return hip_status(launch_product(a, mx8 && !f32, false, false, a.J != m->rows, st));
+    a.p_ld = a.q_ld = (int)(K * bytes);
+    return hip_status(launch_product(a, bytes, false, false, gated, st));
 }
 
 // dx = d W and dw = d^T x, d ([T][R]) being the pre-activations' gradient
 static moe_status run_backward(const moe_dense* m, const void* x, int32_t T, const void* w, size_t R, const void* d,
                                void* dx, void* dw, uint8_t* ws, const DenseLayout& L, hipStream_t st) {
-    const bool f32 = m->act_dtype == MOE_DT_F32;
+    const int bytes = m->act_dtype == MOE_DT_F32 ? 4 : 2;
     const size_t K = m->cols;
     ProductArgs a = product_args(m, T, (int)K, (int)R, dx);
     a.part = (float*)(ws + L.part);
-    a.pairs = f32 ? 6 : 1;
     a.p = (const uint8_t*)d;
-    a.p_plane = T * R * 2;
-    a.p_ld = (int)(2 * R);
-    a.q_ld = (int)(2 * K);
+    a.p_ld = (int)(bytes * R);
+    a.q_ld = (int)(bytes * K);
     if (dx) {
         a.q = (const uint8_t*)w;
-        if (f32) {
-            MOE_HIP(launch_planes((const float*)w, R * K, (uint16_t*)(ws + L.wp), st));
-            a.q = ws + L.wp;
-            a.q_plane = R * K * 2;
-        }
-        MOE_HIP(launch_product(a, false, false, true, false, st));
+        MOE_HIP(launch_product(a, bytes, false, true, false, st));
     }
     if (dw) {
         a.I = (int)R;
         a.K = T;
         a.out = dw;
         a.q = (const uint8_t*)x;
-        if (f32) {
-            MOE_HIP(launch_planes((const float*)x, T * K, (uint16_t*)(ws + L.xp), st));
-            a.q = ws + L.xp;
-            a.q_plane = T * K * 2;
-        }
-        MOE_HIP(launch_product(a, false, true, true, false, st));
+        MOE_HIP(launch_product(a, bytes, true, true, false, st));
     }
     return MOE_OK;
 }
@@ -840,7 +818,7 @@ static moe_status dense_backward(const moe_dense* m, const void* x, int32_t T, c
     const DenseLayout L = dense_layout(m, T, R, true);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     uint8_t* w8 = (uint8_t*)ws;
-    const bool as_is = !wants_pre && !f32;       // dy itself is the pre-activations' gradient
+    const bool as_is = !wants_pre;               // dy itself is the pre-activations' gradient
     PreGradArgs g;
     memset(&g, 0, sizeof g);
     g.T = T;
@@ -849,7 +827,7 @@ static moe_status dense_backward(const moe_dense* m, const void* x, int32_t T, c
     g.gated = gated;
     g.dy = dy;
     g.pre = pre;
-    g.d = as_is || (!dx && !dw) ? nullptr : (uint16_t*)(w8 + L.d);
+    g.d = as_is || (!dx && !dw) ? nullptr : w8 + L.d;
     g.bias_part = d_bias ? (float*)(w8 + L.bias) : nullptr;
     g.d_bias = d_bias;
     if (g.d || d_bias) MOE_HIP(launch_pre_grad(g, f32, stream));

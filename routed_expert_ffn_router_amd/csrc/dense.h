@@ -6,16 +6,13 @@
 
 namespace moe {
 
-// One product out[i][j] = sum_k P[i][k] Q[j][k], i < I, j < J, with its epilogue.  P and Q are bf16, MXFP8
-// codes, or the three bf16 planes of an fp32 operand; each is stored with k along its rows ([i][k]) or,
-// "k-major", across them ([k][i]).
+// One product out[i][j] = sum_k P[i][k] Q[j][k], i < I, j < J, with its epilogue.  P and Q are bf16, fp32 or MXFP8
+// codes; each is stored with k along its rows ([i][k]) or, "k-major", across them ([k][i]).
 struct ProductArgs {
     int I, J, K;
     const uint8_t *p, *q;
-    size_t p_plane, q_plane;      // bytes from one plane of an fp32 operand to the next
     int p_ld, q_ld;               // bytes of a stored row
     const uint8_t *p_scales, *q_scales;   // MXFP8: [i][K/32], [j][K/32]
-    int pairs;                    // products of planes: 1, or 6 for fp32 operands
     int splits;                   // parts of the sum over k; more than one: fp32 sums to part, [splits][I][J]
     float* part;
     // epilogue; the outputs' rows are J long (gated: N = J / 2)
@@ -128,16 +125,13 @@ __device__ __forceinline__ void gated_out8(const ProductArgs& a, int i, int n, b
 // ---------------------------------------------------------------------------------------------
 // bytes for the partial sums of any product of up to I rows and J columns
 size_t product_part_bytes(size_t I, size_t J);
-// mx8: MXFP8 operands; p_kmajor, q_kmajor: stored [k][i], [k][j] (bf16 only); gated: Q holds the gate's rows, then
-// the up projection's.  Chooses a.splits, given a.part with product_part_bytes(I, J) bytes.
-hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st);
+// bytes: of an operand's value (2 bf16, 4 fp32, 1 MXFP8); p_kmajor, q_kmajor: stored [k][i], [k][j] (not MXFP8); gated: Q
+// holds the gate's rows, then the up projection's.  Chooses a.splits, given a.part with product_part_bytes(I, J) bytes.
+hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st);
 
-// Few rows of P, both operands as they are ([i][k], [j][k], `bytes` a value: 2 bf16, 4 fp32, 1 MXFP8)
+// Few rows of P, neither operand k-major
 bool product_few_ok(const ProductArgs& a, int bytes);
 hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st);
-
-// fp32 [n] as three bf16 planes of n values, n a multiple of 8
-hipError_t launch_planes(const float* x, size_t n, uint16_t* planes, hipStream_t st);
 
 // MXFP8 [n] as bf16, which holds every code times its scale
 hipError_t launch_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, uint16_t* values, hipStream_t st);
@@ -147,7 +141,7 @@ struct PreGradArgs {
     int T, N;                     // gated: pre and d are [T][2 N]
     int activation, gated;
     const void *dy, *pre;
-    uint16_t* d;                  // the pre-activations' gradient in bf16, or three planes for fp32; or null
+    void* d;                      // the pre-activations' gradient in bf16 or fp32; or null
     float* bias_part;             // or null: [chunks][N]
     float* d_bias;
 };

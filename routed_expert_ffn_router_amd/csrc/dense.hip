@@ -4,8 +4,8 @@
 //   multiplied), which serves the forward products (P the tokens, Q the weight), the input's gradient (Q the weight
 //   stored k-major) and the weight's gradient (both stored k-major: k runs over the tokens).
 //
-// fp32 operands are split into three bf16 planes first (8 + 8 + 8 bits of mantissa), and six products of planes
-// are summed in fp32; the three left out are below 2^-24 of the whole.
+// An fp32 value becomes three bf16 terms on its way from LDS to the matrix cores (8 + 8 + 8 bits of mantissa), and six
+// products of terms are summed in fp32; the three left out are below 2^-24 of the whole.
 //
 // A tile of P and Q advances by 128 bytes of k a step through a ring in LDS, filled by direct loads.  The matrix
 // instruction's rows are Q's, so that a lane ends with four consecutive columns of one output row.
@@ -15,72 +15,57 @@
 
 namespace moe {
 
-// Place of a k-major tile's 16-byte chunk, as row_key: sixteen lanes read 32 bytes of each of four rows k
-template <int B>
-__device__ __forceinline__ int kmajor_key(int k) { return (((k & 3) << 1) | (k & 8)) & (B / 8 - 1); }
+// Place of a k-major tile's 16-byte chunk, as row_key: sixteen lanes read 32 bytes of each of four rows k; of fp32, 64 bytes
+// of each of two
+template <int FMT, int B>
+__device__ __forceinline__ int kmajor_key(int k) {
+    return FMT == kF32 ? (k >> 1) & 4 : (((k & 3) << 1) | (k & 8)) & (B / 8 - 1);
+}
 
 // gated: of each 64 rows of Q's tile, the first 32 are the gate's of 32 columns of h, the others the up projection's
 __device__ __forceinline__ int gated_row(int r) { return (r & ~63) / 2 + (r & 31); }
 
-// Where an operand's next step is: step s of a part of the sum is step s / pairs of k, in one plane.  Scalar state that is
-// moved on by a step at a time, since the products wait for what computes their loads' addresses.
+// Where an operand's next step is.  Scalar state that is moved on by a step at a time, since the products wait for what
+// computes their loads' addresses.
 struct Walk {
-    const uint8_t *k, *at;   // the step of k in the first plane, and the plane's
-    size_t step, plane;
-    uint32_t planes;         // plane of each product, four bits each
-    int pairs, pair, unit, left, steps;
+    const uint8_t* at;
+    size_t step;
+    int unit, left, steps;   // units (bytes of a row; k-major: rows) of a step, and left of the sum
 
-    // rows: KMAJOR: rows left of the sum, else bytes left of a row; unit: of them a step; the steps [s, end) are walked
-    __device__ __forceinline__ void init(const uint8_t* p, size_t step_, int left_, int unit_, size_t plane_, uint32_t planes_,
-                                         int pairs_, int s, int end) {
+    // the steps [s, end) are walked
+    __device__ __forceinline__ void init(const uint8_t* p, size_t step_, int left_, int unit_, int s, int end) {
         step = step_;
-        plane = plane_;
-        planes = planes_;
-        pairs = pairs_;
         unit = unit_;
-        int first = s;
-        pair = 0;
-        if (pairs > 1) {
-            first = s / 6;
-            pair = s - 6 * first;
-        }
-        k = p + (size_t)first * step;
-        left = left_ - first * unit;
+        at = p + (size_t)s * step;
+        left = left_ - s * unit;
         steps = end - s;
-        place();
     }
-    __device__ __forceinline__ void place() { at = k + ((planes >> (4 * pair)) & 15) * plane; }
     // units of the step that there are; none past the last step
     __device__ __forceinline__ int here() const { return steps > 0 ? left : 0; }
     __device__ __forceinline__ void next() {
         --steps;
-        if (++pair >= pairs) {
-            pair = 0;
-            k += step;
-            left -= unit;
-        }
-        place();
+        at += step;
+        left -= unit;
     }
 };
 
 // One operand's tile of B rows: the lane's share of a step's loads.
-template <bool KMAJOR, int B, int N, bool GATED>
+template <int FMT, bool KMAJOR, int B, int N, bool GATED>
 struct TileLoads {
+    static constexpr int ES = kSize<FMT>, C = B * ES / 16;  // chunks of a row k of a k-major tile
     uint32_t off[N];         // from the step's first byte; kNowhere outside the matrix
     size_t upper;            // bytes from the gate's rows to the up projection's
     Walk walk;
 
     // first: the tile's first row (gated: h column); rows: rows of the matrix; ld: its rows' bytes; K: length of the sum;
     // [s, end): the steps
-    __device__ __forceinline__ void init(const uint8_t* p, int first, int rows, int ld, int K, int esize, size_t plane,
-                                         uint32_t planes, int pairs, int s, int end, int wave, int lane) {
+    __device__ __forceinline__ void init(const uint8_t* p, int first, int rows, int ld, int K, int s, int end, int wave, int lane) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             if constexpr (KMAJOR) {
-                constexpr int C = B / 8;                    // chunks of a k
                 const int unit = (wave * N + n) * 64 + lane, k = unit / C;
-                const int c = (unit % C) ^ kmajor_key<B>(k);
-                off[n] = first + c * 8 < rows ? (uint32_t)(k * ld + c * 16) : kNowhere;
+                const int c = (unit % C) ^ kmajor_key<FMT, B>(k);
+                off[n] = first + c * (16 / ES) < rows ? (uint32_t)(k * ld + c * 16) : kNowhere;
             } else {
                 const int r = (wave * N + n) * 8 + (lane >> 3), c = (lane & 7) ^ row_key(r);
                 const int row = GATED ? gated_row(r) : r;
@@ -88,13 +73,13 @@ struct TileLoads {
             }
         }
         upper = (size_t)rows * ld;
-        if constexpr (KMAJOR) walk.init(p + (size_t)first * 2, (size_t)ld * 64, K, 64, plane, planes, pairs, s, end);
-        else walk.init(p + (size_t)first * ld, kStepBytes, K * esize, kStepBytes, plane, planes, pairs, s, end);
+        if constexpr (KMAJOR) walk.init(p + (size_t)first * ES, (size_t)ld * kStep<FMT>, K, kStep<FMT>, s, end);
+        else walk.init(p + (size_t)first * ld, kStepBytes, K * ES, kStepBytes, s, end);
     }
     // load n of the walk's step; zeros past the end of the sum
     __device__ __forceinline__ void load(int n, uint8_t* lds, int wave, int lane) const {
         int at;
-        if constexpr (KMAJOR) at = ((wave * N + n) * 64 + lane) / (B / 8);
+        if constexpr (KMAJOR) at = ((wave * N + n) * 64 + lane) / C;
         else at = ((lane & 7) ^ row_key((wave * N + n) * 8 + (lane >> 3))) * 16;
         load_lds16(GATED && ((wave * N + n) & 4) ? walk.at + upper : walk.at, at < walk.here() ? off[n] : kNowhere,
                    lds + (wave * N + n) * 1024);
@@ -113,7 +98,7 @@ __device__ __forceinline__ pr_bf16x8 fragment(const uint8_t* tile, int first, in
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int kk = k + 4 * e;
-            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<B>(kk)) << 4) + (m & 4) * 2;
+            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<kBf16, B>(kk)) << 4) + (m & 4) * 2;
             v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) pr_i16x4*)p);
         }
         __builtin_memcpy(&r, v, 16);
@@ -123,12 +108,69 @@ __device__ __forceinline__ pr_bf16x8 fragment(const uint8_t* tile, int first, in
     }
     return r;
 }
+// the same of fp32 (a step is one fragment of 32 k)
+struct Values {
+    float v[8];
+};
+template <bool KMAJOR, int B>
+__device__ __forceinline__ Values fragment_f32(const uint8_t* tile, int first, int f, int lane) {
+    const int i = lane & 15, g = lane >> 4, m = first + f * 16 + i;
+    Values r;
+    if constexpr (KMAJOR) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int k = 8 * g + e;
+            r.v[e] = *(const float*)(tile + k * (4 * B) + (((m >> 2) ^ kmajor_key<kF32, B>(k)) << 4) + (m & 3) * 4);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const pr_f32x4 x = *(const pr_f32x4*)(tile + m * kStepBytes + (((2 * g + h) ^ row_key(m)) << 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.v[4 * h + e] = x[e];
+        }
+    }
+    return r;
+}
+// its three bf16 terms: each the nearest to what the terms before it leave.  Two values at a time, taken back to fp32 as
+// bits: from the bf16 values the compiler would round each one a second time.
+struct Terms {
+    pr_bf16x8 t[3];
+};
+__device__ __forceinline__ Terms split_terms(Values x) {
+    Terms r;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+            w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f_t{x.v[2 * e], x.v[2 * e + 1]}, v2));
+            if (t < 2) {
+                x.v[2 * e] -= __uint_as_float(w[e] << 16);
+                x.v[2 * e + 1] -= __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+        __builtin_memcpy(&r.t[t], w, 16);
+    }
+    return r;
+}
+// acc[f] += the six largest products of terms, the smallest first
+__device__ __forceinline__ void multiply_f32(pr_f32x4 (&acc)[4], const Terms (&q)[4], const Terms& p) {
+    constexpr int TQ[6] = {2, 0, 1, 1, 0, 0}, TP[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+    for (int n = 0; n < 6; ++n)
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[f].t[TQ[n]], p.t[TP[n]], acc[f], 0, 0, 0);
+}
+
 // The steps [first, end) of a workgroup's part of the sum
 struct Steps {
     int first, end;
-    template <bool MX8>
+    template <int FMT>
     __device__ __forceinline__ void init(const ProductArgs& a) {
-        const int total = (a.K + (MX8 ? 127 : 63)) / (MX8 ? 128 : 64) * a.pairs;
+        const int total = (a.K + kStep<FMT> - 1) / kStep<FMT>;
         first = 0;
         end = total;
         if (a.splits > 1) {                                  // (K up to 2^20: 32 bits hold the products)
@@ -159,19 +201,20 @@ struct ScaleLoads {
 };
 
 // The lane's share of every load of a tile's step.
-template <bool MX8, bool PK, bool QK, int BI, int BJ, int W, bool GATED>
+template <int FMT, bool PK, bool QK, int BI, int BJ, int W, bool GATED>
 struct StepLoads {
+    static constexpr bool MX8 = FMT == kMx8;
     static constexpr int NP = BI / 8 / W, NQ = BJ / 8 / W, NS = MX8 ? ((BI + BJ) / 64 + W - 1) / W : 0, PER = NP + NQ + NS;
     static constexpr int PB = BI * kStepBytes, QB = BJ * kStepBytes, BYTES = PB + QB + NS * W * 256;
     static_assert(BI % 64 == 0, "whole loads of scales");
-    TileLoads<PK, BI, NP, false> p;
-    TileLoads<QK, BJ, NQ, GATED> q;
+    TileLoads<FMT, PK, BI, NP, false> p;
+    TileLoads<FMT, QK, BJ, NQ, GATED> q;
     ScaleLoads sc[NS > 0 ? NS : 1];
 
     __device__ __forceinline__ void init(const ProductArgs& a, const Steps& s, int i0, int j0, int wave, int lane) {
         const int JH = GATED ? a.J / 2 : a.J;
-        p.init(a.p, i0, a.I, a.p_ld, a.K, MX8 ? 1 : 2, a.p_plane, kPlaneP, a.pairs, s.first, s.end, wave, lane);
-        q.init(a.q, j0, JH, a.q_ld, a.K, MX8 ? 1 : 2, a.q_plane, kPlaneQ, a.pairs, s.first, s.end, wave, lane);
+        p.init(a.p, i0, a.I, a.p_ld, a.K, s.first, s.end, wave, lane);
+        q.init(a.q, j0, JH, a.q_ld, a.K, s.first, s.end, wave, lane);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int at = (wave * NS + n) * 64;
@@ -260,10 +303,10 @@ __device__ __forceinline__ void multiply_mx8(pr_f32x4 (&acc)[4], const pr_i32x8&
 }
 
 // Tile of BI rows and 64 WJ columns; WI x WJ waves, each BI / WI rows by 64 columns.  ST stages.
-template <bool MX8, bool PK, bool QK, int BI, int WI, int WJ, int ST, bool GATED>
+template <int FMT, bool PK, bool QK, int BI, int WI, int WJ, int ST, bool GATED>
 __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
     constexpr int W = WI * WJ, BJ = 64 * WJ, FI = BI / WI / 16, BH = GATED ? BJ / 2 : BJ;
-    typedef StepLoads<MX8, PK, QK, BI, BJ, W, GATED> Loads;
+    typedef StepLoads<FMT, PK, QK, BI, BJ, W, GATED> Loads;
     constexpr int STG = Loads::BYTES, PB = Loads::PB, PER = Loads::PER;
     __shared__ __align__(1024) uint8_t ring[ST * STG];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -273,7 +316,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
     i0 *= BI;
     j0 *= BH;
     Steps steps;
-    steps.init<MX8>(a);
+    steps.init<FMT>(a);
     Loads loads;
     loads.init(a, steps, i0, j0, wave, lane);
     const int wi = wave / WJ * (BI / WI), wj = wave % WJ * 64;
@@ -291,7 +334,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
         loads.load(ring + (at == 0 ? ST - 1 : at - 1) * STG, wave, lane);
         const uint8_t* st = ring + at * STG;
         at = at + 1 == ST ? 0 : at + 1;
-        if constexpr (MX8) {
+        if constexpr (FMT == kMx8) {
             pr_i32x8 p[FI], q[4];
             int ps[(FI + 3) / 4];                            // (fewer fragments: the other bytes are not used)
             const int qs = four_scales(st + PB + Loads::QB + 4 * BI, wj, lane);
@@ -305,6 +348,25 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
                 constexpr int fi = decltype(n)::value;
                 multiply_mx8<fi>(acc[fi], p[fi], q, ps[fi / 4], qs);
             }, std::make_integer_sequence<int, FI>{});
+        } else if constexpr (FMT == kF32) {
+            Values pv[FI];
+            Terms q[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) q[f] = split_terms(fragment_f32<QK, BJ>(st + PB, wj, f, lane));
+#pragma unroll
+            for (int fi = 0; fi < FI; ++fi) pv[fi] = fragment_f32<PK, BI>(st, wi, fi, lane);
+            Terms p = split_terms(pv[0]);
+#pragma unroll
+            for (int fi = 0; fi < FI; ++fi) {                // one fragment's products over the next one's terms
+                const Terms now = p;
+                if (fi + 1 < FI) p = split_terms(pv[fi + 1]);
+                multiply_f32(acc[fi], q, now);
+#pragma unroll
+                for (int n = 0; n < 24; ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+                }
+            }
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -323,16 +385,20 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
     }
     wait_vm<0>();                                            // no direct load is under way
     ring_barrier();
-    static_assert(ST * STG >= W * FI * 4096, "the waves' sums fit into the ring");
-    uint8_t* mine = ring + wave * FI * 4096;
+    constexpr int RF = FI > 4 ? 4 : FI;                      // 16 RF rows at a time
+    static_assert(ST * STG >= W * RF * 4096, "the waves' sums fit into the ring");
+    uint8_t* mine = ring + wave * RF * 4096;
 #pragma unroll
-    for (int fi = 0; fi < FI; ++fi)
+    for (int f0 = 0; f0 < FI; f0 += RF) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            mfma_results_here(acc[fi][f]);
-            *sums_chunk(mine, fi * 16 + (lane & 15), f * 4 + (lane >> 4)) = acc[fi][f];
-        }
-    write_rows<FI * 16, GATED>(a, mine, i0 + wi, GATED ? j0 + wj / 2 : j0 + wj, lane);
+        for (int fi = 0; fi < RF; ++fi)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                mfma_results_here(acc[f0 + fi][f]);
+                *sums_chunk(mine, fi * 16 + (lane & 15), f * 4 + (lane >> 4)) = acc[f0 + fi][f];
+            }
+        write_rows<RF * 16, GATED>(a, mine, i0 + wi + f0 * 16, GATED ? j0 + wj / 2 : j0 + wj, lane);
+    }
 }
 
 // of 32 rows, first + 32 f ..: 16 k from 16 j on
@@ -346,7 +412,7 @@ __device__ __forceinline__ pr_bf16x8 fragment32(const uint8_t* tile, int first, 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int kk = k + 4 * e;
-            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<B>(kk)) << 4) + (m & 4) * 2;
+            const uint8_t* p = tile + kk * (2 * B) + (((m >> 3) ^ kmajor_key<kBf16, B>(kk)) << 4) + (m & 4) * 2;
             v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) pr_i16x4*)p);
         }
         __builtin_memcpy(&r, v, 16);
@@ -374,8 +440,9 @@ __device__ __forceinline__ int scales32(const uint8_t* scales, int first, int f,
 // handed out between the products (a burst of them would hold the products up).  One barrier a step, before its last
 // part: every wave has the whole step in registers then, and the next one has landed.  P has two places in LDS, whose
 // loads follow that barrier; Q three, and its loads a step more to land.  (With MXFP8 the scales leave room for two.)
-template <bool MX8, bool PK, bool QK, bool GATED>
+template <int FMT, bool PK, bool QK, bool GATED>
 __global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
+    constexpr bool MX8 = FMT == kMx8;
     constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kStepBytes, QS = MX8 ? 2 : 3, PARTS = MX8 ? 2 : 4;
     constexpr int QAT = 2 * TB, SAT = QAT + QS * TB, SB = MX8 ? 8 * B : 0;
     __shared__ __align__(1024) uint8_t lds[SAT + 2 * SB];
@@ -386,12 +453,12 @@ __global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
     i0 *= B;
     j0 *= BH;
     Steps steps;
-    steps.init<MX8>(a);
-    TileLoads<PK, B, 8, false> lp;
-    TileLoads<QK, B, 8, GATED> lq;
+    steps.init<FMT>(a);
+    TileLoads<FMT, PK, B, 8, false> lp;
+    TileLoads<FMT, QK, B, 8, GATED> lq;
     ScaleLoads ls[2];
-    lp.init(a.p, i0, a.I, a.p_ld, a.K, MX8 ? 1 : 2, a.p_plane, kPlaneP, a.pairs, steps.first, steps.end, wave, lane);
-    lq.init(a.q, j0, JH, a.q_ld, a.K, MX8 ? 1 : 2, a.q_plane, kPlaneQ, a.pairs, steps.first, steps.end, wave, lane);
+    lp.init(a.p, i0, a.I, a.p_ld, a.K, steps.first, steps.end, wave, lane);
+    lq.init(a.q, j0, JH, a.q_ld, a.K, steps.first, steps.end, wave, lane);
     if constexpr (MX8) {
         ls[0].init<false>(a.p_scales, i0, wave * 64, a.I, a.K, steps, lane);
         ls[1].init<GATED>(a.q_scales, j0, wave * 64, JH, a.K, steps, lane);
@@ -596,8 +663,8 @@ struct TileChoice {
 static const TileChoice kTiles[] = {
     {64, 64, 2, 5.4f, 0.25f, 0.42f}, {64, 128, 2, 5.7f, 0.32f, 0.57f}, {128, 256, 1, 5.2f, 0.92f, 0.92f}, {256, 256, 1, 6.2f, 1.55f, 1.55f}};
 
-static int choose_tile(ProductArgs& a, bool mx8) {
-    const int steps = (a.K + (mx8 ? 127 : 63)) / (mx8 ? 128 : 64) * a.pairs;
+static int choose_tile(ProductArgs& a, int per_step, float slower) {
+    const int steps = (a.K + per_step - 1) / per_step;
     float least = 0.0f;
     int best = -1;
     for (int t = 0; t < 4; ++t) {
@@ -607,8 +674,7 @@ static int choose_tile(ProductArgs& a, bool mx8) {
             const size_t part = (size_t)splits * a.I * a.J * 4;
             if (splits > 1 && (splits * 4 > steps || part > product_part_bytes(a.I, a.J) || tiles * splits > 256 * c.per_cu)) break;
             const long long groups = tiles * splits, rounds = (groups + 256 * c.per_cu - 1) / (256 * c.per_cu);
-            // (a step of 128 codes takes a third longer than one of 64 bf16)
-            const float step = (groups <= 256 ? c.step : c.step2) * (mx8 ? 1.35f : 1.0f);
+            const float step = (groups <= 256 ? c.step : c.step2) * slower;
             float us = rounds * (steps / (float)splits) * step + c.start * (rounds < 2 ? 1.0f : 0.5f + 0.5f * rounds);
             if (splits > 1) us += 4.0f + part * 1.5e-7f;
             if (best < 0 || us < least) {
@@ -621,39 +687,51 @@ static int choose_tile(ProductArgs& a, bool mx8) {
     return best;
 }
 
-template <bool MX8, bool PK, bool QK, bool GATED, int BI, int WI, int WJ, int ST>
+template <int FMT, bool PK, bool QK, bool GATED, int BI, int WI, int WJ, int ST>
 static void product_launch_as(const ProductArgs& a, hipStream_t st) {
     const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 32 * WJ : 64 * WJ, tiles = (a.I + BI - 1) / BI * ((JH + BH - 1) / BH);
-    MOE_LAUNCH((k_product<MX8, PK, QK, BI, WI, WJ, ST, GATED>), dim3(tiles, a.splits), dim3(64 * WI * WJ), 0, st, a);
+    MOE_LAUNCH((k_product<FMT, PK, QK, BI, WI, WJ, ST, GATED>), dim3(tiles, a.splits), dim3(64 * WI * WJ), 0, st, a);
 }
 
-template <bool MX8, bool PK, bool QK, bool GATED>
+template <int FMT, bool PK, bool QK, bool GATED>
 static void product_launch(ProductArgs& a, hipStream_t st) {
-    switch (choose_tile(a, MX8)) {
-        case 0: product_launch_as<MX8, PK, QK, GATED, 64, 4, 1, 4>(a, st); break;
-        case 1: product_launch_as<MX8, PK, QK, GATED, 64, 2, 2, 3>(a, st); break;
-        case 2: product_launch_as<MX8, PK, QK, GATED, 128, 2, 4, 3>(a, st); break;
-        default: {
-            const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 128 : 256, tiles = (a.I + 255) / 256 * ((JH + BH - 1) / BH);
-            MOE_LAUNCH((k_product_large<MX8, PK, QK, GATED>), dim3(tiles, a.splits), dim3(256), 0, st, a);
+    switch (choose_tile(a, kStep<FMT>, FMT == kMx8 ? 1.35f : FMT == kF32 ? 2.9f : 1.0f)) {
+        case 0: product_launch_as<FMT, PK, QK, GATED, 64, 4, 1, 4>(a, st); break;
+        case 1: product_launch_as<FMT, PK, QK, GATED, 64, 2, 2, 3>(a, st); break;
+        case 2: product_launch_as<FMT, PK, QK, GATED, 128, 2, 4, 3>(a, st); break;
+        default:
+            if constexpr (FMT == kF32) {
+                product_launch_as<FMT, PK, QK, GATED, 256, 2, 4, 2>(a, st);
+            } else {
+                const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 128 : 256, tiles = (a.I + 255) / 256 * ((JH + BH - 1) / BH);
+                MOE_LAUNCH((k_product_large<FMT, PK, QK, GATED>), dim3(tiles, a.splits), dim3(256), 0, st, a);
+            }
+    }
+}
+template <int FMT>
+static void product_launch(ProductArgs& a, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st) {
+    if (gated) {
+        product_launch<FMT, false, false, true>(a, st);
+        return;
+    }
+    if constexpr (FMT != kMx8) {
+        if (p_kmajor) {
+            product_launch<FMT, true, true, false>(a, st);
+            return;
+        }
+        if (q_kmajor) {
+            product_launch<FMT, false, true, false>(a, st);
+            return;
         }
     }
+    product_launch<FMT, false, false, false>(a, st);
 }
 
-hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st) {
+hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st) {
     trace("product", 0, st);
-    if (mx8) {
-        if (gated) product_launch<true, false, false, true>(a, st);
-        else product_launch<true, false, false, false>(a, st);
-    } else if (gated) {
-        product_launch<false, false, false, true>(a, st);
-    } else if (p_kmajor) {
-        product_launch<false, true, true, false>(a, st);
-    } else if (q_kmajor) {
-        product_launch<false, false, true, false>(a, st);
-    } else {
-        product_launch<false, false, false, false>(a, st);
-    }
+    if (bytes == 2) product_launch<kBf16>(a, p_kmajor, q_kmajor, gated, st);
+    else if (bytes == 4) product_launch<kF32>(a, p_kmajor, q_kmajor, gated, st);
+    else product_launch<kMx8>(a, p_kmajor, q_kmajor, gated, st);
     trace("product", 1, st);
     if (a.splits > 1) {
         const size_t n = (size_t)a.I * (((gated ? a.J / 2 : a.J) + 7) / 8);
@@ -663,46 +741,6 @@ hipError_t launch_product(ProductArgs a, bool mx8, bool p_kmajor, bool q_kmajor,
         else MOE_LAUNCH((k_product_finish<false>), grid, dim3(256), 0, st, a);
         trace("product_finish", 1, st);
     }
-    return hipGetLastError();
-}
-
-// ---------------------------------------------------------------------------------------------
-// three bf16 planes of fp32 values: each the nearest bf16 to what the planes before it leave.  A value whose
-// nearest bf16 would be infinite is cut instead; an infinity or a NaN is its own first plane, the others zero.
-// ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ void planes8(const f32x8& v, uint4 (&out)[3]) {
-    f32x8 rest = v;
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-        uint32_t w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float r = rest.v[e];
-            uint32_t b = f32_to_bf16_bits(r);
-            const bool finite = __builtin_isfinite(r);
-            if (finite && (b & 0x7fffu) == 0x7f80u) b = __float_as_uint(r) >> 16;
-            w[e] = b;
-            rest.v[e] = finite ? r - bf16_bits_to_f32((uint16_t)b) : 0.0f;
-        }
-        out[p] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-    }
-}
-__device__ __forceinline__ void store_planes8(uint16_t* planes, size_t plane, size_t i, const f32x8& v) {
-    uint4 w[3];
-    planes8(v, w);
-#pragma unroll
-    for (int p = 0; p < 3; ++p) *(uint4*)(planes + p * plane + i) = w[p];
-}
-
-__global__ __launch_bounds__(256) void k_planes(const float* __restrict__ x, size_t n, uint16_t* __restrict__ planes) {
-    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (i < n) store_planes8(planes, n, i, load_act8(x, i));
-}
-
-hipError_t launch_planes(const float* x, size_t n, uint16_t* planes, hipStream_t st) {
-    trace("planes", 0, st);
-    MOE_LAUNCH(k_planes, dim3((uint32_t)((n / 8 + 255) / 256)), dim3(256), 0, st, x, n, planes);
-    trace("planes", 1, st);
     return hipGetLastError();
 }
 
@@ -763,13 +801,8 @@ __global__ __launch_bounds__(256) void k_pre_grad(PreGradArgs a) {
                 for (int e = 0; e < 8; ++e) d.v[e] = dy.v[e] * slope(a.activation, v.v[e]);
             }
             if (a.d) {
-                if constexpr (sizeof(XT) == 4) {
-                    store_planes8(a.d, (size_t)a.T * ld, at, d);
-                    if constexpr (GATED) store_planes8(a.d, (size_t)a.T * ld, at + a.N, du);
-                } else {
-                    store_act8(a.d, at, d);
-                    if constexpr (GATED) store_act8(a.d, at + a.N, du);
-                }
+                store_act8((XT*)a.d, at, d);
+                if constexpr (GATED) store_act8((XT*)a.d, at + a.N, du);
             }
             if constexpr (!GATED) {
 #pragma unroll
@@ -796,8 +829,8 @@ __global__ __launch_bounds__(256) void k_bias_sums(PreGradArgs a, int chunks) {
 }
 
 hipError_t launch_pre_grad(const PreGradArgs& a, bool f32, hipStream_t st) {
-    int chunks = (a.T + 31) / 32;
-    if (chunks > kBiasChunks) chunks = kBiasChunks;
+    int chunks = a.bias_part ? (a.T + 31) / 32 : (a.T + 7) / 8;
+    if (a.bias_part && chunks > kBiasChunks) chunks = kBiasChunks;
     const dim3 grid((a.N + 255) / 256, chunks);
     trace("pre_grad", 0, st);
     if (a.gated) {

@@ -13,8 +13,6 @@
 
 namespace moe {
 
-enum { kFewBf16 = 0, kFewF32 = 1, kFewMx8 = 2 };
-
 // eight codes times their block's scale (the E8M0 byte as the exponent of a float), exact in bf16
 __device__ __forceinline__ pr_bf16x8 few_mx8(uint32_t a, uint32_t b, float scale) {
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
@@ -26,8 +24,8 @@ __device__ __forceinline__ pr_bf16x8 few_mx8(uint32_t a, uint32_t b, float scale
 // gated: of a tile's 16 F rows the first half are the gate's of 8 F columns of h, the others the up projection's
 template <int FMT, int F, int C, int W, int ST, bool GATED>
 __global__ __launch_bounds__(64 * W) void k_product_few(ProductArgs a, int tiles) {
-    constexpr bool MX8 = FMT == kFewMx8;
-    constexpr int ES = FMT == kFewF32 ? 4 : MX8 ? 1 : 2, COLS = GATED ? 8 * F : 16 * F, SL = MX8 ? 2 : 0;
+    constexpr bool MX8 = FMT == kMx8;
+    constexpr int ES = kSize<FMT>, COLS = GATED ? 8 * F : 16 * F, SL = MX8 ? 2 : 0;
     constexpr int QB = 2048 * F, PB = 2048 * C, STG = QB + PB + 256 * SL, PER = 2 * F + 2 * C + SL;
     static_assert((ST - 1) * PER < 64, "vmcnt holds 6 bits");
     static_assert(W * (ST * STG + F * C * 1024) <= 160 << 10, "LDS");
@@ -139,7 +137,7 @@ __global__ __launch_bounds__(64 * W) void k_product_few(ProductArgs a, int tiles
                     for (int f = 0; f < F; ++f)
 #pragma unroll
                         for (int c = 0; c < C; ++c) {
-                            if constexpr (FMT == kFewF32) {
+                            if constexpr (FMT == kF32) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(q[f][h][e]), __uint_as_float(p[c][h][e]),
@@ -210,14 +208,14 @@ bool product_few_ok(const ProductArgs& a, int bytes) {
 hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st) {
     trace("product_few", 0, st);
     if (bytes == 2) {
-        if (gated) few_launch<kFewBf16, true>(a, st);
-        else few_launch<kFewBf16, false>(a, st);
+        if (gated) few_launch<kBf16, true>(a, st);
+        else few_launch<kBf16, false>(a, st);
     } else if (bytes == 4) {
-        if (gated) few_launch<kFewF32, true>(a, st);
-        else few_launch<kFewF32, false>(a, st);
+        if (gated) few_launch<kF32, true>(a, st);
+        else few_launch<kF32, false>(a, st);
     } else {
-        if (gated) few_launch<kFewMx8, true>(a, st);
-        else few_launch<kFewMx8, false>(a, st);
+        if (gated) few_launch<kMx8, true>(a, st);
+        else few_launch<kMx8, false>(a, st);
     }
     trace("product_few", 1, st);
     return hipGetLastError();

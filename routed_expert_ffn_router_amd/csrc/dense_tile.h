@@ -16,8 +16,12 @@ typedef __attribute__((address_space(3))) uint8_t* pr_lds_t;
 constexpr int kStepBytes = 128;              // of a row and step: 64 bf16, 128 codes
 constexpr uint32_t kNowhere = 0x80000000u;   // past every descriptor's end: a load from there brings zeros
 
-// planes of the six products of fp32 operands
-constexpr uint32_t kPlaneP = 0x021100u, kPlaneQ = 0x200110u;   // (0,0) (0,1) (1,1) (1,0) (2,0) (0,2), four bits each
+// formats of the operands: values of a step, bytes of a value
+enum { kBf16 = 0, kF32 = 1, kMx8 = 2 };
+template <int FMT>
+constexpr int kStep = FMT == kBf16 ? 64 : FMT == kF32 ? 32 : 128;
+template <int FMT>
+constexpr int kSize = kStepBytes / kStep<FMT>;
 
 // Direct loads to LDS: 16 (4) bytes per lane from base + off, lane l's to lds + 16 l (4 l); an offset past the descriptor's
 // end brings zeros.  In assembly, because the compiler has every transposing read of LDS wait for all direct loads that
