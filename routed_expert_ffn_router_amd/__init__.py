@@ -169,17 +169,29 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+_torch_c = None
+
+
+def _torch_core():
+    """torch._C with the GPU initialised; its calls take half the time of torch.cuda's, which look at that every time."""
+    global _torch_c
+    if _torch_c is None:
+        import torch
+        torch.cuda.current_device()
+        _torch_c = torch._C
+    return _torch_c
+
+
 def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    return (_torch_c or _torch_core())._cuda_getDevice()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         # the current stream of the current device; torch.cuda.current_stream() builds a Stream object
         # around this handle, which takes 2.5 us, half of a small call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        c = _torch_c or _torch_core()
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -304,7 +316,7 @@ def _pointers(fn: str, *args) -> list:
     out = []
     device = None
     for t, dtype, n in args:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int or isinstance(t, int):
             out.append(t)
             continue
         on = t.get_device()
@@ -369,12 +381,17 @@ def moe_block_norm(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: 
                                                  residual_scale, eps, pxo, pn, _stream(stream)))
 
 
+_EIGHT_BITS = {}
+
+
 def _eight_bits(t, kind: str):
     """dtype of a tensor of MXFP8 codes or scales: torch's float8 type of that name, or its bytes as uint8."""
-    import torch
-    if t is not None and not isinstance(t, int) and t.dtype is getattr(torch, kind):
+    if not _EIGHT_BITS:
+        import torch
+        _EIGHT_BITS.update({k: getattr(torch, k) for k in ("float8_e4m3fn", "float8_e8m0fnu", "uint8")})
+    if t is not None and not isinstance(t, int) and t.dtype is _EIGHT_BITS[kind]:
         return t.dtype
-    return torch.uint8
+    return _EIGHT_BITS["uint8"]
 
 
 def moe_block_norm_mx8(shape, x, y, T: int, post_gamma, pre_gamma, gate, gate_kind: int, residual_scale: float,
@@ -475,10 +492,11 @@ def _operands(dense, x, x_scales, T: int, w, w_scales, R: int) -> list:
 def moe_matmul(dense, x, x_scales, T: int, w, w_scales, bias, residual, pre, y, ws, ws_bytes=None, stream=None):
     act, f32, _, _ = _dtypes(dense.act_dtype)
     N = dense.rows
+    n = T * N
     scratch, ws_bytes = _scratch(ws, ws_bytes)
     px, pxs, pw, pws, pb, pr, pp, py, ps = _pointers(
-        "moe_matmul", *_operands(dense, x, x_scales, T, w, w_scales, N), (bias, f32, N), (residual, act, T * N),
-        (pre, act, T * N), (y, act, T * N), scratch)
+        "moe_matmul", *_operands(dense, x, x_scales, T, w, w_scales, N), (bias, f32, N), (residual, act, n), (pre, act, n),
+        (y, act, n), scratch)
     _check("moe_matmul", _lib.moe_matmul(ctypes.byref(dense), px, pxs, T, pw, pws, pb, pr, pp, py, ps, ws_bytes,
                                          _stream(stream)))
 
