@@ -264,14 +264,32 @@ __device__ __forceinline__ void write_rows(const ProductArgs& a, uint8_t* mine, 
             if (GATED) store_act8(sums, (size_t)N, read8(r, 8 + 2 * c));
         }
     } else {
+        f32x8 bias = {};
+        if (!GATED && a.bias && n < N) bias = load_act8(a.bias, (size_t)n);
         with_activation(a.activation, [&](auto f) {
             constexpr int F = decltype(f)::value;
-#pragma unroll 2
-            for (int r = lane / PER_ROW; r < ROWS; r += 64 / PER_ROW) {
-                const int i = row + r;
-                const f32x8 v = read8(r, 2 * c);
-                if constexpr (GATED) gated_out8<F>(a, i, n, i < a.I && n < N, v, read8(r, 8 + 2 * c));
-                else if (i < a.I && n < N) product_out8<F>(a, i, n, v);
+            if constexpr (GATED) {
+#pragma unroll 4
+                for (int r = lane / PER_ROW; r < ROWS; r += 64 / PER_ROW)
+                    gated_out8<F>(a, row + r, n, row + r < a.I && n < N, read8(r, 2 * c), read8(r, 8 + 2 * c));
+            } else {
+                // four rows at a time, their residuals in flight together
+#pragma unroll 1
+                for (int r0 = lane / PER_ROW; r0 < ROWS; r0 += 32) {
+                    f32x8 res[ROWS < 32 ? ROWS / 8 : 4];
+                    constexpr int R = sizeof(res) / sizeof(res[0]);
+#pragma unroll
+                    for (int u = 0; u < R; ++u) {
+                        const int i = row + r0 + 8 * u;
+                        res[u] = f32x8{};
+                        if (a.residual && i < a.I && n < N) res[u] = residual8(a, (size_t)i * a.J + n);
+                    }
+#pragma unroll
+                    for (int u = 0; u < R; ++u) {
+                        const int i = row + r0 + 8 * u;
+                        if (i < a.I && n < N) product_out8<F>(a, (size_t)i * a.J + n, read8(r0 + 8 * u, 2 * c), bias, res[u]);
+                    }
+                }
             }
         });
     }
