@@ -765,26 +765,27 @@ hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor
 // A scale byte b stands for 2^(b - 127); codes of blocks under 2^-117 that pass bf16's smallest number are rounded.
 __global__ __launch_bounds__(256) void k_unpack(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, size_t n,
                                                 uint16_t* __restrict__ values) {
-    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (i >= n) return;
-    const uint2 c = *(const uint2*)(codes + i);
-    const float sc = mx8_scale(scales[i / 32]);
-    f32x8 v;
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (size_t)gridDim.x * 2048) {
+        const uint2 c = *(const uint2*)(codes + i);
+        const float sc = mx8_scale(scales[i / 32]);
+        f32x8 v;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const uint32_t w = e ? c.y : c.x;
-        const v2f_t lo = fp8x2_decode<false>(w, 1.0f), hi = fp8x2_decode<true>(w, 1.0f);
-        v.v[4 * e] = lo[0] * sc;
-        v.v[4 * e + 1] = lo[1] * sc;
-        v.v[4 * e + 2] = hi[0] * sc;
-        v.v[4 * e + 3] = hi[1] * sc;
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t w = e ? c.y : c.x;
+            const v2f_t lo = fp8x2_decode<false>(w, 1.0f), hi = fp8x2_decode<true>(w, 1.0f);
+            v.v[4 * e] = lo[0] * sc;
+            v.v[4 * e + 1] = lo[1] * sc;
+            v.v[4 * e + 2] = hi[0] * sc;
+            v.v[4 * e + 3] = hi[1] * sc;
+        }
+        store_act8(values, i, v);
     }
-    store_act8(values, i, v);
 }
 
 hipError_t launch_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, uint16_t* values, hipStream_t st) {
     trace("unpack", 0, st);
-    MOE_LAUNCH(k_unpack, dim3((uint32_t)((n / 8 + 255) / 256)), dim3(256), 0, st, codes, scales, n, values);
+    const size_t blocks = (n / 8 + 255) / 256;
+    MOE_LAUNCH(k_unpack, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, st, codes, scales, n, values);
     trace("unpack", 1, st);
     return hipGetLastError();
 }
@@ -848,7 +849,8 @@ __global__ __launch_bounds__(256) void k_bias_sums(PreGradArgs a, int chunks) {
 
 hipError_t launch_pre_grad(const PreGradArgs& a, bool f32, hipStream_t st) {
     int chunks = a.bias_part ? (a.T + 31) / 32 : (a.T + 7) / 8;
-    if (a.bias_part && chunks > kBiasChunks) chunks = kBiasChunks;
+    const int most = a.bias_part ? kBiasChunks : 1024;
+    if (chunks > most) chunks = most;
     const dim3 grid((a.N + 255) / 256, chunks);
     trace("pre_grad", 0, st);
     if (a.gated) {

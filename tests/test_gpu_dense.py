@@ -489,6 +489,46 @@ def test_streams_and_graph_replays_give_the_same_bits(act, T):
         assert all(torch.equal(a, b) for a, b in zip(want, got)), seed
 
 
+@pytest.mark.parametrize("T", [3, 70])
+def test_offsets_past_32_bits(T):
+    """A weight of more than 4 GiB: its last rows forward, and their share of the input's gradient and of their own."""
+    K, last = 4096, 72
+    N = (1 << 32) // (2 * K) + 1032
+    g = gen(15)
+    w = torch.zeros(N, K, dtype=BF16, device="cuda")
+    w[-last:] = rand(g, last, K, dtype=BF16, std=0.1)
+    x, dy = rand(g, T, K, dtype=BF16), rand(g, T, N, dtype=BF16)
+    d = dense(N, K, BF16)
+    ws, y, dx, dw = scratch(d, T), nan(T, N, dtype=BF16), nan(T, K, dtype=BF16), torch.empty_like(w)
+    m.moe_matmul(d, x, None, T, w, None, None, None, None, y, ws)
+    assert (y[:, :-last] == 0).all()
+    check(y[:, -last:], ref.product(x.double(), w[-last:].double(), "bf16"), BF16, "y")
+    m.moe_matmul_backward(d, x, T, w, None, dy, dx, dw, None, ws)
+    wx = ref.product(dy[:, -last:].double(), w[-last:].double().t(), "bf16")
+    check(dx, Val(wx.v, wx.e * (N // last)), BF16, "dx")      # (as many more additions, of zeros)
+    check(dw[-last:], ref.product(dy[:, -last:].double().t(), x.double().t(), "bf16"), BF16, "dw")
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace and outputs."""
+    g = gen(16)
+    T, N, K = 300, 1032, 2056
+    for act in (BF16, F32):
+        d = dense(N, K, act, "gelu")
+        xs, w = [rand(g, T, K, dtype=act) for _ in range(2)], rand(g, 2 * N, K, dtype=act, std=0.1)
+        want = [nan(T, N, dtype=act) for _ in xs]
+        for x, y in zip(xs, want):
+            m.moe_gated(d, x, None, T, w, None, None, y, None, scratch(d, T))
+        torch.cuda.synchronize()
+        streams, got, ws = [torch.cuda.Stream() for _ in xs], [nan(T, N, dtype=act) for _ in xs], [scratch(d, T) for _ in xs]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for k in range(2):
+                m.moe_gated(d, xs[k], None, T, w, None, None, got[k], None, ws[k], stream=streams[k])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_rows_past_the_last_token_are_left_alone():
     T, N, K = 5, 72, 136
     g = gen(14)
