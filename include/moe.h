@@ -419,14 +419,18 @@ moe_status moe_linear(const moe_matrix *matrix, const uint8_t *q, const uint8_t 
  * training.
  *
  * moe_dense describes one: rows outputs (of the gated block: columns of h) and cols inputs.
- *   operands MOE_OPERANDS_ACT: x and the weight in act_dtype.  bf16 values enter the products as they are.  fp32
- *     values enter as three bf16 terms each, of which the six largest products are summed (what is left out is
- *     below 2^-24 of |x| |W|); bits below 2^-133 are left out, and a sum that an infinity enters is infinite or NaN.
+ *   operands MOE_OPERANDS_ACT: x and the weight in act_dtype.  bf16 values enter the products as they are, and so do
+ *     fp32 values in the forward products of up to 64 tokens.  Beyond and in the gradients, fp32 values enter as three
+ *     bf16 terms each, of which the six largest products are summed (what is left out is below 2^-24 of |x| |W|); bits
+ *     below 2^-133 are left out, values that bf16 rounds to infinity (0x1.ffp127 or more) count as infinite, and a sum
+ *     that an infinity enters is infinite or NaN.
  *   operands MOE_OPERANDS_MXFP8: x and the weight as E4M3FN codes with a scale byte for each 32 consecutive columns
  *     (moe_block_norm_mx8 writes both), x_scales [T][cols/32] and w_scales [weight rows][cols/32]; forward only.
- *     With bf16 outputs the sums are the scaled FP8 matrix cores', which cut the products of eight neighbouring codes to
- *     2^-13 of the largest before they add them (1.5e-5 of a result); with fp32 outputs the values enter bf16 products,
- *     whose sums are right to fp32.
+ *     With fp32 outputs, or few tokens (all up to 32, some calls up to 64), the values enter bf16 products, whose sums
+ *     are right to fp32; bits below 2^-133 are left out, and a value of 2^128 or more (scale bytes from 247 on) is
+ *     infinite, its sums infinite or NaN.  Otherwise the sums are the scaled FP8 matrix cores', which cut the products
+ *     of eight neighbouring codes to 2^-13 of the largest before they add them (7 * 2^-13 of sum |x| |W| at most,
+ *     about 1.5e-5 of a result).  So the same token's result may differ in that between a short call and a long one.
  *   Sums are fp32; y, h, pre, dx and dw are rounded once to act_dtype.
  * Limits: rows a multiple of 8, cols of 8 (MXFP8: of 128), each at most 2^20, rows * cols at most 2^33,
  * T <= 65536 (MOE_ERR_UNSUPPORTED beyond).  Pointers are 16-byte aligned (scales of operands: 4 bytes; of h: any).

@@ -348,6 +348,23 @@ def test_mxfp8_nan_blocks():
         assert torch.equal(torch.isnan(y), want)
 
 
+@pytest.mark.parametrize("T", [3, 20, 50, 200])
+def test_mxfp8_scales_of_the_whole_range(T):
+    N, K = 64, 256
+    g = gen(17)
+    for act in (BF16, F32):
+        for sx, sw in ((0, 180), (1, 180), (180, 0), (246, 10), (10, 246), (246, 7)):
+            (x, xs), (w, ws) = mx8(g, T, K), mx8(g, N, K)
+            xs.fill_(sx), ws.fill_(sw)
+            d, y = dense(N, K, act, "none", True), nan(T, N, dtype=act)
+            m.moe_matmul(d, x, xs, T, w, ws, None, None, None, y, scratch(d, T))
+            X, W = ref.values(x, xs), ref.values(w, ws)
+            want = ref.product(X, W, "mx8" if act == BF16 else "bf16")
+            # a value is right to half of bf16's smallest number, 2^-133
+            tiny = 2.0 ** -134 * (X.abs().sum(1, keepdim=True) + W.abs().sum(1))
+            check(y, Val(want.v, want.e + tiny), act, f"y {sx} {sw}")
+
+
 NORMS = [(1, 128, BF16, "none", 1, 1), (3, 256, F32, "token", 0, 1), (1, 4096, BF16, "none", 1, 1), (70, 640, BF16, "element", 1, 1),
          (33, 4352, F32, "element", 1, 1), (5, 16384, BF16, "token", 0, 1), (2, 8320, F32, "none", 1, 0), (257, 2176, BF16, "none", 0, 0)]
 
