@@ -1,4 +1,4 @@
-// Declarations of the dense products (dense.hip, dense_rows.hip): operand planes, the products' arguments, the
+// Declarations of the dense products (dense.hip, dense_few.hip): the products' arguments, the
 // epilogue shared by the kernels, and the launchers.
 #pragma once
 
@@ -30,9 +30,8 @@ struct ProductArgs {
 // ---------------------------------------------------------------------------------------------
 __device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + expf(-v)); }
 // The normal distribution's function, and exp(-v^2 / 2).  The tail by Abramowitz and Stegun, Handbook of Mathematical
-// Functions, 7.1.26, off by at most 7.5e-8 (with the roundings 6 units of 2^-24
-// of 1); erff in its place took 40 of
-// 150 us of a 4096^3 product.
+// Functions, 7.1.26, off by at most 7.5e-8 (with the roundings 8 units of 2^-24
+// of 1); erff in its place took 40 of 150 us of a 4096^3 product.
 struct Normal {
     float cdf, density;
 };

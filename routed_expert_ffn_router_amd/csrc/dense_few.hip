@@ -9,6 +9,9 @@
 // A step is 128 bytes of a row.  bf16: chunks g and 4 + g of 16 bytes for lane group g, in two products.  fp32 values enter
 // fp32 matrix products as they are: the same chunks, four values each, in eight products.  MXFP8: block g, whose
 // codes times their scale are exact in bf16, in four products.
+//
+// bf16, 4096 x 4096, one token 8.1 us (33.6 MB at 4.1 TB/s; 2 us of it are the launch and the first step's way), gated 8192 x
+// 4096 26.9 us (134 MB at 5.0 TB/s); fp32 4096 x 4096 12.8 us (5.2 TB/s); 64 tokens, bf16, 4096 x 4096 10.5 us.
 #include "dense_tile.h"
 
 namespace moe {
@@ -199,6 +202,10 @@ static void few_launch(const ProductArgs& a, hipStream_t st) {
     }
 }
 
+// Each workgroup reads all tokens again for each of its 16 F rows of the weight, which up to 32 tokens hides behind the
+// weight's own bytes.  Beyond, tiles of 64 tokens win once they fill the CUs.  us, this kernel and the tiles, 64 tokens, bf16,
+// 4096 columns: 4096 rows 10.6, 14.0; 16384 rows 56, 37.  fp32 stays here (1024 x 1024: 9, 22: no terms, no parts).  A
+// block of 32 outputs in MXFP8 needs four fragments of rows, for which LDS has no room with more than 32 tokens.
 bool product_few_ok(const ProductArgs& a, int bytes) {
     if (a.I <= 32) return true;
     if (a.I > 64 || a.out_scales) return false;
