@@ -199,10 +199,11 @@ struct ScaleLoads {
         at = scales + (size_t)first * ld + 4 * (size_t)s.first;
         steps = s.end - s.first;
     }
-    __device__ __forceinline__ void load(uint8_t* lds) const { load_lds4(at, steps > 0 ? off : kNowhere, lds); }
-    __device__ __forceinline__ void next() {
-        at += 4;
-        --steps;
+    // of the n-th step from here
+    __device__ __forceinline__ void load(uint8_t* lds, int n = 0) const { load_lds4(at + 4 * n, steps > n ? off : kNowhere, lds); }
+    __device__ __forceinline__ void next(int n = 1) {
+        at += 4 * n;
+        steps -= n;
     }
 };
 
@@ -452,186 +453,47 @@ __device__ __forceinline__ pr_bf16x8 fragment32(const uint8_t* tile, int first, 
     return r;
 }
 
-// of 128 codes, 64 from 64 j on: lane group g holds k 16 g .. and 32 + 16 g ..
-__device__ __forceinline__ pr_i32x8 fragment8_32(const uint8_t* tile, int first, int f, int j, int lane) {
+// Half steps of MXFP8: 64 codes of a row, 64 bytes.  Eight lanes, on eight rows, are served at once.
+constexpr int kHalfBytes = kStepBytes / 2;
+__device__ __forceinline__ int half_key(int r) { return (r >> 1) & 3; }
+// of 32 rows, first + 32 f ..: lane group g holds k 16 g .. and 32 + 16 g ..
+__device__ __forceinline__ pr_i32x8 fragment8_half(const uint8_t* tile, int first, int f, int lane) {
     const int row = first + f * 32 + (lane & 31), g = lane >> 5;
-    const uint4 a = *(const uint4*)(tile + row * kStepBytes + (((4 * j + g) ^ row_key(row)) << 4));
-    const uint4 b = *(const uint4*)(tile + row * kStepBytes + (((4 * j + 2 + g) ^ row_key(row)) << 4));
+    const uint4 a = *(const uint4*)(tile + row * kHalfBytes + ((g ^ half_key(row)) << 4));
+    const uint4 b = *(const uint4*)(tile + row * kHalfBytes + (((2 + g) ^ half_key(row)) << 4));
     return pr_i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
+// one operand's 256 rows: the lane's share of a half step's loads, four for each of four waves
+template <bool GATED>
+struct HalfLoads {
+    uint32_t off[4];
+    size_t upper;
+    Walk walk;
+    // as TileLoads; rows are a multiple of 128 codes long, and [s, end) are half steps
+    __device__ __forceinline__ void init(const uint8_t* p, int first, int rows, int ld, int s, int end, int wave, int lane) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int r = (wave * 4 + n) * 16 + (lane >> 2), c = (lane & 3) ^ half_key(r), row = GATED ? gated_row(r) : r;
+            off[n] = first + row < rows ? (uint32_t)(row * ld + c * 16) : kNowhere;
+        }
+        upper = (size_t)rows * ld;
+        walk.init(p + (size_t)first * ld, kHalfBytes, ld, kHalfBytes, s, end);
+    }
+    __device__ __forceinline__ void load(int n, uint8_t* lds, int wave) const {
+        load_lds16(GATED && (n & 2) ? walk.at + upper : walk.at, walk.here() > 0 ? off[n] : kNowhere, lds + (wave * 4 + n) * 1024);
+    }
+};
 // the row's four scale bytes, moved so that bytes 0 and 2 are those of the lane group's blocks
 __device__ __forceinline__ int scales32(const uint8_t* scales, int first, int f, int lane) {
     return (int)(*(const uint32_t*)(scales + 4 * (first + f * 32 + (lane & 31))) >> (8 * (lane >> 5)));
 }
 
-// Tile of 256 x 256 for large products: four waves of 128 x 128, each alone on its SIMD.  A step is four parts of 16 k (two
-// of 64 codes); while the matrix cores work on one, the next one's fragments come from LDS, and the direct loads are
-// handed out between the products (a burst of them would hold the products up).  One barrier a step, before its last
-// part: every wave has the whole step in registers then, and the next one has landed.  P has two places in LDS, whose
-// loads follow that barrier; Q three, and its loads a step more to land.  (With MXFP8 the scales leave room for two.)
-// bf16: 4096^3 112 us (1228 TFLOP/s; dx 116, dw 118), 8192^3 802 us (1370): the matrix cores are busy 81% of its cycles,
-// at a clock that falls to 1.6 GHz under the load.  MXFP8, 4096 x 4096 x 8192 145 us (1896): busy 44%, the loads have
-// half a step to land.
-template <int FMT, bool PK, bool QK, bool GATED>
-__global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
-    constexpr bool MX8 = FMT == kMx8;
-    constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kStepBytes, QS = MX8 ? 2 : 3, PARTS = MX8 ? 2 : 4;
-    constexpr int QAT = 2 * TB, SAT = QAT + QS * TB, SB = MX8 ? 8 * B : 0;
-    __shared__ __align__(1024) uint8_t lds[SAT + 2 * SB];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int JH = GATED ? a.J / 2 : a.J;
-    int i0, j0;
-    tile_place(blockIdx.x, gridDim.x, (a.I + B - 1) / B, (JH + BH - 1) / BH, &i0, &j0);
-    i0 *= B;
-    j0 *= BH;
-    Steps steps;
-    steps.init<FMT>(a);
-    TileLoads<FMT, PK, B, 8, false> lp;
-    TileLoads<FMT, QK, B, 8, GATED> lq;
-    ScaleLoads ls[2];
-    lp.init(a.p, i0, a.I, a.p_ld, a.K, steps.first, steps.end, wave, lane);
-    lq.init(a.q, j0, JH, a.q_ld, a.K, steps.first, steps.end, wave, lane);
-    if constexpr (MX8) {
-        ls[0].init<false>(a.p_scales, i0, wave * 64, a.I, a.K, steps, lane);
-        ls[1].init<GATED>(a.q_scales, j0, wave * 64, JH, a.K, steps, lane);
-    }
-    const int wi = wave / 2 * 128, wj = wave % 2 * 128;
-    pr_f32x16 acc[4][4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[f][g][e] = 0.0f;
-    // the places where the next loads go, and of the step that is read
-    int p_to = 0, q_to = QAT, s_to = SAT, p_at = 0, q_at = QAT, s_at = SAT;
-    auto q_after = [](int q) { return q == QAT + (QS - 1) * TB ? QAT : q + TB; };
-    auto load_p = [&](int n) { lp.load(n, lds + p_to, wave, lane); };
-    auto load_q = [&](int n) { lq.load(n, lds + q_to, wave, lane); };
-    auto load_s = [&](int n) { ls[n].load(lds + s_to + n * 4 * B + wave * 256); };
-    auto p_next = [&] {
-        p_to ^= TB;
-        lp.walk.next();
-    };
-    auto q_next = [&] {
-        q_to = q_after(q_to);
-        lq.walk.next();
-    };
-    auto s_next = [&] {
-        s_to = s_to == SAT ? SAT + SB : SAT;
-        ls[0].next();
-        ls[1].next();
-    };
-    typename std::conditional<MX8, pr_i32x8, pr_bf16x8>::type p[2][4], q[2][4];
-    int ps[4], qs[4], ps_next[4], qs_next[4];
-    // fragment n of part j: Q's, then P's
-    auto read = [&](int j, int n) {
-        if constexpr (MX8) {
-            if (n < 4) q[j & 1][n] = fragment8_32(lds + q_at, wj, n, j, lane);
-            else p[j & 1][n - 4] = fragment8_32(lds + p_at, wi, n - 4, j, lane);
-        } else {
-            if (n < 4) q[j & 1][n] = fragment32<QK, B>(lds + q_at, wj, n, j, lane);
-            else p[j & 1][n - 4] = fragment32<PK, B>(lds + p_at, wi, n - 4, j, lane);
-        }
-    };
-    auto read_scales = [&](int f) {
-        ps_next[f] = scales32(lds + s_at, wi, f, lane);
-        qs_next[f] = scales32(lds + s_at + 4 * B, wj, f, lane);
-    };
-    auto multiply = [&](auto part, int n) {                  // products 2 n and 2 n + 1 of a part
-        constexpr int j = decltype(part)::value;
-#pragma unroll
-        for (int f = n % 2 * 2; f < n % 2 * 2 + 2; ++f) {
-            pr_f32x16& c = acc[n / 2][f];
-            if constexpr (MX8)
-                c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j & 1][f], p[j & 1][n / 2], c, 0, 0, 2 * j, qs[f], 2 * j, ps[n / 2]);
-            else c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j & 1][f], p[j & 1][n / 2], c, 0, 0, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    auto take_scales = [&] {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            ps[f] = ps_next[f];
-            qs[f] = qs_next[f];
-        }
-    };
-    auto load_all = [&](bool with_p, bool with_q) {
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            if (with_p) load_p(n);
-            if (with_q) load_q(n);
-        }
-        if (with_p) p_next();
-        if (with_q) q_next();
-    };
-    load_all(true, true);
-    if constexpr (MX8) {
-        load_s(0);
-        load_s(1);
-        s_next();
-        load_all(true, true);
-        load_s(0);
-        load_s(1);
-        s_next();
-        wait_vm<18>();
-    } else {
-        load_all(false, true);
-        load_all(true, false);
-        wait_vm<16>();
-    }
-    ring_barrier();
-#pragma unroll
-    for (int n = 0; n < 8; ++n) read(0, n);
-    if constexpr (MX8) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) read_scales(f);
-        take_scales();
-    }
-    for (int s = steps.first; s < steps.end; ++s) {
-        for_steps<0>([&](auto part) {
-            constexpr int j = decltype(part)::value;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                if (n < 4) {
-                    read(j + 1, 2 * n);
-                    read(j + 1, 2 * n + 1);
-                }
-                if (!MX8 && j == 0) load_q(n);
-                multiply(part, n);
-            }
-            if (!MX8 && j == 0) q_next();
-        }, std::make_integer_sequence<int, PARTS - 1>{});
-        wait_vm<MX8 ? 0 : 8>();
-        __builtin_amdgcn_sched_barrier(0);
-        ring_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        p_at ^= TB;
-        q_at = q_after(q_at);
-        s_at = s_at == SAT ? SAT + SB : SAT;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            if (n < 4) {
-                read(0, 2 * n);
-                read(0, 2 * n + 1);
-            }
-            load_p(n);
-            if constexpr (MX8) {
-                load_q(n);
-                if (n >= 4) read_scales(n - 4);
-                if (n >= 6) load_s(n - 6);
-            }
-            multiply(StepPos<PARTS - 1>{}, n);
-        }
-        p_next();
-        if constexpr (MX8) {
-            q_next();
-            s_next();
-            take_scales();
-        }
-    }
+// The sums of four waves' 128 x 128, acc[i][j] of 32 x 32, through LDS and the epilogue.
+template <bool GATED>
+__device__ __forceinline__ void write_large(const ProductArgs& a, uint8_t* lds, const pr_f32x16 (&acc)[4][4], int i0, int j0, int wave, int lane) {
     wait_vm<0>();                                            // no direct load is under way
     ring_barrier();
+    const int wi = wave / 2 * 128, wj = wave % 2 * 128;
     uint8_t* mine = lds + wave * 32768;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -649,6 +511,228 @@ __global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
             }
         write_rows<128, GATED>(a, mine, i0 + wi, GATED ? j0 + wj / 2 + 32 * c : j0 + wj + 64 * c, lane);
     }
+}
+__device__ __forceinline__ void clear(pr_f32x16 (&acc)[4][4]) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[f][g][e] = 0.0f;
+}
+
+// Tile of 256 x 256 for large bf16 products: four waves of 128 x 128, each alone on its SIMD.  A step is four parts of 16 k;
+// while the matrix cores work on one, the next one's fragments come from LDS, and the direct loads are handed out between
+// the products (a burst of them would hold the products up).  One barrier a step, before its last part: every wave has
+// the whole step in registers then, and the next one has landed.  P has two places in LDS, whose loads follow that
+// barrier; Q three, and its loads a step more to land.
+// 4096^3 112 us (1228 TFLOP/s; dx 116, dw 118), 8192^3 802 us (1370): the matrix cores are busy 81% of its cycles, at a
+// clock that falls to 1.6 GHz under the load.
+template <bool PK, bool QK, bool GATED>
+__global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
+    constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kStepBytes, QS = 3, QAT = 2 * TB;
+    __shared__ __align__(1024) uint8_t lds[QAT + QS * TB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int JH = GATED ? a.J / 2 : a.J;
+    int i0, j0;
+    tile_place(blockIdx.x, gridDim.x, (a.I + B - 1) / B, (JH + BH - 1) / BH, &i0, &j0);
+    i0 *= B;
+    j0 *= BH;
+    Steps steps;
+    steps.init<kBf16>(a);
+    TileLoads<kBf16, PK, B, 8, false> lp;
+    TileLoads<kBf16, QK, B, 8, GATED> lq;
+    lp.init(a.p, i0, a.I, a.p_ld, a.K, steps.first, steps.end, wave, lane);
+    lq.init(a.q, j0, JH, a.q_ld, a.K, steps.first, steps.end, wave, lane);
+    const int wi = wave / 2 * 128, wj = wave % 2 * 128;
+    pr_f32x16 acc[4][4];
+    clear(acc);
+    // the places where the next loads go, and of the step that is read
+    int p_to = 0, q_to = QAT, p_at = 0, q_at = QAT;
+    auto q_after = [](int q) { return q == QAT + (QS - 1) * TB ? QAT : q + TB; };
+    auto load_p = [&](int n) { lp.load(n, lds + p_to, wave, lane); };
+    auto load_q = [&](int n) { lq.load(n, lds + q_to, wave, lane); };
+    auto p_next = [&] {
+        p_to ^= TB;
+        lp.walk.next();
+    };
+    auto q_next = [&] {
+        q_to = q_after(q_to);
+        lq.walk.next();
+    };
+    pr_bf16x8 p[2][4], q[2][4];
+    // fragment n of part j: Q's, then P's
+    auto read = [&](int j, int n) {
+        if (n < 4) q[j & 1][n] = fragment32<QK, B>(lds + q_at, wj, n, j, lane);
+        else p[j & 1][n - 4] = fragment32<PK, B>(lds + p_at, wi, n - 4, j, lane);
+    };
+    auto multiply = [&](int j, int n) {                      // products 2 n and 2 n + 1 of a part
+#pragma unroll
+        for (int f = n % 2 * 2; f < n % 2 * 2 + 2; ++f)
+            acc[n / 2][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j & 1][f], p[j & 1][n / 2], acc[n / 2][f], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_all = [&](bool with_p, bool with_q) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            if (with_p) load_p(n);
+            if (with_q) load_q(n);
+        }
+        if (with_p) p_next();
+        if (with_q) q_next();
+    };
+    load_all(true, true);
+    load_all(false, true);
+    load_all(true, false);
+    wait_vm<16>();
+    ring_barrier();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) read(0, n);
+    for (int s = steps.first; s < steps.end; ++s) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                if (n < 4) {
+                    read(j + 1, 2 * n);
+                    read(j + 1, 2 * n + 1);
+                }
+                if (j == 0) load_q(n);
+                multiply(j, n);
+            }
+            if (j == 0) q_next();
+        }
+        wait_vm<8>();
+        __builtin_amdgcn_sched_barrier(0);
+        ring_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        p_at ^= TB;
+        q_at = q_after(q_at);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            if (n < 4) {
+                read(0, 2 * n);
+                read(0, 2 * n + 1);
+            }
+            load_p(n);
+            multiply(3, n);
+        }
+        p_next();
+    }
+    write_large<GATED>(a, lds, acc, i0, j0, wave, lane);
+}
+
+// The same tile of MXFP8, in half steps of 64 codes with four places in LDS.  While the matrix cores work on half step h,
+// fragments of h + 1 come from LDS and loads of h + 4 go to the place of h, which every wave has in registers; one barrier
+// at its end, by when h + 2 has landed: a load has two to three half steps for that.  Scales are loaded for four steps
+// at a time: each load of them touches a line for every row, and step by step the lines' way through L2 took as long as
+// the operands' (8192^3 600 us so, 534 now).
+// 4096 x 4096 x 8192 135 us (2032 TFLOP/s), 8192^3 534 (2060): what bounds it is still the vector L1, which takes a line of
+// scales a cycle, 512 for a step's 2048 of products; two whole steps in LDS, whose loads have half a step to land, 145.
+template <bool GATED>
+__global__ __launch_bounds__(256, 1) void k_product_large_mx8(ProductArgs a) {
+    constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kHalfBytes, STG = 2 * TB, SAT = 4 * STG, SB = 8 * B;
+    __shared__ __align__(1024) uint8_t lds[SAT + 8 * SB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int JH = GATED ? a.J / 2 : a.J;
+    int i0, j0;
+    tile_place(blockIdx.x, gridDim.x, (a.I + B - 1) / B, (JH + BH - 1) / BH, &i0, &j0);
+    i0 *= B;
+    j0 *= BH;
+    Steps steps;
+    steps.init<kMx8>(a);
+    HalfLoads<false> lp;
+    HalfLoads<GATED> lq;
+    ScaleLoads ls[2];
+    lp.init(a.p, i0, a.I, a.p_ld, 2 * steps.first, 2 * steps.end, wave, lane);
+    lq.init(a.q, j0, JH, a.q_ld, 2 * steps.first, 2 * steps.end, wave, lane);
+    ls[0].init<false>(a.p_scales, i0, wave * 64, a.I, a.K, steps, lane);
+    ls[1].init<GATED>(a.q_scales, j0, wave * 64, JH, a.K, steps, lane);
+    const int wi = wave / 2 * 128, wj = wave % 2 * 128;
+    pr_f32x16 acc[4][4];
+    clear(acc);
+    int to = 0, s_to = 0, at = 0, s_at = 0;              // the places of the next loads, and of the next reads
+    auto load = [&](int n) {
+        if (n < 4) lp.load(n, lds + to, wave);
+        else lq.load(n - 4, lds + to + TB, wave);
+    };
+    auto load_scales = [&] {                                 // of four steps
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) ls[n].load(lds + SAT + s_to + u * SB + n * 4 * B + wave * 256, u);
+            ls[n].next(4);
+        }
+        s_to ^= 4 * SB;
+    };
+    auto next = [&] {
+        to = (to + STG) & (4 * STG - 1);
+        lp.walk.next();
+        lq.walk.next();
+    };
+    pr_i32x8 p[2][4], q[2][4];
+    int ps[4], qs[4], ps_next[4], qs_next[4];
+    auto read = [&](int j, int n) {                          // fragment n of half j: Q's, then P's
+        if (n < 4) q[j][n] = fragment8_half(lds + at + TB, wj, n, lane);
+        else p[j][n - 4] = fragment8_half(lds + at, wi, n - 4, lane);
+    };
+    auto read_scales = [&](int f) {
+        ps_next[f] = scales32(lds + SAT + s_at, wi, f, lane);
+        qs_next[f] = scales32(lds + SAT + s_at + 4 * B, wj, f, lane);
+    };
+    auto take_scales = [&] {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            ps[f] = ps_next[f];
+            qs[f] = qs_next[f];
+        }
+        s_at = (s_at + SB) & (8 * SB - 1);
+    };
+    static_assert((4 * STG & (4 * STG - 1)) == 0 && (8 * SB & (8 * SB - 1)) == 0, "places by a mask");
+    load_scales();
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) load(n);
+        next();
+    }
+    wait_vm<16>();                                           // the first two half steps
+    ring_barrier();
+#pragma unroll
+    for (int n = 0; n < 8; ++n) read(0, n);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) read_scales(f);
+    take_scales();
+    at = STG;
+    ring_barrier();
+    for (int s = steps.first; s < steps.end; ++s) {
+        for_steps<0>([&](auto half) {
+            constexpr int j = decltype(half)::value;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                if (n < 4) {
+                    read(j ^ 1, 2 * n);
+                    read(j ^ 1, 2 * n + 1);
+                }
+                load(n);
+                if (j == 0 && n == 7 && (s - steps.first) % 4 == 0) load_scales();
+                if (j == 1 && n >= 4) read_scales(n - 4);
+#pragma unroll
+                for (int f = n % 2 * 2; f < n % 2 * 2 + 2; ++f) {
+                    pr_f32x16& c = acc[n / 2][f];
+                    c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(q[j][f], p[j][n / 2], c, 0, 0, 2 * j, qs[f], 2 * j, ps[n / 2]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            next();
+            at = (at + STG) & (4 * STG - 1);
+            if (j == 1) take_scales();
+            wait_vm<16>();                                   // at most this half step's loads and the one's before are under way
+            __builtin_amdgcn_sched_barrier(0);
+            ring_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        }, std::make_integer_sequence<int, 2>{});
+    }
+    write_large<GATED>(a, lds, acc, i0, j0, wave, lane);
 }
 
 // the parts' sums in order, then the epilogue; eight columns per thread (gated: of h).  Out of L2 and the last-level
@@ -737,7 +821,8 @@ static void product_launch(ProductArgs& a, hipStream_t st) {
                 product_launch_as<FMT, PK, QK, GATED, 256, 2, 4, 2>(a, st);
             } else {
                 const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 128 : 256, tiles = (a.I + 255) / 256 * ((JH + BH - 1) / BH);
-                MOE_LAUNCH((k_product_large<FMT, PK, QK, GATED>), dim3(tiles, a.splits), dim3(256), 0, st, a);
+                if constexpr (FMT == kMx8) MOE_LAUNCH((k_product_large_mx8<GATED>), dim3(tiles, a.splits), dim3(256), 0, st, a);
+                else MOE_LAUNCH((k_product_large<PK, QK, GATED>), dim3(tiles, a.splits), dim3(256), 0, st, a);
             }
     }
 }
