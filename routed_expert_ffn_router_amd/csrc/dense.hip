@@ -627,8 +627,8 @@ __global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
 // at its end, by when h + 2 has landed: a load has two to three half steps for that.  Scales are loaded for four steps
 // at a time: each load of them touches a line for every row, and step by step the lines' way through L2 took as long as
 // the operands' (8192^3 600 us so, 534 now).
-// 4096 x 4096 x 8192 135 us (2032 TFLOP/s), 8192^3 534 (2060): what bounds it is still the vector L1, which takes a line of
-// scales a cycle, 512 for a step's 2048 of products; two whole steps in LDS, whose loads have half a step to land, 145.
+// 4096 x 4096 x 8192 135 us (2032 TFLOP/s; two whole steps in LDS, whose loads have half a step to land, 145), 8192^3 534
+// (2060): the matrix cores are busy about half of it, and the scales' lines, one for each row, are the likely rest.
 template <bool GATED>
 __global__ __launch_bounds__(256, 1) void k_product_large_mx8(ProductArgs a) {
     constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kHalfBytes, STG = 2 * TB, SAT = 4 * STG, SB = 8 * B;
