@@ -432,7 +432,7 @@ moe_status moe_linear(const moe_matrix *matrix, const uint8_t *q, const uint8_t 
  *     of eight neighbouring codes to 2^-13 of the largest before they add them (7 * 2^-13 of sum |x| |W| at most,
  *     about 1.5e-5 of a result).  So the same token's result may differ in that between a short call and a long one.
  *   Sums are fp32; y, h, pre, dx and dw are rounded once to act_dtype.
- * Limits: rows a multiple of 8, cols of 8 (MXFP8: of 128), each at most 2^20, rows * cols at most 2^33,
+ * Limits: rows a multiple of 8, cols of 8 (MXFP8: of 32), each at most 2^20, rows * cols at most 2^33,
  * T <= 65536 (MOE_ERR_UNSUPPORTED beyond).  Pointers are 16-byte aligned (scales of operands: 4 bytes; of h: any).
  * Arrays are contiguous, and outputs alias neither inputs nor one another unless a call says so.
  *

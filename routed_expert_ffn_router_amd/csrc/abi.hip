@@ -355,13 +355,13 @@ static moe_status check_dense(const moe_dense* m, int32_t T) {
     if (m->activation < MOE_ACT_NONE || m->activation > MOE_ACT_SIGMOID) return MOE_ERR_INVALID;
     if (T > 65536 || m->rows > (1 << 20) || m->cols > (1 << 20) || (long long)m->rows * m->cols > (1LL << 33))
         return MOE_ERR_UNSUPPORTED;
-    if (m->rows % 8 != 0 || m->cols % (m->operands == MOE_OPERANDS_MXFP8 ? 128 : 8) != 0) return MOE_ERR_UNSUPPORTED;
+    if (m->rows % 8 != 0 || m->cols % (m->operands == MOE_OPERANDS_MXFP8 ? 32 : 8) != 0) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
 // regions of a call's workspace
 struct DenseLayout {
-    size_t d, xp, wp, bias, part, total;
+    size_t d, scales, xp, wp, bias, part, total;
 };
 static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool backward) {
     // MXFP8 operands of fp32 outputs are copied to bf16
@@ -371,6 +371,8 @@ static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool ba
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o += align256(bytes); return at; };
     L.d = take(backward ? t * R * (m->act_dtype == MOE_DT_F32 ? 4 : 2) : 0);
+    // rows of scales that end inside a step of the products are copied to whole ones
+    L.scales = take(m->operands == MOE_OPERANDS_MXFP8 && K % 128 != 0 ? (t + R) * scale_row(m->cols) : 0);
     L.xp = take(t * K * copies);
     L.wp = take(R * K * copies);
     L.bias = take(backward ? (size_t)kBiasChunks * m->rows * 4 : 0);
@@ -408,7 +410,14 @@ static moe_status run_forward(const moe_dense* m, const void* x, const uint8_t* 
     a.q_scales = w_scales;
     a.part = (float*)(ws + L.part);
     a.splits = 1;
-    if (product_few_ok(a, bytes)) return hip_status(launch_product_few(a, bytes, gated, st));
+    const bool few = product_few_ok(a, bytes);
+    if (mx8 && (few || !f32) && K % 128 != 0) {
+        uint8_t* padded = ws + L.scales;
+        MOE_HIP(launch_pad_scales(x_scales, T, w_scales, (int)R, m->cols, padded, st));
+        a.p_scales = padded;
+        a.q_scales = padded + (size_t)T * scale_row(m->cols);
+    }
+    if (few) return hip_status(launch_product_few(a, bytes, gated, st));
     if (f32 && mx8) {
         // the scaled matrix cores' sums are right to about 1.5e-5 of a result, bf16 ones to fp32
         uint16_t *xp = (uint16_t*)(ws + L.xp), *wp = (uint16_t*)(ws + L.wp);

@@ -6,13 +6,16 @@
 
 namespace moe {
 
+// bytes of a row of scales in the products of MXFP8: a step's four are read at once
+constexpr int scale_row(int K) { return (K + 127) / 128 * 4; }
+
 // One product out[i][j] = sum_k P[i][k] Q[j][k], i < I, j < J, with its epilogue.  P and Q are bf16, fp32 or MXFP8
 // codes; each is stored with k along its rows ([i][k]) or, "k-major", across them ([k][i]).
 struct ProductArgs {
     int I, J, K;
     const uint8_t *p, *q;
     int p_ld, q_ld;               // bytes of a stored row
-    const uint8_t *p_scales, *q_scales;   // MXFP8: [i][K/32], [j][K/32]
+    const uint8_t *p_scales, *q_scales;   // MXFP8: a byte for each 32 of k, rows of scale_row(K) bytes (past K/32: no NaN's)
     int splits;                   // parts of the sum over k; more than one: fp32 sums to part, [splits][I][J]
     float* part;
     // epilogue; the outputs' rows are J long (gated: N = J / 2)
@@ -154,6 +157,10 @@ hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor
 // Few rows of P, neither operand k-major
 bool product_few_ok(const ProductArgs& a, int bytes);
 hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st);
+
+// Rows of K/32 scale bytes to rows of scale_row(K), filled up with 2^0 (beside codes of zero): scales_p [I], then scales_q
+// [J], to `padded`.
+hipError_t launch_pad_scales(const uint8_t* scales_p, int I, const uint8_t* scales_q, int J, int K, uint8_t* padded, hipStream_t st);
 
 // MXFP8 [n] as bf16, which holds every code times its scale
 hipError_t launch_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, uint16_t* values, hipStream_t st);

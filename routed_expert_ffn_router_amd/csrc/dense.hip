@@ -194,7 +194,7 @@ struct ScaleLoads {
     // rows first + from + lane of a tile from `first` on (gated: rows from + lane of Q's tile)
     template <bool GATED>
     __device__ __forceinline__ void init(const uint8_t* scales, int first, int from, int rows, int K, const Steps& s, int lane) {
-        const int ld = K / 32, r = from + lane, row = GATED ? gated_row(r) : r;
+        const int ld = scale_row(K), r = from + lane, row = GATED ? gated_row(r) : r;
         off = first + row < rows ? (uint32_t)((row + (GATED && (r & 32) ? rows : 0)) * ld) : kNowhere;
         at = scales + (size_t)first * ld + 4 * (size_t)s.first;
         steps = s.end - s.first;
@@ -469,7 +469,7 @@ struct HalfLoads {
     uint32_t off[4];
     size_t upper;
     Walk walk;
-    // as TileLoads; rows are a multiple of 128 codes long, and [s, end) are half steps
+    // as TileLoads; [s, end) are half steps, the last of which may lie past the end of the sum
     __device__ __forceinline__ void init(const uint8_t* p, int first, int rows, int ld, int s, int end, int wave, int lane) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -479,8 +479,9 @@ struct HalfLoads {
         upper = (size_t)rows * ld;
         walk.init(p + (size_t)first * ld, kHalfBytes, ld, kHalfBytes, s, end);
     }
-    __device__ __forceinline__ void load(int n, uint8_t* lds, int wave) const {
-        load_lds16(GATED && (n & 2) ? walk.at + upper : walk.at, walk.here() > 0 ? off[n] : kNowhere, lds + (wave * 4 + n) * 1024);
+    __device__ __forceinline__ void load(int n, uint8_t* lds, int wave, int lane) const {
+        const int at = ((lane & 3) ^ half_key(lane >> 2)) * 16;      // (the key of 16 rows on is the same)
+        load_lds16(GATED && (n & 2) ? walk.at + upper : walk.at, at < walk.here() ? off[n] : kNowhere, lds + (wave * 4 + n) * 1024);
     }
 };
 // the row's four scale bytes, moved so that bytes 0 and 2 are those of the lane group's blocks
@@ -653,8 +654,8 @@ __global__ __launch_bounds__(256, 1) void k_product_large_mx8(ProductArgs a) {
     clear(acc);
     int to = 0, s_to = 0, at = 0, s_at = 0;              // the places of the next loads, and of the next reads
     auto load = [&](int n) {
-        if (n < 4) lp.load(n, lds + to, wave);
-        else lq.load(n - 4, lds + to + TB, wave);
+        if (n < 4) lp.load(n, lds + to, wave, lane);
+        else lq.load(n - 4, lds + to + TB, wave, lane);
     };
     auto load_scales = [&] {                                 // of four steps
 #pragma unroll
@@ -859,6 +860,31 @@ hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor
         else MOE_LAUNCH((k_product_finish<false>), grid, dim3(256), 0, st, a);
         trace("product_finish", 1, st);
     }
+    return hipGetLastError();
+}
+
+// Four bytes of a row per thread.  Direct loads to LDS take whole aligned words, which rows of K/32 bytes are not made of unless
+// K is a multiple of 128.  2.5 us of a call: 4096 x 4128, one token 10.4 us, 4096 x 4096 7.8.
+__global__ __launch_bounds__(256) void k_pad_scales(const uint8_t* __restrict__ scales_p, const uint8_t* __restrict__ scales_q, int I, int J,
+                                                    int blocks, uint32_t* __restrict__ padded) {
+    const int words = (blocks + 3) / 4;
+    const size_t all = (size_t)(I + J) * words;
+    for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (size_t)gridDim.x * 256) {
+        const int row = (int)(at / words), b = (int)(at % words) * 4;
+        const uint8_t* from = row < I ? scales_p + (size_t)row * blocks : scales_q + (size_t)(row - I) * blocks;
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w |= (uint32_t)(b + e < blocks ? from[b + e] : 127) << (8 * e);
+        padded[at] = w;
+    }
+}
+
+hipError_t launch_pad_scales(const uint8_t* scales_p, int I, const uint8_t* scales_q, int J, int K, uint8_t* padded, hipStream_t st) {
+    const size_t blocks = ((size_t)(I + J) * (scale_row(K) / 4) + 255) / 256;
+    trace("pad_scales", 0, st);
+    MOE_LAUNCH(k_pad_scales, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, st, scales_p, scales_q, I, J, K / 32,
+               (uint32_t*)padded);
+    trace("pad_scales", 1, st);
     return hipGetLastError();
 }
 

@@ -54,12 +54,12 @@ __global__ __launch_bounds__(64 * W) void k_product_few(ProductArgs a, int tiles
         if constexpr (MX8) {                                 // a row's four scale bytes, a row per lane
             const int q = GATED ? lane % (8 * F) : lane;
             qsoff = lt < tiles && lane < 16 * F && n0 + q < N
-                        ? (uint32_t)((size_t)(n0 + q + (GATED && lane >= 8 * F ? N : 0)) * (a.K / 32)) : kNowhere;
+                        ? (uint32_t)((size_t)(n0 + q + (GATED && lane >= 8 * F ? N : 0)) * scale_row(a.K)) : kNowhere;
         }
     };
 #pragma unroll
     for (int u = 0; u < 2 * C; ++u) poff[u] = u * 8 + r8 < a.I ? (uint32_t)((u * 8 + r8) * ld + at) : kNowhere;
-    if constexpr (MX8) psoff = lane < 16 * C && lane < a.I ? (uint32_t)(lane * (a.K / 32)) : kNowhere;
+    if constexpr (MX8) psoff = lane < 16 * C && lane < a.I ? (uint32_t)(lane * scale_row(a.K)) : kNowhere;
     new_tile();
     auto load = [&](uint8_t* st) {
         const size_t k = (size_t)ls * kStepBytes;
