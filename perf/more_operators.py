@@ -84,9 +84,7 @@ def draw(rng):
         return _norm(T, d, act, rng.choice(["none", "token", "element"]), rng.random() < 0.75)
     mx8 = op in ("matmul", "gated") and rng.random() < 0.4
     rows, cols = 32 * _log(rng, 1, 256), 32 * _log(rng, 1, 256)
-    if mx8:         # whole steps of 128 columns; rows that end inside a tile
-        cols = 128 * _log(rng, 1, 64)
-    else:           # rows and columns that end inside a tile
+    if not mx8:     # rows and columns that end inside a tile
         rows, cols = rows - 8 * rng.randint(0, 3), cols - 8 * rng.randint(0, 3)
     T = _log(rng, 1, 4096)
     most = _MOST[op] // (8 if act == "f32" and not mx8 else 1)
