@@ -6,7 +6,8 @@
 //
 // An fp32 value becomes three bf16 terms on its way from LDS to the matrix cores (8 + 8 + 8 bits of mantissa), and six
 // products of terms are summed in fp32; the three left out are below 2^-24 of the whole.  (The fp32 matrix instructions
-// have a sixteenth of bf16's rate: 4096^3 takes 602 us here, 228 TFLOP/s, where their peak is 157.)
+// have a sixteenth of bf16's rate: 4096^3 takes 602 us here, 228 TFLOP/s, where their peak is 157.)  An infinity has no
+// such terms: a tile with one is summed again by the fp32 matrix instructions.
 //
 // Roundings: sums and epilogues are fp32; y, pre, h and the gradients are rounded once.  The pre-activations' gradient is
 // rounded to the activations' type, so that its two products run at bf16's rate.  MXFP8 sums with bf16 outputs are the
@@ -347,74 +348,113 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
     j0 *= BH;
     Steps steps;
     steps.init<FMT>(a);
-    Loads loads;
-    loads.init(a, steps, i0, j0, wave, lane);
     const int wi = wave / WJ * (BI / WI), wj = wave % WJ * 64;
     pr_f32x4 acc[FI][4];
+    // The tile's sums; exact: fp32 values as they are, in fp32 matrix products.
+    auto sums = [&](auto exact) {
+        Loads loads;
+        loads.init(a, steps, i0, j0, wave, lane);
 #pragma unroll
-    for (int f = 0; f < FI; ++f)
+        for (int f = 0; f < FI; ++f)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) acc[f][g] = pr_f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int g = 0; g < 4; ++g) acc[f][g] = pr_f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) loads.load(ring + s * STG, wave, lane);
-    int at = 0;
-    for (int s = steps.first; s < steps.end; ++s) {
-        wait_vm<(ST - 2) * PER>();
-        ring_barrier();
-        loads.load(ring + (at == 0 ? ST - 1 : at - 1) * STG, wave, lane);
-        const uint8_t* st = ring + at * STG;
-        at = at + 1 == ST ? 0 : at + 1;
-        if constexpr (FMT == kMx8) {
-            pr_i32x8 p[FI], q[4];
-            int ps[(FI + 3) / 4];                            // (fewer fragments: the other bytes are not used)
-            const int qs = four_scales(st + PB + Loads::QB + 4 * BI, wj, lane);
+        for (int s = 0; s < ST - 1; ++s) loads.load(ring + s * STG, wave, lane);
+        int at = 0;
+        for (int s = steps.first; s < steps.end; ++s) {
+            wait_vm<(ST - 2) * PER>();
+            ring_barrier();
+            loads.load(ring + (at == 0 ? ST - 1 : at - 1) * STG, wave, lane);
+            const uint8_t* st = ring + at * STG;
+            at = at + 1 == ST ? 0 : at + 1;
+            if constexpr (FMT == kMx8) {
+                pr_i32x8 p[FI], q[4];
+                int ps[(FI + 3) / 4];                            // (fewer fragments: the other bytes are not used)
+                const int qs = four_scales(st + PB + Loads::QB + 4 * BI, wj, lane);
 #pragma unroll
-            for (int f = 0; f < (FI + 3) / 4; ++f) ps[f] = four_scales(st + PB + Loads::QB, wi + 64 * f, lane);
+                for (int f = 0; f < (FI + 3) / 4; ++f) ps[f] = four_scales(st + PB + Loads::QB, wi + 64 * f, lane);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) q[f] = fragment8(st + PB, wj, f, lane);
+                for (int f = 0; f < 4; ++f) q[f] = fragment8(st + PB, wj, f, lane);
 #pragma unroll
-            for (int f = 0; f < FI; ++f) p[f] = fragment8(st, wi, f, lane);
-            for_steps<0>([&](auto n) {
-                constexpr int fi = decltype(n)::value;
-                multiply_mx8<fi>(acc[fi], p[fi], q, ps[fi / 4], qs);
-            }, std::make_integer_sequence<int, FI>{});
-        } else if constexpr (FMT == kF32) {
-            Values pv[FI];
-            Terms q[4];
+                for (int f = 0; f < FI; ++f) p[f] = fragment8(st, wi, f, lane);
+                for_steps<0>([&](auto n) {
+                    constexpr int fi = decltype(n)::value;
+                    multiply_mx8<fi>(acc[fi], p[fi], q, ps[fi / 4], qs);
+                }, std::make_integer_sequence<int, FI>{});
+            } else if constexpr (decltype(exact)::value) {
+                Values q[4];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) q[f] = split_terms(fragment_f32<QK, BJ>(st + PB, wj, f, lane));
+                for (int f = 0; f < 4; ++f) q[f] = fragment_f32<QK, BJ>(st + PB, wj, f, lane);
 #pragma unroll
-            for (int fi = 0; fi < FI; ++fi) pv[fi] = fragment_f32<PK, BI>(st, wi, fi, lane);
-            Terms p = split_terms(pv[0]);
+                for (int fi = 0; fi < FI; ++fi) {
+                    const Values p = fragment_f32<PK, BI>(st, wi, fi, lane);
 #pragma unroll
-            for (int fi = 0; fi < FI; ++fi) {                // one fragment's products over the next one's terms
-                const Terms now = p;
-                if (fi + 1 < FI) p = split_terms(pv[fi + 1]);
-                multiply_f32(acc[fi], q, now);
+                    for (int e = 0; e < 8; ++e)
 #pragma unroll
-                for (int n = 0; n < 24; ++n) {
-                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+                        for (int f = 0; f < 4; ++f) acc[fi][f] = __builtin_amdgcn_mfma_f32_16x16x4f32(q[f].v[e], p.v[e], acc[fi][f], 0, 0, 0);
+                }
+            } else if constexpr (FMT == kF32) {
+                Values pv[FI];
+                Terms q[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) q[f] = split_terms(fragment_f32<QK, BJ>(st + PB, wj, f, lane));
+#pragma unroll
+                for (int fi = 0; fi < FI; ++fi) pv[fi] = fragment_f32<PK, BI>(st, wi, fi, lane);
+                Terms p = split_terms(pv[0]);
+#pragma unroll
+                for (int fi = 0; fi < FI; ++fi) {                // one fragment's products over the next one's terms
+                    const Terms now = p;
+                    if (fi + 1 < FI) p = split_terms(pv[fi + 1]);
+                    multiply_f32(acc[fi], q, now);
+#pragma unroll
+                    for (int n = 0; n < 24; ++n) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    pr_bf16x8 q[4], p[FI];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) q[f] = fragment<QK, BJ>(st + PB, wj, f, h, lane);
+#pragma unroll
+                    for (int fi = 0; fi < FI; ++fi) p[fi] = fragment<PK, BI>(st, wi, fi, h, lane);
+#pragma unroll
+                    for (int fi = 0; fi < FI; ++fi)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            acc[fi][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[f], p[fi], acc[fi][f], 0, 0, 0);
                 }
             }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                pr_bf16x8 q[4], p[FI];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) q[f] = fragment<QK, BJ>(st + PB, wj, f, h, lane);
-#pragma unroll
-                for (int fi = 0; fi < FI; ++fi) p[fi] = fragment<PK, BI>(st, wi, fi, h, lane);
-#pragma unroll
-                for (int fi = 0; fi < FI; ++fi)
-#pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        acc[fi][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[f], p[fi], acc[fi][f], 0, 0, 0);
-            }
         }
+        wait_vm<0>();                                        // no direct load is under way
+        ring_barrier();
+    };
+    sums(StepPos<0>{});
+    if constexpr (FMT == kF32) {
+        // A value without finite terms (an infinity, or one that bf16 rounds to it) leaves every sum that it enters infinite or
+        // NaN, and so does a sum past the type's end: then the tile's sums are taken again, of the values themselves.  (To look at
+        // the sums takes 0.2 us at 128 tokens, 1024 x 1024, and 3 of 601 at 4096^3.)
+        float none = 0.0f;
+#pragma unroll
+        for (int fi = 0; fi < FI; ++fi)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                mfma_results_here(acc[fi][f]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) none = fmaf(acc[fi][f][e], 0.0f, none);
+            }
+        uint32_t* bad = (uint32_t*)ring;
+        const bool mine_bad = __ballot(none != 0.0f) != 0;   // (a NaN is unequal to everything)
+        if (lane == 0) bad[wave] = mine_bad;
+        ring_barrier();
+        uint32_t any = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) any |= bad[w];
+        ring_barrier();
+        if (__builtin_amdgcn_readfirstlane((int)any)) sums(StepPos<1>{});
     }
-    wait_vm<0>();                                            // no direct load is under way
-    ring_barrier();
     constexpr int RF = FI > 4 ? 4 : FI;                      // 16 RF rows at a time
     static_assert(ST * STG >= W * RF * 4096, "the waves' sums fit into the ring");
     uint8_t* mine = ring + wave * RF * 4096;

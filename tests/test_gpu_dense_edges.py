@@ -1,4 +1,6 @@
 """The dense products on the GPU at the edges of their contract, against the plain float64 forms of dense_ref."""
+import math
+
 import pytest
 import torch
 
@@ -87,3 +89,66 @@ def test_mxfp8_blocks_replayed(T):
         m.moe_matmul(d, x, xs, T, w, ws, None, None, None, want, ws2)
         torch.cuda.synchronize()
         assert torch.equal(got, want), seed
+
+
+def _rows_alike(got, want, what):
+    """Infinite and NaN in the same places, with the same signs."""
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN"
+    assert torch.equal(got == math.inf, want == math.inf) and torch.equal(got == -math.inf, want == -math.inf), f"{what}: infinities"
+
+
+# one product of a row is left by the weight's columns that are zeros; the rest of the sum is of order one
+@pytest.mark.parametrize("T,N,K", [(40, 136, 200), (70, 136, 200), (300, 264, 72), (700, 1032, 2056), (3593, 3600, 136)])
+def test_fp32_infinities_and_the_largest_values(T, N, K):
+    """What an fp32 sum that an infinity or a value near the type's end enters is does not depend on the call's length."""
+    g = gen(650)
+    d, lowest = dense(N, K, F32), torch.finfo(F32).min
+    x, w = rand(g, T, K), rand(g, N, K)
+    x[3, 5], x[9, 7], x[12, 1], x[12, 2], x[20, 0], x[T - 1, K - 1] = math.inf, -math.inf, math.inf, -math.inf, lowest, math.inf
+    w[:, [0, 5, 7, 1, 2, K - 1]] = 0.0
+    w[N // 2:, [5, 7, 1, K - 1]] = w[N // 2:, [5, 7, 1, K - 1]] + 0.25   # zeros times an infinity below, numbers above
+    w[N // 2:, 2] = w[N // 2:, 1]
+    w[N // 2:, 0] = 2.0 ** -3
+    w[N - 1, 3] = -math.inf
+    y, ws = nan(T, N), scratch(d, T)
+    m.moe_matmul(d, x, None, T, w, None, None, None, None, y, ws)
+    # (in 64 bits the infinities are the same and the lowest value's products are no infinities)
+    want = torch.matmul(x.double().cpu(), w.double().cpu().t().contiguous()).cuda()
+    _rows_alike(y, want, "y")
+    rows = torch.ones(T, dtype=torch.bool, device="cuda")
+    rows[[3, 9, 12, T - 1]] = False
+    v = ref.matmul(x[rows].double(), w[:N - 1].double(), "f32", "none")[1]
+    check(y[rows][:, :N - 1], v, F32, "y")                     # the lowest value's row too
+
+
+@pytest.mark.parametrize("T,N,K", [(50, 72, 136), (300, 264, 328), (1500, 776, 640)])
+def test_fp32_infinities_in_gradients(T, N, K):
+    g = gen(660)
+    d = dense(N, K, F32)
+    x, w, dy = rand(g, T, K), rand(g, N, K), rand(g, T, N)
+    x[5, 8], dy[7, 3], w[2, 9] = math.inf, torch.finfo(F32).min, -math.inf
+    w[3], dy[5] = 2.0 ** -4, 0.0
+    dx, dw = nan(T, K), nan(N, K)
+    m.moe_matmul_backward(d, x, T, w, None, dy, dx, dw, None, scratch(d, T))
+    wx = torch.matmul(dy.double().cpu(), w.double().cpu()).cuda()
+    ww = torch.matmul(dy.double().cpu().t().contiguous(), x.double().cpu()).cuda()
+    _rows_alike(dx, wx, "dx")
+    x7 = x[7].double()
+    ww[3] = torch.where(x7.abs() * -torch.finfo(F32).min > torch.finfo(F32).max, -torch.sign(x7) * math.inf, ww[3])
+    ww[3, 8] = math.nan
+    _rows_alike(dw, ww, "dw")
+
+
+@pytest.mark.parametrize("T", [20, 48, 200])
+def test_fp32_gated_near_the_types_end(T):
+    N, K = 64, 136
+    g = gen(670)
+    x, w = rand(g, T, K), rand(g, 2 * N, K, std=0.1)
+    x[1, 4] = 3.4028e38
+    w[:N, 4], w[N:, 4] = 0.0, 2.0 ** -100
+    d, (codes, scales), h = dense(N, K, F32, "silu"), h8_outputs(T, N), nan(T, N)
+    v, want = ref.gated(x.double(), w.double(), "f32", "silu")
+    m.moe_gated(d, x, None, T, w, None, None, h, None, scratch(d, T))
+    check(h, want, F32, "h")
+    m.moe_gated(d, x, None, T, w, None, None, codes, scales, scratch(d, T))
+    ref.check_mx8(codes, scales, want, "h8")
