@@ -31,7 +31,19 @@ struct ProductArgs {
 // ---------------------------------------------------------------------------------------------
 // activations, in fp32
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ float logistic(float v) { return __builtin_amdgcn_rcpf(1.0f + expf(-v)); }
+// 1 / d for d of ordinary size, to a rounding: a bare reciprocal instruction is a unit off
+__device__ __forceinline__ float reciprocal(float d) {
+    const float r = __builtin_amdgcn_rcpf(d);
+    return fmaf(fmaf(-d, r, 1.0f), r, r);
+}
+// The logistic function of v and of -v, each right relative to itself: 1 - p has lost q where p is next to 1.
+struct Logistic {
+    float p, q;
+};
+__device__ __forceinline__ Logistic logistic(float v) {
+    const float e = expf(-fabsf(v)), large = reciprocal(1.0f + e), small = e * large;
+    return v < 0.0f ? Logistic{small, large} : Logistic{large, small};
+}
 // The normal distribution's function, and exp(-v^2 / 2).  The tail by Abramowitz and Stegun, Handbook of Mathematical
 // Functions, 7.1.26, off by at most 7.5e-8 (with the roundings 8 units of 2^-24
 // of 1); erff in its place took 40 of 150 us of a 4096^3 product.
@@ -39,8 +51,7 @@ struct Normal {
     float cdf, density;
 };
 __device__ __forceinline__ Normal normal(float v) {
-    const float d = fmaf(0.3275911f * 0.70710678118654752f, fminf(fabsf(v), 32.0f), 1.0f), t0 = __builtin_amdgcn_rcpf(d);
-    const float t = fmaf(fmaf(-d, t0, 1.0f), t0, t0);
+    const float t = reciprocal(fmaf(0.3275911f * 0.70710678118654752f, fminf(fabsf(v), 32.0f), 1.0f));
     const float e = __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);
     float p = fmaf(t, 1.061405429f, -1.453152027f);
     p = fmaf(t, p, 1.421413741f);
@@ -52,9 +63,9 @@ __device__ __forceinline__ Normal normal(float v) {
 
 template <int F>
 __device__ __forceinline__ float activate(float v) {
-    if constexpr (F == MOE_ACT_SILU) return v * logistic(v);
+    if constexpr (F == MOE_ACT_SILU) return v * logistic(v).p;
     if constexpr (F == MOE_ACT_GELU) return v * normal(v).cdf;
-    if constexpr (F == MOE_ACT_SIGMOID) return logistic(v);
+    if constexpr (F == MOE_ACT_SIGMOID) return logistic(v).p;
     return v;
 }
 __device__ __forceinline__ float activate(int f, float v) {
@@ -79,16 +90,16 @@ __device__ __forceinline__ void with_activation(int activation, Fn&& f) {
 __device__ __forceinline__ float slope(int f, float v) {
     switch (f) {
         case MOE_ACT_SILU: {
-            const float p = logistic(v);
-            return p * (1.0f + v * (1.0f - p));
+            const Logistic l = logistic(v);
+            return l.p * fmaf(v, l.q, 1.0f);
         }
         case MOE_ACT_GELU: {
             const Normal n = normal(v);
             return n.cdf + v * 0.39894228040143268f * n.density;
         }
         case MOE_ACT_SIGMOID: {
-            const float p = logistic(v);
-            return p * (1.0f - p);
+            const Logistic l = logistic(v);
+            return l.p * l.q;
         }
         default: return 1.0f;
     }

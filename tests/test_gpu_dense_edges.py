@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import dense_ref as ref
-from block_ref import check
+from block_ref import U, check
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +152,60 @@ def test_fp32_gated_near_the_types_end(T):
     check(h, want, F32, "h")
     m.moe_gated(d, x, None, T, w, None, None, codes, scales, scratch(d, T))
     ref.check_mx8(codes, scales, want, "h8")
+
+
+def points():
+    """Pre-activations of every size: dense around zero, out to where the functions leave the type's range."""
+    v = torch.cat([torch.linspace(-20, 20, 4001), torch.linspace(-110, 110, 551), 2.0 ** torch.linspace(-40, 6, 93), -2.0 ** torch.linspace(-40, 6, 93)])
+    return v[:v.numel() // 8 * 8].to(F32).cuda()
+
+
+def forward_at(v, fn, T=None):
+    """The activation of exact pre-activations, from a product with one value a row; with 8 or with T tokens a call."""
+    x, w, d = torch.zeros(v.numel(), 8, device="cuda"), torch.zeros(8, 8, device="cuda"), dense(8, 8, F32, fn)
+    x[:, 0], w[:, 0] = v, 1.0
+    y, T = nan(v.numel(), 8), T or v.numel()
+    for t in range(0, v.numel(), T):
+        n = min(T, v.numel() - t)
+        m.moe_matmul(d, x[t:t + n], None, n, w, None, None, None, None, y[t:t + n], scratch(d, n))
+    assert torch.equal(y, y[:, :1].expand(-1, 8))
+    return y[:, 0].double()
+
+
+def slope_at(v, fn):
+    """The activation's derivative as the bias gradient of one token, which is summed from nothing else."""
+    N, d_bias = v.numel(), nan(v.numel())
+    d = dense(N, 8, F32, fn)
+    m.moe_matmul_backward(d, None, 1, None, v, torch.ones(1, N, device="cuda"), None, None, d_bias, scratch(d, 1))
+    return d_bias.double()
+
+
+def within(got, want, bound, what):
+    off = (got - want).abs() - bound
+    k = off.argmax()
+    assert off.max() <= 0, f"{what}: {got[k]} for {want[k]}, bound {bound[k]}"
+
+
+def test_the_logistic_function_relative_to_itself():
+    """exp off by a unit (2 U), the sum, the reciprocal's rounding and one product: 6 U for either side, with what the sum
+    passes on; one more product with v for SiLU.  Its slope p (1 + v q) is taken against the sum of its parts' sizes: 12 U
+    with the product and sum of 1 and v q; the sigmoid's p q relative to itself, 13 U.  Below 2^-126 the steps are 2^-149."""
+    v = points()
+    x = v.double()
+    p, q = torch.sigmoid(x), torch.sigmoid(-x)
+    tiny = 2.0 ** -140
+    for T in (32, 600, None):
+        within(forward_at(v, "sigmoid", T), p, 6 * U * p + tiny, "sigmoid")
+        within(forward_at(v, "silu", T), x * p, 7 * U * (x * p).abs() + tiny, "silu")
+    within(slope_at(v, "sigmoid"), p * q, 13 * U * p * q + tiny, "sigmoid's slope")
+    within(slope_at(v, "silu"), p * (1 + x * q), 20 * U * p * (1 + x.abs() * q) + tiny, "SiLU's slope")
+
+
+def test_the_logistic_functions_gradient_of_large_pre_activations():
+    """bf16: a gradient that a rounding of its own is the only one of, half a step (2^-8)."""
+    v = torch.linspace(4, 80, 1024, device="cuda").to(BF16).reshape(128, 8)
+    d, dx = dense(8, 8, BF16, "sigmoid"), nan(128, 8, dtype=BF16)
+    m.moe_matmul_backward(d, None, 128, torch.eye(8, dtype=BF16, device="cuda"), v, torch.ones(128, 8, dtype=BF16, device="cuda"), dx, None, None,
+                          scratch(d, 128))
+    want = torch.sigmoid(v.double()) * torch.sigmoid(-v.double())
+    within(dx.double().flatten(), want.flatten(), (2.0 ** -8 * want * (1 + 2.0 ** -8)).flatten(), "dx")
