@@ -209,3 +209,33 @@ def test_the_logistic_functions_gradient_of_large_pre_activations():
                           scratch(d, 128))
     want = torch.sigmoid(v.double()) * torch.sigmoid(-v.double())
     within(dx.double().flatten(), want.flatten(), (2.0 ** -8 * want * (1 + 2.0 ** -8)).flatten(), "dx")
+
+
+def normal_cdf(x):
+    """Relative to itself in the tail too (ndtr comes in steps of 2^-54 there)."""
+    return 0.5 * torch.special.erfc(-x * math.sqrt(0.5))
+
+
+def test_gelu_relative_to_itself():
+    """The tail of the distribution function: 0.5 U of the approximation, nine steps of its polynomial that lose up to
+    a third of their sizes' sum (1.3) as R falls to 0.03 (33 U in a replay of every step), and the exponential, a unit of its
+    instruction (2 U) and three roundings: 40 U.  The function itself: the tail is at most a half, 1.2 U in that
+    replay, a unit of each instruction and the rounding of 1 - tail: 3 U.  Its slope adds v times the density (the
+    exponential's 5 U, two products, 8 U).  Below 2^-126 the exponential's instruction gives zero."""
+    v = points()
+    x = v.double()
+    cdf, density = normal_cdf(x), torch.exp(-0.5 * x * x) / math.sqrt(2 * math.pi)
+    off = U * torch.minimum(40 * cdf, torch.full_like(cdf, 3.0))
+    tiny = 2.0 ** -125 * (1 + x.abs())
+    for T in (32, 600, None):
+        within(forward_at(v, "gelu", T), x * cdf, x.abs() * off + 2 * U * (x * cdf).abs() + tiny, "gelu")
+    within(slope_at(v, "gelu"), cdf + x * density, off + 8 * U * x.abs() * density + 2 * U * (cdf + x * density).abs() + tiny, "its slope")
+
+
+def test_gelu_in_bf16_is_rounded_once():
+    v = -torch.linspace(0.01, 13, 4096, device="cuda").to(BF16)
+    x, w, d, y = torch.zeros(4096, 8, dtype=BF16, device="cuda"), torch.zeros(8, 8, dtype=BF16, device="cuda"), dense(8, 8, BF16, "gelu"), nan(4096, 8, dtype=BF16)
+    x[:, 0], w[:, 0] = v, 1.0
+    m.moe_matmul(d, x, None, 4096, w, None, None, None, None, y, scratch(d, 4096))
+    want = v.double() * normal_cdf(v.double())
+    within(y[:, 0].double(), want, 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8) + 2.0 ** -120, "y")
