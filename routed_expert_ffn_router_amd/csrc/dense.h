@@ -46,9 +46,9 @@ __device__ __forceinline__ Logistic logistic(float v) {
 }
 // The normal distribution's function, and exp(-v^2 / 2).  With x = |v|, Phi(-x) = exp(-x^2 / 2) R(x): R = 1/2 + u S(u) with
 // u = x / (x + 9/4), S the polynomial of degree 8 whose largest relative error of R over 0 .. 13.4 is least (half of 2^-24; a
-// fit to the scaled complementary error function by reweighted least squares).  Past 13.2 the exponential is zero.  Its argument is
-// carried in two parts, since a rounding of x^2 / 2 = 80 is one of 80 units of the result.  Evaluated in fp32 Phi(-x) is right to
-// 33 * 2^-24 of itself and Phi to 1.7 * 2^-24.  4096^3 with bias and residual: 148.5 us; 145 with a
+// fit to the scaled complementary error function by reweighted least squares).  Past 13.2 the exponential is zero.  Its
+// argument is carried in two parts, since a rounding of x^2 / 2 = 80 is one of 80 units of the result.  Evaluated in fp32
+// Phi(-x) is right to 33 * 2^-24 of itself and Phi to 1.7 * 2^-24.  4096^3 with bias and residual: 148.7 us; 145 with a
 // formula that is right to 8 * 2^-24 of 1 only.
 struct Normal {
     float cdf, density;
@@ -174,7 +174,8 @@ size_t product_part_bytes(size_t I, size_t J);
 // holds the gate's rows, then the up projection's.  Chooses a.splits, given a.part with product_part_bytes(I, J) bytes.
 hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st);
 
-// Few rows of P, neither operand k-major
+// Few rows of P, neither operand k-major: up to kFewTokens every product, up to 64 by rule
+constexpr int kFewTokens = 32;
 bool product_few_ok(const ProductArgs& a, int bytes);
 hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st);
 

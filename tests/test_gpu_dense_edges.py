@@ -239,3 +239,24 @@ def test_gelu_in_bf16_is_rounded_once():
     m.moe_matmul(d, x, None, 4096, w, None, None, None, None, y, scratch(d, 4096))
     want = v.double() * normal_cdf(v.double())
     within(y[:, 0].double(), want, 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8) + 2.0 ** -120, "y")
+
+
+@pytest.mark.parametrize("T,h8", [(32, 1), (33, 1), (64, 0), (65, 0)])
+def test_fp32_bits_below_bf16s_smallest(T, h8):
+    """Values enter as they are up to 32 tokens with h in MXFP8 and up to 64 without; beyond, bits below 2^-133 are left out."""
+    g = gen(680)
+    N, K = 64, 136
+    x, w = torch.zeros(T, K, device="cuda"), rand(g, 2 * N, K)
+    x[:, 0] = 3 * 2.0 ** -134
+    w[:N] = 0.0
+    w[:N, 1], x[:, 1], w[N:, 0], w[N:, 1] = 1.0, 1.0, 2.0 ** 100, 0.0    # gate 1, up 3 * 2^-34
+    d = dense(N, K, F32, "none")
+    if h8:
+        codes, scales = h8_outputs(T, N)
+        m.moe_gated(d, x, None, T, w, None, None, codes, scales, scratch(d, T))
+        h = ref.values(codes, scales)
+    else:
+        h = nan(T, N)
+        m.moe_gated(d, x, None, T, w, None, None, h, None, scratch(d, T))
+    as_they_are = T <= (32 if h8 else 64)
+    assert ((h.double() - 3 * 2.0 ** -34).abs() <= (0 if as_they_are else 2.0 ** -34)).all()
