@@ -364,22 +364,23 @@ struct DenseLayout {
     size_t d, scales, xp, wp, bias, part, total;
 };
 static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool backward) {
-    // MXFP8 operands of fp32 outputs are copied to bf16
-    const size_t copies = m->act_dtype == MOE_DT_F32 && m->operands == MOE_OPERANDS_MXFP8 ? 2 : 0;
+    // MXFP8 operands of fp32 outputs are copied to bf16, except for few tokens, whose products have no parts either
+    const bool mx8 = m->operands == MOE_OPERANDS_MXFP8, few = mx8 && T <= kFewTokens;
+    const size_t copies = mx8 && m->act_dtype == MOE_DT_F32 && !few ? 2 : 0;
     const size_t K = m->cols, t = T;
     DenseLayout L;
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o += align256(bytes); return at; };
     L.d = take(backward ? t * R * (m->act_dtype == MOE_DT_F32 ? 4 : 2) : 0);
     // rows of scales that end inside a step of the products are copied to whole ones
-    L.scales = take(m->operands == MOE_OPERANDS_MXFP8 && K % 128 != 0 ? (t + R) * scale_row(m->cols) : 0);
+    L.scales = take(mx8 && K % 128 != 0 ? (t + R) * scale_row(m->cols) : 0);
     L.xp = take(t * K * copies);
     L.wp = take(R * K * copies);
     L.bias = take(backward ? (size_t)kBiasChunks * m->rows * 4 : 0);
     size_t part = product_part_bytes(backward ? R : t, backward ? K : R);
     if (backward && product_part_bytes(t, K) > part) part = product_part_bytes(t, K);
-    L.part = take(part);
-    L.total = o;
+    L.part = take(few ? 0 : part);
+    L.total = o > 256 ? o : 256;
     return L;
 }
 

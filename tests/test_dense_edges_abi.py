@@ -4,7 +4,7 @@ import pytest
 
 m = pytest.importorskip("routed_expert_ffn_router_amd")
 
-from test_dense_abi import INV, OK, P, UNS, W, WSC, X, XS, Y, gated, matmul
+from test_dense_abi import INV, OK, P, UNS, W, WSC, WSP, X, XS, Y, gated, matmul
 
 
 @pytest.mark.parametrize("f", [matmul, gated])
@@ -32,3 +32,17 @@ def test_a_workspace_of_blocks_serves_every_call_with_fewer_tokens(N, K, act):
     d = m.make_dense(N, K, act, m.MOE_OPERANDS_MXFP8)
     sizes = [m.moe_dense_workspace_bytes(d, T) for T in [*range(600), *range(4000, 4100), 65535, 65536]]
     assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_few_tokens_bring_no_room_for_copies(act):
+    """A decoded token's MXFP8 products read their operands where they are: a workspace of the scales' copies at most."""
+    for N, K in ((8192, 4096), (8192, 4128)):
+        d = m.make_dense(N, K, act, m.MOE_OPERANDS_MXFP8)
+        scales = 0 if K % 128 == 0 else (2 * N + 32) * (K + 127) // 128 * 4
+        for T in (1, 32):
+            assert 0 < m.moe_dense_workspace_bytes(d, T) <= scales + 1024
+        assert m.moe_dense_workspace_bytes(d, 33) > 1 << 20
+        for f in (matmul, gated):
+            size = m.moe_dense_workspace_bytes(d, 1)
+            assert f(N=N, K=K, act=act, ops=1, xs=XS, ws=WSC, T=33, n=size) == WSP
