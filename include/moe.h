@@ -434,7 +434,8 @@ moe_status moe_linear(const moe_matrix *matrix, const uint8_t *q, const uint8_t 
  *   Sums are fp32; y, h, pre, dx and dw are rounded once to act_dtype.
  * Limits: rows a multiple of 8, cols of 8 (MXFP8: of 32), each at most 2^20, rows * cols at most 2^33,
  * T <= 65536 (MOE_ERR_UNSUPPORTED beyond).  Pointers are 16-byte aligned (scales of operands: 4 bytes; of h: any).
- * Arrays are contiguous, and outputs alias neither inputs nor one another unless a call says so.
+ * Arrays are contiguous, and outputs and ws overlap neither inputs nor one another unless a call says so
+ * (MOE_ERR_INVALID).
  *
  * ws: a workspace of moe_dense_workspace_bytes(dense, T) bytes, 256-byte aligned, for the calls below with that
  * description (any activation) and at most T tokens.  It needs no preparation, and nothing in it outlives a call;

@@ -359,6 +359,10 @@ static moe_status check_dense(const moe_dense* m, int32_t T) {
     return MOE_OK;
 }
 
+// bytes of a value of the activations, and of the forward products' operands
+static size_t act_bytes(const moe_dense* m) { return m->act_dtype == MOE_DT_F32 ? 4 : 2; }
+static size_t operand_bytes(const moe_dense* m) { return m->operands == MOE_OPERANDS_MXFP8 ? 1 : act_bytes(m); }
+
 // regions of a call's workspace
 struct DenseLayout {
     size_t d, scales, xp, wp, bias, part, total;
@@ -371,7 +375,7 @@ static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool ba
     DenseLayout L;
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o += align256(bytes); return at; };
-    L.d = take(backward ? t * R * (m->act_dtype == MOE_DT_F32 ? 4 : 2) : 0);
+    L.d = take(backward ? t * R * act_bytes(m) : 0);
     // rows of scales that end inside a step of the products are copied to whole ones
     L.scales = take(mx8 && K % 128 != 0 ? (t + R) * scale_row(m->cols) : 0);
     L.xp = take(t * K * copies);
@@ -461,14 +465,22 @@ static bool all_aligned(std::initializer_list<const void*> ps, size_t to) {
         if (p && !aligned(p, to)) return false;
     return true;
 }
-// no output in the place of an input or of another output
-static bool apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+// an argument's bytes
+struct Span {
+    const void* at;
+    size_t bytes;
+};
+static bool meet(const Span& a, const Span& b) {
+    const uintptr_t p = (uintptr_t)a.at, q = (uintptr_t)b.at;
+    return p && q && (p == q || (p < q + b.bytes && q < p + a.bytes));
+}
+// no output over an input or another output
+static bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
     for (auto o = outs.begin(); o != outs.end(); ++o) {
-        if (!*o) continue;
         for (auto q = outs.begin(); q != o; ++q)
-            if (*q == *o) return false;
-        for (const void* i : ins)
-            if (i == *o) return false;
+            if (meet(*q, *o)) return false;
+        for (const Span& i : ins)
+            if (meet(i, *o)) return false;
     }
     return true;
 }
@@ -677,7 +689,9 @@ moe_status moe_block_norm_mx8(const moe_shape* s, const void* x, const void* y, 
     if (!x || !codes || !scales || (!y && (post_gamma || gate))) return MOE_ERR_INVALID;
     const void* element = gate_kind == MOE_GATE_ELEMENT ? gate : nullptr;
     if (!all_aligned({x, y, x_out, codes, post_gamma, pre_gamma, element}, 16)) return MOE_ERR_INVALID;
-    if (!apart({codes, scales}, {x, y, x_out, gate, post_gamma, pre_gamma})) return MOE_ERR_INVALID;
+    const size_t d = s->d_model, n = T * d, rows = n * (s->act_dtype == MOE_DT_F32 ? 4 : 2);
+    if (!apart({{codes, n}, {scales, n / 32}}, {{x, rows}, {y, rows}, {x_out, rows}, {gate, element ? rows : 4 * (size_t)T},
+                                                {post_gamma, 4 * d}, {pre_gamma, 4 * d}})) return MOE_ERR_INVALID;
     return hip_status(launch_block_norm(s, a, stream));
 }
 
@@ -780,9 +794,12 @@ moe_status moe_matmul(const moe_dense* m, const void* x, const uint8_t* x_scales
     if (T == 0) return MOE_OK;
     MOE_TRY(check_operands(m, x, x_scales, w, w_scales));
     if (!y || !ws || !all_aligned({bias, residual, pre, y}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
-    if (!apart({y, pre}, {x, x_scales, w, w_scales, bias}) || (pre && pre == residual)) return MOE_ERR_INVALID;
     const DenseLayout L = dense_layout(m, T, m->rows, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    const size_t R = m->rows, rows = T * R * act_bytes(m), x_bytes = (size_t)T * m->cols * operand_bytes(m), w_bytes = R * m->cols * operand_bytes(m);
+    const Span kept = {residual == y ? nullptr : residual, rows};
+    if (!apart({{y, rows}, {pre, rows}, {ws, L.total}}, {{x, x_bytes}, {x_scales, x_bytes / 32}, {w, w_bytes}, {w_scales, w_bytes / 32},
+                                                         {bias, 4 * R}, kept})) return MOE_ERR_INVALID;
     ProductArgs a = product_args(m, T, m->rows, m->cols, y);
     a.bias = bias;
     a.residual = residual;
@@ -798,10 +815,12 @@ moe_status moe_gated(const moe_dense* m, const void* x, const uint8_t* x_scales,
     if (T == 0) return MOE_OK;
     MOE_TRY(check_operands(m, x, x_scales, w, w_scales));
     if (!h || !ws || !all_aligned({pre, h}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
-    if (!apart({h, h_scales, pre}, {x, x_scales, w, w_scales})) return MOE_ERR_INVALID;
     const size_t R = 2 * (size_t)m->rows;
     const DenseLayout L = dense_layout(m, T, R, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    const size_t n = (size_t)T * m->rows, x_bytes = (size_t)T * m->cols * operand_bytes(m), w_bytes = R * m->cols * operand_bytes(m);
+    if (!apart({{h, h_scales ? n : n * act_bytes(m)}, {h_scales, n / 32}, {pre, 2 * n * act_bytes(m)}, {ws, L.total}},
+               {{x, x_bytes}, {x_scales, x_bytes / 32}, {w, w_bytes}, {w_scales, w_bytes / 32}})) return MOE_ERR_INVALID;
     ProductArgs a = product_args(m, T, (int)R, m->cols, h);
     a.pre = pre;
     a.out_scales = h_scales;
@@ -815,9 +834,12 @@ static moe_status dense_backward(const moe_dense* m, const void* x, int32_t T, c
     MOE_TRY(check_dense(m, T));
     if (m->operands != MOE_OPERANDS_ACT) return MOE_ERR_UNSUPPORTED;
     const bool f32 = m->act_dtype == MOE_DT_F32, wants_pre = gated || m->activation != MOE_ACT_NONE;
-    const size_t R = (size_t)m->rows * (gated ? 2 : 1);
-    // written whatever T is
-    if (!all_aligned({dw, d_bias}, 16) || !apart({dx, dw, d_bias}, {x, w, pre, dy})) return MOE_ERR_INVALID;
+    const size_t R = (size_t)m->rows * (gated ? 2 : 1), es = act_bytes(m), x_bytes = T * es * m->cols, w_bytes = R * es * m->cols;
+    const DenseLayout L = dense_layout(m, T, R, true);
+    // dw and d_bias are written whatever T is, the workspace with any tokens
+    if (!all_aligned({dw, d_bias}, 16)) return MOE_ERR_INVALID;
+    if (!apart({{dx, x_bytes}, {dw, w_bytes}, {d_bias, 4 * (size_t)m->rows}, {T > 0 ? ws : nullptr, L.total}},
+               {{x, x_bytes}, {w, w_bytes}, {pre, T * es * R}, {dy, T * es * m->rows}})) return MOE_ERR_INVALID;
     if (T == 0) {
         if (dw) MOE_HIP(launch_ws_init((uint32_t*)dw, R * m->cols * (f32 ? 4 : 2) / 4, 0, stream));
         if (d_bias) MOE_HIP(launch_ws_init((uint32_t*)d_bias, m->rows, 0, stream));
@@ -825,7 +847,6 @@ static moe_status dense_backward(const moe_dense* m, const void* x, int32_t T, c
     }
     if (!dy || !ws || (!dx && !dw && !d_bias) || (dx && !w) || (dw && !x) || wants_pre != (pre != nullptr)) return MOE_ERR_INVALID;
     if (!all_aligned({x, w, pre, dy, dx}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
-    const DenseLayout L = dense_layout(m, T, R, true);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     uint8_t* w8 = (uint8_t*)ws;
     const bool as_is = !wants_pre;               // dy itself is the pre-activations' gradient
