@@ -182,6 +182,15 @@ def _torch_core():
     return _torch_c
 
 
+def _forget_torch_core():
+    global _torch_c
+    _torch_c = None
+
+
+# a forked child has no GPU: its first call asks torch, which says so
+os.register_at_fork(after_in_child=_forget_torch_core)
+
+
 def _current_device() -> int:
     return (_torch_c or _torch_core())._cuda_getDevice()
 

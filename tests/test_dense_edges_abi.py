@@ -1,6 +1,7 @@
 """What the dense products accept and refuse at the edges of their contract, on the host (fake device pointers that are
 never dereferenced: every accepted call has no tokens)."""
 import ctypes
+import os
 
 import pytest
 
@@ -83,3 +84,16 @@ def test_norm_outputs_that_meet_an_operand_half_way():
     for bad in ({"c": X + 16}, {"c": Y - 496}, {"c": P + 1008}, {"s": X + 1}, {"s": W + 511}, {"s": P + 3}, {"c": B + 1008}, {"s": R + 4},
                 {"kind": 2, "gate": W + 16}, {"kind": 1, "gate": W + 508}):
         assert f(**bad) == INV, bad
+
+
+def test_a_forked_child_asks_torch_for_the_gpu_again():
+    """torch refuses a GPU that was initialised before a fork; the binding keeps nothing that passes its check by."""
+    kept, m._torch_c = m._torch_c, object()                     # as after a first call
+    try:
+        child = os.fork()
+        if child == 0:
+            os._exit(0 if m._torch_c is None else 1)
+        assert os.waitstatus_to_exitcode(os.waitpid(child, 0)[1]) == 0
+        assert m._torch_c is not None
+    finally:
+        m._torch_c = kept
