@@ -25,7 +25,7 @@ constexpr int kSize = kStepBytes / kStep<FMT>;
 
 // Direct loads to LDS: 16 (4) bytes per lane from base + off, lane l's to lds + 16 l (4 l); an offset past the descriptor's
 // end brings zeros.  In assembly, because the compiler has every transposing read of LDS wait for all direct loads that
-// it knows of; they have no result in registers, and are waited for by count (wait_vm).  (Nothing else here uses m0.)
+// it knows of; they have no result in registers, and are waited for by count (wait_vm).
 __device__ __forceinline__ pr_u32x4 load_rsrc(const uint8_t* base) {
     const uint64_t p = (uint64_t)base;                       // the same in every lane
     return pr_u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
@@ -33,11 +33,11 @@ __device__ __forceinline__ pr_u32x4 load_rsrc(const uint8_t* base) {
 }
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint8_t* lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
-                 "v"(off), "s"(load_rsrc(base)) : "memory");
+                 "v"(off), "s"(load_rsrc(base)) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t off, uint8_t* lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
-                 "v"(off), "s"(load_rsrc(base)) : "memory");
+                 "v"(off), "s"(load_rsrc(base)) : "memory", "m0");
 }
 
 // Place of a row's 16-byte chunk in LDS: chunk ^ key(row).  Eight lanes, on eight rows, are served at once, from 32 banks.
