@@ -381,8 +381,8 @@ static DenseLayout dense_layout(const moe_dense* m, int32_t T, size_t R, bool ba
     L.xp = take(t * K * copies);
     L.wp = take(R * K * copies);
     L.bias = take(backward ? (size_t)kBiasChunks * m->rows * 4 : 0);
-    size_t part = product_part_bytes(backward ? R : t, backward ? K : R);
-    if (backward && product_part_bytes(t, K) > part) part = product_part_bytes(t, K);
+    size_t part = part_bytes(backward ? R : t, backward ? K : R);
+    if (backward && part_bytes(t, K) > part) part = part_bytes(t, K);
     L.part = take(few ? 0 : part);
     L.total = o > 256 ? o : 256;
     return L;
@@ -415,7 +415,7 @@ static moe_status run_forward(const moe_dense* m, const void* x, const uint8_t* 
     a.q_scales = w_scales;
     a.part = (float*)(ws + L.part);
     a.splits = 1;
-    const bool few = product_few_ok(a, bytes);
+    const bool few = few_rows(a.I, a.J, mx8 ? kMx8 : f32 ? kF32 : kBf16, a.out_scales);
     if (mx8 && (few || !f32) && K % 128 != 0) {
         uint8_t* padded = ws + L.scales;
         MOE_HIP(launch_pad_scales(x_scales, T, w_scales, (int)R, m->cols, padded, st));

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "block_ops.h"
+#include "dense_rule.h"
 
 namespace moe {
 
@@ -168,15 +169,11 @@ __device__ __forceinline__ void gated_out8(const ProductArgs& a, int i, int n, b
 // ---------------------------------------------------------------------------------------------
 // launchers; all return hipGetLastError() of their launches
 // ---------------------------------------------------------------------------------------------
-// bytes for the partial sums of any product of up to I rows and J columns
-size_t product_part_bytes(size_t I, size_t J);
 // bytes: of an operand's value (2 bf16, 4 fp32, 1 MXFP8); p_kmajor, q_kmajor: stored [k][i], [k][j] (not MXFP8); gated: Q
-// holds the gate's rows, then the up projection's.  Chooses a.splits, given a.part with product_part_bytes(I, J) bytes.
+// holds the gate's rows, then the up projection's.  Chooses a.splits, given a.part with part_bytes(I, J) bytes.
 hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor, bool gated, hipStream_t st);
 
-// Few rows of P, neither operand k-major: up to kFewTokens every product, up to 64 by rule
-constexpr int kFewTokens = 32;
-bool product_few_ok(const ProductArgs& a, int bytes);
+// few_rows(...) of P, neither operand k-major
 hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st);
 
 // Rows of K/32 scale bytes to rows of scale_row(K), filled up with 2^0 (beside codes of zero): scales_p [I], then scales_q

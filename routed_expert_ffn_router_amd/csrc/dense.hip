@@ -802,49 +802,6 @@ __global__ __launch_bounds__(256) void k_product_finish(ProductArgs a) {
     });
 }
 
-constexpr size_t kPartBytes = (size_t)64 << 20;
-constexpr int kMostSplits = 16;
-size_t product_part_bytes(size_t I, size_t J) {
-    const size_t all = kMostSplits * I * J * 4;
-    return all < kPartBytes ? all : kPartBytes;
-}
-
-// Which tile, and how many parts of the sum: the least time by a model of each tile's own measurements.  A workgroup takes
-// `start` and `step` for each 128 bytes of k, `step2` where two share a CU; parts cost a second kernel, that adds them.
-// us, model and measured (bf16): 256 tokens, 4096 x 4096 64 x 128 in two parts 21, 21.6 (128 x 256 26); 1024 tokens 64 x 128
-// 42, 42.0 (128 x 256 48); 2048 tokens 128 x 256 64, 64.1 (64 x 128 80); 4096 tokens 256 x 256 106, 110 (128 x 256 125);
-// 512 tokens, 1024 x 1024 64 x 64 9.4, 9.3 (64 x 128 9.8).
-struct TileChoice {
-    int bi, bj, per_cu;
-    float start, step, step2;
-};
-static const TileChoice kTiles[] = {
-    {64, 64, 2, 5.4f, 0.25f, 0.42f}, {64, 128, 2, 5.7f, 0.32f, 0.57f}, {128, 256, 1, 5.2f, 0.92f, 0.92f}, {256, 256, 1, 6.2f, 1.55f, 1.55f}};
-
-static int choose_tile(ProductArgs& a, int per_step, float slower) {
-    const int steps = (a.K + per_step - 1) / per_step;
-    float least = 0.0f;
-    int best = -1;
-    for (int t = 0; t < 4; ++t) {
-        const TileChoice& c = kTiles[t];
-        const long long tiles = (long long)((a.I + c.bi - 1) / c.bi) * ((a.J + c.bj - 1) / c.bj);
-        for (int splits = 1; splits <= kMostSplits; ++splits) {
-            const size_t part = (size_t)splits * a.I * a.J * 4;
-            if (splits > 1 && (splits * 4 > steps || part > product_part_bytes(a.I, a.J) || tiles * splits > 256 * c.per_cu)) break;
-            const long long groups = tiles * splits, rounds = (groups + 256 * c.per_cu - 1) / (256 * c.per_cu);
-            const float step = (groups <= 256 ? c.step : c.step2) * slower;
-            float us = rounds * (steps / (float)splits) * step + c.start * (rounds < 2 ? 1.0f : 0.5f + 0.5f * rounds);
-            if (splits > 1) us += 4.0f + part * 1.5e-7f;
-            if (best < 0 || us < least) {
-                least = us;
-                best = t;
-                a.splits = splits;
-            }
-        }
-    }
-    return best;
-}
-
 template <int FMT, bool PK, bool QK, bool GATED, int BI, int WI, int WJ, int ST>
 static void product_launch_as(const ProductArgs& a, hipStream_t st) {
     const int JH = GATED ? a.J / 2 : a.J, BH = GATED ? 32 * WJ : 64 * WJ, tiles = (a.I + BI - 1) / BI * ((JH + BH - 1) / BH);
@@ -853,7 +810,7 @@ static void product_launch_as(const ProductArgs& a, hipStream_t st) {
 
 template <int FMT, bool PK, bool QK, bool GATED>
 static void product_launch(ProductArgs& a, hipStream_t st) {
-    switch (choose_tile(a, kStep<FMT>, FMT == kMx8 ? 1.35f : FMT == kF32 ? 2.9f : 1.0f)) {
+    switch (choose_tile(a.I, a.J, a.K, FMT, &a.splits)) {
         case 0: product_launch_as<FMT, PK, QK, GATED, 64, 4, 1, 4>(a, st); break;
         case 1: product_launch_as<FMT, PK, QK, GATED, 64, 2, 2, 3>(a, st); break;
         case 2: product_launch_as<FMT, PK, QK, GATED, 128, 2, 4, 3>(a, st); break;

@@ -202,16 +202,6 @@ static void few_launch(const ProductArgs& a, hipStream_t st) {
     }
 }
 
-// Each workgroup reads all tokens again for each of its 16 F rows of the weight, which up to 32 tokens hides behind the
-// weight's own bytes.  Beyond, tiles of 64 tokens win once they fill the CUs.  us, this kernel and the tiles, 64 tokens, bf16,
-// 4096 columns: 4096 rows 10.6, 14.0; 16384 rows 56, 37.  fp32 stays here (1024 x 1024: 9, 22: no terms, no parts).  A
-// block of 32 outputs in MXFP8 needs four fragments of rows, for which LDS has no room with more than 32 tokens.
-bool product_few_ok(const ProductArgs& a, int bytes) {
-    if (a.I <= kFewTokens) return true;
-    if (a.I > 64 || a.out_scales) return false;
-    return bytes == 4 || a.J <= 6144;
-}
-
 hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipStream_t st) {
     trace("product_few", 0, st);
     if (bytes == 2) {

@@ -16,8 +16,7 @@ typedef __attribute__((address_space(3))) uint8_t* pr_lds_t;
 constexpr int kStepBytes = 128;              // of a row and step: 64 bf16, 128 codes
 constexpr uint32_t kNowhere = 0x80000000u;   // past every descriptor's end: a load from there brings zeros
 
-// formats of the operands: values of a step, bytes of a value
-enum { kBf16 = 0, kF32 = 1, kMx8 = 2 };
+// values of a step, bytes of a value
 template <int FMT>
 constexpr int kStep = FMT == kBf16 ? 64 : FMT == kF32 ? 32 : 128;
 template <int FMT>
@@ -31,6 +30,9 @@ __device__ __forceinline__ pr_u32x4 load_rsrc(const uint8_t* base) {
     return pr_u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
 }
+// (m0 is reserved: the compiler sets it right before each use of its own, and warns of its name among what is overwritten)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint8_t* lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
                  "v"(off), "s"(load_rsrc(base)) : "memory", "m0");
@@ -39,6 +41,7 @@ __device__ __forceinline__ void load_lds4(const uint8_t* base, uint32_t off, uin
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"((uint32_t)(uintptr_t)(pr_lds_t)lds),
                  "v"(off), "s"(load_rsrc(base)) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Place of a row's 16-byte chunk in LDS: chunk ^ key(row).  Eight lanes, on eight rows, are served at once, from 32 banks.
 __device__ __forceinline__ int row_key(int r) { return r & 7; }
