@@ -260,3 +260,39 @@ def test_fp32_bits_below_bf16s_smallest(T, h8):
         m.moe_gated(d, x, None, T, w, None, None, h, None, scratch(d, T))
     as_they_are = T <= (32 if h8 else 64)
     assert ((h.double() - 3 * 2.0 ** -34).abs() <= (0 if as_they_are else 2.0 ** -34)).all()
+
+
+@pytest.mark.parametrize("T", [3, 70, 300])
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_gated_offsets_past_32_bits(act, T):
+    """The up projection's rows start past 4 GiB, and the gate's last rows too with fp32."""
+    K, last = 4096, 40
+    N = (1 << 32) // (K * 2) + 1032
+    g = gen(690)
+    w = torch.zeros(2 * N, K, dtype=act, device="cuda")
+    for end in (N, 2 * N):
+        w[end - last:end] = rand(g, last, K, dtype=act, std=0.1)
+    x = rand(g, T, K, dtype=act)
+    d, h = dense(N, K, act, "silu"), nan(T, N, dtype=act)
+    m.moe_gated(d, x, None, T, w, None, None, h, None, scratch(d, T))
+    assert (h[:, :-last] == 0).all()
+    rows = torch.cat([w[N - last:N], w[2 * N - last:]]).double()
+    check(h[:, -last:], ref.gated(x.double(), rows, "bf16" if act == BF16 else "f32", "silu")[1], act, "h")
+
+
+@pytest.mark.parametrize("T", [3, 70, 300])
+@pytest.mark.parametrize("K", [8192, 8224])
+def test_mxfp8_offsets_past_32_bits(K, T):
+    """Gated, more than 4 GiB of codes in either half, with the operands' own scales and with copied ones."""
+    last = 40
+    N = ((1 << 32) // K + 1032) // 8 * 8
+    g = gen(695)
+    w, ws = torch.zeros(2 * N, K, dtype=torch.uint8, device="cuda"), torch.full((2 * N, K // 32), 121, dtype=torch.uint8, device="cuda")
+    for end in (N, 2 * N):
+        w[end - last:end], ws[end - last:end] = mx8(g, last, K, std=0.1)
+    x, xs = mx8(g, T, K)
+    d, h = dense(N, K, BF16, "silu", True), nan(T, N, dtype=BF16)
+    m.moe_gated(d, x, xs, T, w, ws, None, h, None, scratch(d, T))
+    assert (h[:, :-last] == 0).all()
+    rows = torch.cat([ref.values(w[e - last:e], ws[e - last:e]) for e in (N, 2 * N)])
+    check(h[:, -last:], ref.gated(ref.values(x, xs), rows, "mx8", "silu")[1], BF16, "h")
