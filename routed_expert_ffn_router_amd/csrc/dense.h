@@ -180,7 +180,8 @@ hipError_t launch_product_few(const ProductArgs& a, int bytes, bool gated, hipSt
 // [J], to `padded`.
 hipError_t launch_pad_scales(const uint8_t* scales_p, int I, const uint8_t* scales_q, int J, int K, uint8_t* padded, hipStream_t st);
 
-// MXFP8 [n] as bf16, which holds every code times its scale
+// MXFP8 [n] as bf16, which holds every code times its scale but for the ends of the range: bits below 2^-133 are rounded off,
+// and 2^128 and more is infinite
 hipError_t launch_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, uint16_t* values, hipStream_t st);
 
 constexpr int kBiasChunks = 64;   // row chunks of the bias gradient's sums, at most

@@ -180,7 +180,7 @@ struct Steps {
         const int total = (a.K + kStep<FMT> - 1) / kStep<FMT>;
         first = 0;
         end = total;
-        if (a.splits > 1) {                                  // (K up to 2^20: 32 bits hold the products)
+        if (a.splits > 1) {                                  // (K up to 2^21, the gated block's rows: 32 bits hold the products)
             first = (int)((uint32_t)(blockIdx.y * total) / (uint32_t)a.splits);
             end = (int)((uint32_t)((blockIdx.y + 1) * total) / (uint32_t)a.splits);
         }

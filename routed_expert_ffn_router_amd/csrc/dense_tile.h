@@ -15,6 +15,9 @@ typedef __attribute__((address_space(3))) uint8_t* pr_lds_t;
 
 constexpr int kStepBytes = 128;              // of a row and step: 64 bf16, 128 codes
 constexpr uint32_t kNowhere = 0x80000000u;   // past every descriptor's end: a load from there brings zeros
+// A row is 2^23 bytes long at most (2^21 fp32 values of the gated block's gradient), and a tile's last row is its 256th: every
+// offset from a tile's first byte stays below the descriptors' 2^31 - 1 bytes.
+static_assert(255ull * (1 << 23) + kStepBytes < 0x7fffffffu, "offsets in a tile");
 
 // values of a step, bytes of a value
 template <int FMT>

@@ -296,3 +296,15 @@ def test_mxfp8_offsets_past_32_bits(K, T):
     assert (h[:, :-last] == 0).all()
     rows = torch.cat([ref.values(w[e - last:e], ws[e - last:e]) for e in (N, 2 * N)])
     check(h[:, -last:], ref.gated(ref.values(x, xs), rows, "mx8", "silu")[1], BF16, "h")
+
+
+def test_the_most_rows():
+    """The gated block's gradient over 2^20 rows of h: sums over 2^21 values, rows of 2^23 bytes."""
+    T, N, K = 70, 1 << 20, 8
+    g = gen(698)
+    d = dense(N, K, F32, "sigmoid")
+    w, dh, pre = rand(g, 2 * N, K, std=0.1), rand(g, T, N), rand(g, T, 2 * N)
+    dx = nan(T, K)
+    m.moe_gated_backward(d, None, T, w, pre, dh, dx, None, scratch(d, T))
+    grad = ref.gated_grad(dh, pre, "sigmoid")
+    check(dx, ref.product(grad.v, w.double().t(), "f32", grad.e), F32, "dx")
