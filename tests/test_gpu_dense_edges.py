@@ -308,3 +308,24 @@ def test_the_most_rows():
     m.moe_gated_backward(d, None, T, w, pre, dh, dx, None, scratch(d, T))
     grad = ref.gated_grad(dh, pre, "sigmoid")
     check(dx, ref.product(grad.v, w.double().t(), "f32", grad.e), F32, "dx")
+
+
+@pytest.mark.parametrize("act", [BF16, F32])
+def test_outputs_past_32_bits(act):
+    """More than 4 GiB of y, residual and pre: rows from the ends and the middle, the residual in y's place."""
+    T, N, K = 65536, 36872, 8
+    g = gen(699)
+    x, w, d = rand(g, T, K, dtype=act), rand(g, N, K, dtype=act), dense(N, K, act, "silu")
+    y, pre = torch.empty(T, N, dtype=act, device="cuda"), torch.empty(T, N, dtype=act, device="cuda")
+    for t in range(0, T, 8192):
+        y[t:t + 8192] = torch.randn(8192, 1, generator=g, device="cuda")
+    rows = torch.tensor([0, 1, 29119, 29120, 32768, 58255, T - 2, T - 1], device="cuda")
+    residual = y[rows].clone()
+    m.moe_matmul(d, x, None, T, w, None, None, y, pre, y, scratch(d, T))
+    v, want = ref.matmul(x[rows].double(), w.double(), "bf16" if act == BF16 else "f32", "silu", None, residual)
+    check(pre[rows], v, act, "pre")
+    check(y[rows], want, act, "y")
+    dx = nan(T, K, dtype=act)
+    m.moe_matmul_backward(d, None, T, w, pre, y, dx, None, None, scratch(d, T))
+    grad = ref.matmul_grad(y[rows], pre[rows], "silu")
+    check(dx[rows], ref.backward(grad, x[rows].double(), w.double(), "bf16" if act == BF16 else "f32")[0], act, "dx")
