@@ -330,10 +330,10 @@ __device__ __forceinline__ void multiply_mx8(pr_f32x4 (&acc)[4], const pr_i32x8&
 
 // Tile of BI rows and 64 WJ columns; WI x WJ waves, each BI / WI rows by 64 columns.  ST stages.
 // Small tiles fill the CUs, two workgroups on one covering each other's waits; what bounds them is a step's chain of
-// barrier, LDS reads and products.  bf16, 4096 x 4096: 256 tokens 19.3 us and 4.2 of k_product_finish, 1024 tokens 40.7
-// (845 TFLOP/s).  fp32, 333 tokens, 6144 x 2048: 71.7 us and 6.7 (matrix cores 46% busy where there is a workgroup: the
-// terms' vector instructions, five for each product, take the other half).  MXFP8 gated, 64 tokens, 8192 x 4096: 15.8
-// us, 69 MB of weights at 4.4 TB/s.
+// barrier, LDS reads and products.  bf16, 4096 x 4096: 256 tokens 20.0 us and 4.2 of k_product_finish, 1024 tokens 42.2
+// (814 TFLOP/s).  fp32, 333 tokens, 6144 x 2048: 71.5 us and 6.6 (matrix cores 46% busy where there is a workgroup: the
+// terms' vector instructions, five for each product, take the other half).  MXFP8 gated, 64 tokens, 8192 x 4096: 14.7
+// us a call where the last-level cache holds the weight (69 MB, 4.7 TB/s), 20 and more where it comes from HBM.
 template <int FMT, bool PK, bool QK, int BI, int WI, int WJ, int ST, bool GATED>
 __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
     constexpr int W = WI * WJ, BJ = 64 * WJ, FI = BI / WI / 16, BH = GATED ? BJ / 2 : BJ;
@@ -668,8 +668,9 @@ __global__ __launch_bounds__(256, 1) void k_product_large(ProductArgs a) {
 // at its end, by when h + 2 has landed: a load has two to three half steps for that.  Scales are loaded for four steps
 // at a time: each load of them touches a line for every row, and step by step the lines' way through L2 took as long as
 // the operands' (8192^3 600 us so, 534 now).
-// 4096 x 4096 x 8192 135 us (2032 TFLOP/s; two whole steps in LDS, whose loads have half a step to land, 145), 8192^3 534
-// (2060): the matrix cores are busy about half of it, and the scales' lines, one for each row, are the likely rest.
+// 4096 x 4096 x 8192 136 us (2020 TFLOP/s; two whole steps in LDS, whose loads have half a step to land, 145), 8192^3 517
+// (2130): counters show the matrix cores busy for 46% of either's cycles, and 4.5 vector instructions for each matrix one; the
+// scales' lines, one for each row, are the likely rest.  Rows that end inside a line cost more than that: 4096 x 8224 180 us.
 template <bool GATED>
 __global__ __launch_bounds__(256, 1) void k_product_large_mx8(ProductArgs a) {
     constexpr int B = 256, BH = GATED ? B / 2 : B, TB = B * kHalfBytes, STG = 2 * TB, SAT = 4 * STG, SB = 8 * B;
@@ -860,7 +861,7 @@ hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor
     return hipGetLastError();
 }
 
-// Four bytes of a row per thread.  Direct loads to LDS take whole aligned words, which rows of K/32 bytes are not made of unless
+// Four bytes of a row per thread, 3.3 us for a token and 4096 rows of 129 bytes.  Direct loads to LDS take whole aligned words, which rows of K/32 bytes are not made of unless
 // K is a multiple of 128.  2.5 us of a call: 4096 x 4128, one token 10.4 us, 4096 x 4096 7.8.
 __global__ __launch_bounds__(256) void k_pad_scales(const uint8_t* __restrict__ scales_p, const uint8_t* __restrict__ scales_q, int I, int J,
                                                     int blocks, uint32_t* __restrict__ padded) {
@@ -919,7 +920,8 @@ hipError_t launch_unpack(const uint8_t* codes, const uint8_t* scales, size_t n, 
 // rounding (the bias's gradient: row chunks apart, then added in order).  A workgroup takes 256 columns, 32 threads
 // of eight, and every eighth row of its chunk per thread row.  A stream: gated, 4096 x 8192, bf16, 336 MB in 59 us (5.7
 // TB/s); fp32, 777 x 1536, 8.3 us.  Formed inside the products instead, it would be computed again for every tile that
-// reads it, 16 and 64 times here.
+// reads it, 16 and 64 times here.  With a bias's gradient, 4096 x 4096, bf16, GELU: 31 us (100 MB at 3.2 TB/s, in 1024
+// workgroups of serial sums), and 20 for the 64 chunks' sums, sixteen workgroups that wait for one load after another.
 // ---------------------------------------------------------------------------------------------
 template <typename XT, bool GATED>
 __global__ __launch_bounds__(256) void k_pre_grad(PreGradArgs a) {

@@ -11,7 +11,8 @@
 // codes times their scale are exact in bf16 (but for the ends of its range), in four products.
 //
 // bf16, 4096 x 4096, one token 8.1 us (33.6 MB at 4.1 TB/s; 2 us of it are the launch and the first step's way), gated 8192 x
-// 4096 26.9 us (134 MB at 5.0 TB/s); fp32 4096 x 4096 12.8 us (5.2 TB/s); 64 tokens, bf16, 4096 x 4096 10.5 us.
+// 4096 26.9 us (134 MB at 5.0 TB/s); fp32 4096 x 4096 12.8 us (5.2 TB/s); 64 tokens, bf16, 4096 x 4096 10.5 us; MXFP8,
+// 4096 x 4096, one token 7.6 us (17.3 MB).
 #include "dense_tile.h"
 
 namespace moe {

@@ -32,7 +32,9 @@ inline size_t part_bytes(size_t I, size_t J) {
 // `start` and `step` for each 128 bytes of k, `step2` where two share a CU; parts cost a second kernel, that adds them.
 // us, model and measured (bf16): 256 tokens, 4096 x 4096 64 x 128 in two parts 21, 21.6 (128 x 256 26); 1024 tokens 64 x 128
 // 42, 42.0 (128 x 256 48); 2048 tokens 128 x 256 64, 64.1 (64 x 128 80); 4096 tokens 256 x 256 106, 110 (128 x 256 125);
-// 512 tokens, 1024 x 1024 64 x 64 9.4, 9.3 (64 x 128 9.8).  Steps of fp32 and MXFP8 are taken to be longer by one factor each.
+// 512 tokens, 1024 x 1024 64 x 64 9.4, 9.3 (64 x 128 9.8).  Steps of fp32 and MXFP8 are taken to be longer by one factor each:
+// fp32, 333 tokens, 6144 x 2048 128 x 256 in three parts 70, 72; MXFP8, 256 tokens, 4096 x 4096 64 x 64 16.2, 16.1 (kernel),
+// 4096 tokens, 4096 x 8192 256 x 256 140, 136.
 struct TileChoice {
     int bi, bj, per_cu;
     float start, step, step2;

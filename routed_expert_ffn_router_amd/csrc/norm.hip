@@ -78,7 +78,7 @@ __device__ __forceinline__ f32x8 combine8(const NormArgs& a, int t, int c) {
 // (185 MB at 4.2 TB/s: two rows at a time on a CU do not cover each other's sums); kept 1, 8, 7, .. 2 in turn
 // 46, since workgroups go to the eight XCDs in turn.
 // MX8: the normed row goes out as MXFP8, a block of 32 columns in four neighbouring lanes.  4096 rows of 4096, bf16, gate
-// per element, 30.7 us (151 MB at 4.9 TB/s); one row 7.1, the call's host time.
+// per element, 30.7 us (151 MB at 4.9 TB/s), fp32 51 (286 MB at 5.6 TB/s); one row 7.1, the call's host time.
 template <typename XT, int VPT, int COMBINE, bool LATE, bool NT, bool MX8 = false>
 __global__ __launch_bounds__(1024) void k_block_norm(NormArgs a) {
     __shared__ float s_post[16], s_pre[16];
