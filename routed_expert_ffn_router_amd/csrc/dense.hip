@@ -435,7 +435,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a) {
     if constexpr (FMT == kF32) {
         // A value without finite terms (an infinity, or one that bf16 rounds to it) leaves every sum that it enters infinite or
         // NaN, and so does a sum past the type's end: then the tile's sums are taken again, of the values themselves.  (To look at
-        // the sums takes 0.2 us at 128 tokens, 1024 x 1024, and 3 of 601 at 4096^3.)
+        // the sums takes 0.2 us at 128 tokens, 1024 x 1024, and 3 of 601 at 4096^3; an infinity in every tile doubles a call's time.)
         float none = 0.0f;
 #pragma unroll
         for (int fi = 0; fi < FI; ++fi)

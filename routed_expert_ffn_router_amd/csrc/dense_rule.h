@@ -41,7 +41,7 @@ struct TileChoice {
 };
 static const TileChoice kTiles[] = {
     {64, 64, 2, 5.4f, 0.25f, 0.42f}, {64, 128, 2, 5.7f, 0.32f, 0.57f}, {128, 256, 1, 5.2f, 0.92f, 0.92f}, {256, 256, 1, 6.2f, 1.55f, 1.55f}};
-static const struct {
+static constexpr struct {
     int step;                     // values of 128 bytes
     float slower;
 } kFormats[] = {{64, 1.0f}, {32, 2.9f}, {128, 1.35f}};

@@ -24,6 +24,8 @@ template <int FMT>
 constexpr int kStep = FMT == kBf16 ? 64 : FMT == kF32 ? 32 : 128;
 template <int FMT>
 constexpr int kSize = kStepBytes / kStep<FMT>;
+static_assert(kStep<kBf16> == kFormats[kBf16].step && kStep<kF32> == kFormats[kF32].step && kStep<kMx8> == kFormats[kMx8].step,
+              "the rule counts the kernels' steps");
 
 // Direct loads to LDS: 16 (4) bytes per lane from base + off, lane l's to lds + 16 l (4 l); an offset past the descriptor's
 // end brings zeros.  In assembly, because the compiler has every transposing read of LDS wait for all direct loads that
