@@ -422,8 +422,8 @@ moe_status moe_linear(const moe_matrix *matrix, const uint8_t *q, const uint8_t 
  *   operands MOE_OPERANDS_ACT: x and the weight in act_dtype.  bf16 values enter the products as they are, and so do
  *     fp32 values in the forward products of up to 64 tokens (h in MXFP8: up to 32).  Beyond and in the gradients, fp32
  *     values enter as three bf16 terms each, of which the six largest products are summed (what is left out is below 2^-24
- *     of |x| |W|), and bits below 2^-133 are left out.  Values without finite terms (infinities, 0x1.ffp127 and more) enter as they are again:
- *     a sum is infinite, NaN or finite as fp32 arithmetic has it.
+ *     of |x| |W|), and bits below 2^-133 are left out.  Where values have no finite terms (infinities, 0x1.ffp127 and
+ *     more) they enter as they are again: a sum is infinite, NaN or finite as fp32 arithmetic has it.
  *   operands MOE_OPERANDS_MXFP8: x and the weight as E4M3FN codes with a scale byte for each 32 consecutive columns
  *     (moe_block_norm_mx8 writes both), x_scales [T][cols/32] and w_scales [weight rows][cols/32]; forward only.
  *     With fp32 outputs, or few tokens (all up to 32, some calls up to 64), the values enter bf16 products, whose sums

@@ -796,7 +796,7 @@ moe_status moe_matmul(const moe_dense* m, const void* x, const uint8_t* x_scales
     if (!y || !ws || !all_aligned({bias, residual, pre, y}, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID;
     const DenseLayout L = dense_layout(m, T, m->rows, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    const size_t R = m->rows, rows = T * R * act_bytes(m), x_bytes = (size_t)T * m->cols * operand_bytes(m), w_bytes = R * m->cols * operand_bytes(m);
+    const size_t R = m->rows, rows = T * R * act_bytes(m), row = m->cols * operand_bytes(m), x_bytes = T * row, w_bytes = R * row;
     const Span kept = {residual == y ? nullptr : residual, rows};
     if (!apart({{y, rows}, {pre, rows}, {ws, L.total}}, {{x, x_bytes}, {x_scales, x_bytes / 32}, {w, w_bytes}, {w_scales, w_bytes / 32},
                                                          {bias, 4 * R}, kept})) return MOE_ERR_INVALID;
@@ -818,7 +818,7 @@ moe_status moe_gated(const moe_dense* m, const void* x, const uint8_t* x_scales,
     const size_t R = 2 * (size_t)m->rows;
     const DenseLayout L = dense_layout(m, T, R, false);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-    const size_t n = (size_t)T * m->rows, x_bytes = (size_t)T * m->cols * operand_bytes(m), w_bytes = R * m->cols * operand_bytes(m);
+    const size_t n = (size_t)T * m->rows, row = m->cols * operand_bytes(m), x_bytes = T * row, w_bytes = R * row;
     if (!apart({{h, h_scales ? n : n * act_bytes(m)}, {h_scales, n / 32}, {pre, 2 * n * act_bytes(m)}, {ws, L.total}},
                {{x, x_bytes}, {x_scales, x_bytes / 32}, {w, w_bytes}, {w_scales, w_bytes / 32}})) return MOE_ERR_INVALID;
     ProductArgs a = product_args(m, T, (int)R, m->cols, h);
@@ -838,7 +838,8 @@ static moe_status dense_backward(const moe_dense* m, const void* x, int32_t T, c
     const DenseLayout L = dense_layout(m, T, R, true);
     // dw and d_bias are written whatever T is, the workspace with any tokens
     if (!all_aligned({dw, d_bias}, 16)) return MOE_ERR_INVALID;
-    if (!apart({{dx, x_bytes}, {dw, w_bytes}, {d_bias, 4 * (size_t)m->rows}, {T > 0 ? ws : nullptr, L.total}},
+    if (!apart({{dx, x_bytes}, {dw, w_bytes}, {d_bias, 4 * (size_t)m->rows},
+                {T > 0 ? ws : nullptr, ws_bytes < L.total ? ws_bytes : L.total}},
                {{x, x_bytes}, {w, w_bytes}, {pre, T * es * R}, {dy, T * es * m->rows}})) return MOE_ERR_INVALID;
     if (T == 0) {
         if (dw) MOE_HIP(launch_ws_init((uint32_t*)dw, R * m->cols * (f32 ? 4 : 2) / 4, 0, stream));

@@ -861,8 +861,9 @@ hipError_t launch_product(ProductArgs a, int bytes, bool p_kmajor, bool q_kmajor
     return hipGetLastError();
 }
 
-// Four bytes of a row per thread, 3.3 us for a token and 4096 rows of 129 bytes.  Direct loads to LDS take whole aligned words, which rows of K/32 bytes are not made of unless
-// K is a multiple of 128.  2.5 us of a call: 4096 x 4128, one token 10.4 us, 4096 x 4096 7.8.
+// Four bytes of a row per thread, 3.3 us for a token and 4096 rows of 129 bytes.  Direct loads to LDS take whole aligned
+// words, which rows of K/32 bytes are not made of unless K is a multiple of 128.  2.5 us of a call: 4096 x 4128, one token
+// 10.3 us, 4096 x 4096 7.6.
 __global__ __launch_bounds__(256) void k_pad_scales(const uint8_t* __restrict__ scales_p, const uint8_t* __restrict__ scales_q, int I, int J,
                                                     int blocks, uint32_t* __restrict__ padded) {
     const int words = (blocks + 3) / 4;

@@ -97,3 +97,9 @@ def test_a_forked_child_asks_torch_for_the_gpu_again():
         assert m._torch_c is not None
     finally:
         m._torch_c = kept
+
+
+def test_a_workspace_that_is_too_small_is_named_as_that():
+    """... where its end meets the next array, too."""
+    for f in (matmul, gated, matmul_backward, gated_backward):
+        assert f(s=P - 256, n=256) == WSP, f.__name__
